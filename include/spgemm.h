@@ -352,6 +352,130 @@ int spgemm_mcl_prune_numeric(const spgemm_csr* C, double threshold, const double
 int spgemm_symbolic_noalloc(int64_t m, int64_t k, int64_t n, const spgemm_csr* A,
                             const spgemm_csr* B, int64_t* c_row_ptr, int64_t* c_nnz, void* stream);
 
+/* ---- products of rows with the matrix of their group ------------------------------------
+ * A sparse choice sends every row of a dense matrix to one or a few of `groups` matrices: the
+ * experts of a mixture-of-experts layer (chosen by a router) or the low-rank adapters of the
+ * requests in a batch.  The choice is a sparse matrix with top_k entries per row: ids (tokens x
+ * top_k, ascending, -1 = no choice) with one 32-bit weight each.  Slot s = token * top_k + j.
+ * Its transpose is the grouping: the slots in order of their group, slots of one group in
+ * ascending order.  All calls below enqueue on `stream` and return without synchronising; they
+ * take scratch from the library's stream-ordered pool, so calls on several streams never share
+ * any.  Results do not depend on the order in which blocks run.  A check that fails on the
+ * device (an id out of range, an expired wait) sets a word that spgemm_grouped_status reads;
+ * nothing is read or written out of bounds for it. */
+#define SPGEMM_DTYPE_F32 0
+#define SPGEMM_DTYPE_BF16 1
+#define SPGEMM_DTYPE_F16 2
+
+/* A dense row-major matrix in device memory: element (i, j) at data[i * stride + j]. */
+typedef struct {
+  void* data;
+  int64_t rows, cols, stride; /* stride >= cols, in elements */
+  int32_t dtype;              /* SPGEMM_DTYPE_* */
+  int32_t reserved;
+} spgemm_dense;
+
+/* One matrix per group: element (g, i, j) at data[g * group_stride + i * row_stride + j]. */
+typedef struct {
+  void* data;
+  int64_t groups, rows, cols;
+  int64_t group_stride, row_stride; /* in elements */
+  int32_t dtype;
+  int32_t reserved;
+} spgemm_weights;
+
+/* The transposed choice, in device memory. */
+typedef struct {
+  int64_t slots;           /* tokens * top_k */
+  int32_t top_k;
+  int32_t groups;
+  const int32_t* offsets;  /* groups + 1: positions [offsets[g], offsets[g+1]) are group g's */
+  const int32_t* order;    /* slots: the slot at each position; -1 from offsets[groups] on */
+  const int32_t* position; /* slots: the position of each slot; -1 for a slot without a group */
+} spgemm_grouping;
+
+#define SPGEMM_SCORE_SOFTMAX 0
+#define SPGEMM_SCORE_SIGMOID 1
+#define SPGEMM_GROUP_MAX 0   /* an expert group counts as its best expert */
+#define SPGEMM_GROUP_TOP2 1  /* an expert group counts as the sum of its two best experts */
+
+/* How a router chooses.  Scores are computed in 32 bits from the logits; a NaN logit counts as
+ * -inf, +inf as the largest finite value.  An expert whose logit is -inf is never chosen.  The
+ * choice compares score + bias where there is a bias, else the logits themselves; the experts
+ * form `groups` runs of equal length, of which the groups_kept best take part.  Ties go to the
+ * lowest index.  Weights are the scores (without the bias), divided by their sum over the chosen
+ * experts when `renormalise` is set (0 where that sum is 0), times `scale`. */
+typedef struct {
+  int32_t top_k;       /* 1 .. min(experts, 32) */
+  int32_t score;       /* SPGEMM_SCORE_* */
+  int32_t groups;      /* 1 .. 32, divides the number of experts */
+  int32_t groups_kept; /* 1 .. groups */
+  int32_t group_score; /* SPGEMM_GROUP_* */
+  int32_t renormalise;
+  float scale;
+  int32_t reserved;
+} spgemm_route_rule;
+
+/* Routing: logits (tokens x experts, at most 1024 experts) and bias (experts 32-bit values, or
+ * NULL) to ids and weights (tokens x top_k), and the grouping's three arrays.  Tokens that can
+ * choose fewer than top_k experts (none, when every logit is -inf) end in ids -1 with weight 0.
+ * Errors: INVALID_ARG (null pointers, rule out of range), OVERFLOW (tokens * top_k >= 2^31 -
+ * 2^20), OUT_OF_MEMORY, CUDA. */
+int spgemm_route(const spgemm_dense* logits, const spgemm_route_rule* rule, const float* bias, int32_t* ids,
+                 float* weights, int32_t* offsets, int32_t* order, int32_t* position, void* stream);
+
+/* Gradient of the logits (same shape and type as logits, every element written) for a gradient
+ * of the weights (tokens x top_k, 32-bit).  The choice itself and the bias have no gradient. */
+int spgemm_route_backward(const spgemm_dense* logits, const spgemm_route_rule* rule, const int32_t* ids,
+                          const float* grad_weights, const spgemm_dense* grad_logits, void* stream);
+
+/* The grouping of given ids (`slots` of them, -1 = none; other values outside [0, groups) count
+ * as -1 and set the status word). */
+int spgemm_group_rows(const int32_t* ids, int64_t slots, int32_t groups, int32_t* offsets, int32_t* order,
+                      int32_t* position, void* stream);
+
+/* y[p, :] = row(p) * w[g]^T for every position p of every group g.  x has one row per token
+ * (row(p) = x[order[p] / top_k]) or, when x_grouped, one row per position (row(p) = x[p]); w[g] is
+ * y.cols x x.cols.  Rows of y from offsets[groups] on are set to zero.  y may be 32-bit (sums are
+ * held in 32 bits in any case).  All types equal otherwise; 16-bit types whose rows start on 16-byte
+ * boundaries run on the tensor cores, anything else on the CUDA cores. */
+int spgemm_grouped_product(const spgemm_grouping* g, const spgemm_dense* x, int32_t x_grouped,
+                           const spgemm_weights* w, const spgemm_dense* y, void* stream);
+
+/* Gradients of spgemm_grouped_product with one row of x per token: dx[t, :] = sum over the
+ * token's slots of dy[position, :] * w[g], dw[g] = sum over the group's positions of dy[p, :]^T
+ * x[row(p), :] (zero for an empty group).  dx or dw may be NULL. */
+int spgemm_grouped_product_backward(const spgemm_grouping* g, const spgemm_dense* dy, const spgemm_dense* x,
+                                    const spgemm_weights* w, const spgemm_dense* dx, const spgemm_weights* dw,
+                                    void* stream);
+
+/* out[t, :] = sum over the token's slots, in order, of weights[slot] * y[position[slot], :];
+ * weights NULL: ones.  out and y may differ in type. */
+int spgemm_combine(const spgemm_grouping* g, const float* weights, const spgemm_dense* y, const spgemm_dense* out,
+                   void* stream);
+
+/* Gradients of spgemm_combine: dy[p, :] = weights[slot] * dout[t, :] (zero from offsets[groups]
+ * on), dweights[slot] = <dout[t, :], y[p, :]> (zero for a slot without a group). */
+int spgemm_combine_backward(const spgemm_grouping* g, const float* weights, const spgemm_dense* dout,
+                            const spgemm_dense* y, const spgemm_dense* dy, float* dweights, void* stream);
+
+/* A gated expert layer: out[t, :] = sum over the token's slots of weights[slot] * h(slot) *
+ * w_down[g]^T with h = silu(x[t] * gate[g]^T) * (x[t] * up[g]^T); w_up[g] holds the gate's hidden
+ * rows, then up's.  The hidden row of a slot is held in x's type, everything else in 32 bits. */
+int spgemm_experts(const spgemm_grouping* g, const float* weights, const spgemm_dense* x,
+                   const spgemm_weights* w_up, const spgemm_weights* w_down, const spgemm_dense* out, void* stream);
+
+/* A projection with a low-rank adapter per row: y[t, :] = x[t] * w^T + scale[i] * (x[t] * a[i]^T) *
+ * b[i]^T with i = ids[t]; -1: the projection alone.  a: adapters x rank x x.cols, b: adapters x
+ * y.cols x rank, scale: one 32-bit factor per adapter, or NULL for ones. */
+int spgemm_adapted_product(const spgemm_dense* x, const spgemm_dense* w, const spgemm_weights* a,
+                           const spgemm_weights* b, const int32_t* ids, const float* scale, const spgemm_dense* y,
+                           void* stream);
+
+/* Synchronises `stream`, then reads and clears the device's status word of the calls above:
+ * SPGEMM_OK, or SPGEMM_ERR_DEVICE when a device-side check failed since the last call. */
+int spgemm_grouped_status(void* stream);
+
 const char* spgemm_strerror(int code);
 /* Detail of the last failure on the calling host thread ("" if none). */
 const char* spgemm_last_error(void);

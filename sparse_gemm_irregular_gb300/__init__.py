@@ -15,6 +15,8 @@ from .binding import (SpgemmError, load, options, spgemm_create, spgemm_destroy,
                       spgemm_get_plan, spgemm_get_stats, spgemm_kernel_launches, spgemm_last_error, spgemm_numeric,
                       spgemm_numeric_rows, spgemm_plan_params, spgemm_release_memory, spgemm_row_windows,
                       spgemm_strerror, spgemm_symbolic)
+from .grouped import (Routing, adapted_product, combine, combine_backward, expert_product, expert_product_backward,
+                      experts, group_rows, grouped_status, route, route_backward)
 
 __all__ = [
     "DeviceCSR", "multiply", "Product", "SpgemmError", "load", "options", "spgemm_create",
@@ -24,6 +26,8 @@ __all__ = [
     "spgemm_last_error", "spgemm_numeric", "spgemm_numeric_rows", "spgemm_plan_params",
     "spgemm_release_memory", "spgemm_row_windows",
     "spgemm_strerror", "spgemm_symbolic",
+    "Routing", "route", "route_backward", "group_rows", "expert_product", "expert_product_backward", "combine",
+    "combine_backward", "experts", "adapted_product", "grouped_status",
 ]
 
 

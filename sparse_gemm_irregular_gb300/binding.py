@@ -77,6 +77,25 @@ class spgemm_stats(ctypes.Structure):
                 ("gen_symbolic", _i32)]
 
 
+class spgemm_dense(ctypes.Structure):
+    _fields_ = [("data", _vp), ("rows", _i64), ("cols", _i64), ("stride", _i64), ("dtype", _i32), ("reserved", _i32)]
+
+
+class spgemm_weights(ctypes.Structure):
+    _fields_ = [("data", _vp), ("groups", _i64), ("rows", _i64), ("cols", _i64), ("group_stride", _i64),
+                ("row_stride", _i64), ("dtype", _i32), ("reserved", _i32)]
+
+
+class spgemm_grouping(ctypes.Structure):
+    _fields_ = [("slots", _i64), ("top_k", _i32), ("groups", _i32), ("offsets", _vp), ("order", _vp),
+                ("position", _vp)]
+
+
+class spgemm_route_rule(ctypes.Structure):
+    _fields_ = [("top_k", _i32), ("score", _i32), ("groups", _i32), ("groups_kept", _i32), ("group_score", _i32),
+                ("renormalise", _i32), ("scale", ctypes.c_float), ("reserved", _i32)]
+
+
 EXPORTS = {
     "spgemm_plan_params": (ctypes.c_int, [_i64, _i64, _vp, _vp]),
     "spgemm_create": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
@@ -94,6 +113,16 @@ EXPORTS = {
     "spgemm_hll_estimate": (ctypes.c_int, [_vp, _vp, _i32, ctypes.c_double, _vp, _vp]),
     "spgemm_mcl_prune_symbolic": (ctypes.c_int, [_vp, ctypes.c_double, _vp, _vp, _vp, _vp]),
     "spgemm_mcl_prune_numeric": (ctypes.c_int, [_vp, ctypes.c_double, _vp, _vp, _vp, _vp, _vp]),
+    "spgemm_route": (ctypes.c_int, [_vp] * 9),
+    "spgemm_route_backward": (ctypes.c_int, [_vp] * 6),
+    "spgemm_group_rows": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "spgemm_grouped_product": (ctypes.c_int, [_vp, _vp, _i32, _vp, _vp, _vp]),
+    "spgemm_grouped_product_backward": (ctypes.c_int, [_vp] * 7),
+    "spgemm_combine": (ctypes.c_int, [_vp] * 5),
+    "spgemm_combine_backward": (ctypes.c_int, [_vp] * 7),
+    "spgemm_experts": (ctypes.c_int, [_vp] * 7),
+    "spgemm_adapted_product": (ctypes.c_int, [_vp] * 8),
+    "spgemm_grouped_status": (ctypes.c_int, [_vp]),
     "spgemm_release_memory": (ctypes.c_int, []),
     "spgemm_destroy": (ctypes.c_int, [_vp]),
     "spgemm_strerror": (ctypes.c_char_p, [ctypes.c_int]),
@@ -238,6 +267,10 @@ def spgemm_mcl_prune_numeric(C: spgemm_csr, threshold: float, col_sums: int, out
                              out_val: int, stream: int = 0):
     _check(load().spgemm_mcl_prune_numeric(ctypes.byref(C), threshold, _vp(col_sums), _vp(out_row_ptr),
                                            _vp(out_col), _vp(out_val), _vp(stream)), "spgemm_mcl_prune_numeric")
+
+
+def spgemm_grouped_status(stream: int = 0):
+    _check(load().spgemm_grouped_status(_vp(stream)), "spgemm_grouped_status")
 
 
 def spgemm_destroy(h):

@@ -1,0 +1,275 @@
+"""Routing, expert products and per-request adapters: rows of a dense matrix multiplied by the
+matrix of the group that a sparse choice sends them to.
+
+The calls marshal PyTorch device tensors into the C entry points of include/spgemm.h
+(``spgemm_route`` and those after it) and allocate the outputs; they enqueue on the given or the
+current stream and do not synchronise.  ``Routing`` is the choice together with its transpose.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+from typing import Any
+
+from . import binding
+from .binding import _check, _vp, load, spgemm_dense, spgemm_grouping, spgemm_route_rule, spgemm_weights
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"max": 0, "top2": 1}
+
+
+@dataclass
+class Routing:
+    """The choice of every token and its transpose, in device memory.
+
+    ids (tokens, top_k) int32: chosen groups, ascending, -1 for none; weights (tokens, top_k)
+    float32; offsets (groups + 1) int32: positions of each group; order (slots) int32: the slot
+    (token * top_k + j) at each position, -1 behind the last group; position (tokens, top_k)
+    int32: the position of each slot, -1 for none.  ``rule`` holds the options of ``route``."""
+    ids: Any
+    weights: Any
+    offsets: Any
+    order: Any
+    position: Any
+    rule: Any = None
+
+    @property
+    def tokens(self) -> int:
+        return self.ids.shape[0]
+
+    @property
+    def top_k(self) -> int:
+        return self.ids.shape[1]
+
+    @property
+    def groups(self) -> int:
+        return self.offsets.numel() - 1
+
+    def to_csr(self):
+        """The choice as a DeviceCSR (tokens x groups, the weights in float64) for the library's
+        sparse products.  Copies the number of entries to the host."""
+        import torch
+        from . import DeviceCSR
+        there = self.ids >= 0
+        row_ptr = torch.zeros(self.tokens + 1, dtype=torch.int64, device=self.ids.device)
+        row_ptr[1:] = there.sum(1).cumsum(0)
+        return DeviceCSR(self.tokens, self.groups, row_ptr, self.ids[there].contiguous(),
+                         self.weights[there].double().contiguous())
+
+    def transposed_csr(self):
+        """The transposed choice as a DeviceCSR (groups x tokens)."""
+        import torch  # noqa: F401
+        from . import DeviceCSR
+        n = int(self.offsets[-1])
+        slot = self.order[:n].long()
+        return DeviceCSR(self.groups, self.tokens, self.offsets.long(), (slot // self.top_k).int(),
+                         self.weights.reshape(-1)[slot].double())
+
+    def _grouping(self) -> spgemm_grouping:
+        for t, name in ((self.ids, "ids"), (self.offsets, "offsets"), (self.order, "order"), (self.position, "position")):
+            _want(t, name, "int32")
+        _want(self.weights, "weights", "float32")
+        n = self.ids.numel()
+        if self.ids.dim() != 2 or self.position.numel() != n or self.order.numel() != n or self.weights.numel() != n:
+            raise ValueError("routing: ids, weights, order and position want tokens * top_k entries each")
+        return spgemm_grouping(n, self.ids.shape[1], self.groups, self.offsets.data_ptr(), self.order.data_ptr(),
+                               self.position.data_ptr())
+
+
+def _dtype(t, name: str) -> int:
+    import torch
+    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    if code is None:
+        raise TypeError("%s: float32, bfloat16 or float16 wanted, got %s" % (name, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s: a CUDA tensor is wanted" % name)
+    return code
+
+
+def _want(t, name: str, dtype: str):
+    if str(t.dtype) != "torch." + dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s: a contiguous CUDA tensor of %s is wanted" % (name, dtype))
+
+
+def _dense(t, name: str) -> spgemm_dense:
+    code = _dtype(t, name)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s: a matrix whose rows are contiguous is wanted" % name)
+    return spgemm_dense(t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]), code, 0)
+
+
+def _weights(t, name: str) -> spgemm_weights:
+    code = _dtype(t, name)
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError("%s: (groups, rows, columns) with contiguous rows is wanted" % name)
+    return spgemm_weights(t.data_ptr(), t.shape[0], t.shape[1], t.shape[2], t.stride(0), max(t.stride(1), t.shape[2]), code, 0)
+
+
+def _stream(stream, device):
+    import torch
+    return _vp((stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
+
+
+def _ref(s):
+    return ctypes.byref(s)
+
+
+def route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int = 1, groups_kept: int = 1,
+          group_score: str = "max", renormalise: bool = True, scale: float = 1.0, stream=None) -> Routing:
+    """Choose ``top_k`` experts per token from router logits (tokens, experts).
+
+    score: "softmax" or "sigmoid"; bias (experts) float32 takes part in the choice only; the
+    experts form ``groups`` equal runs of which the ``groups_kept`` best ("max": by their best
+    expert, "top2": by the sum of their two best) take part.  See spgemm_route."""
+    import torch
+    d = _dense(logits, "logits")
+    if score not in _SCORES or group_score not in _GROUP_SCORES:
+        raise ValueError("score: softmax or sigmoid; group_score: max or top2")
+    rule = spgemm_route_rule(top_k, _SCORES[score], groups, groups_kept, _GROUP_SCORES[group_score], bool(renormalise),
+                             scale, 0)
+    if bias is not None:
+        _want(bias, "bias", "float32")
+        if bias.numel() != logits.shape[1]:
+            raise ValueError("bias: one value per expert is wanted")
+    t, dev, k = logits.shape[0], logits.device, max(int(top_k), 1)
+    ids = torch.empty((t, k), dtype=torch.int32, device=dev)
+    weights = torch.empty((t, k), dtype=torch.float32, device=dev)
+    offsets = torch.empty(logits.shape[1] + 1, dtype=torch.int32, device=dev)
+    order = torch.empty(t * k, dtype=torch.int32, device=dev)
+    position = torch.empty((t, k), dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        _check(load().spgemm_route(_ref(d), _ref(rule), bias.data_ptr() if bias is not None else None, ids.data_ptr(),
+                                   weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
+                                   _stream(stream, dev)), "spgemm_route")
+    return Routing(ids, weights, offsets, order, position, rule)
+
+
+def route_backward(logits, routing: Routing, grad_weights, *, stream=None):
+    """Gradient of the logits for a gradient of ``routing.weights`` (see spgemm_route_backward)."""
+    import torch
+    if routing.rule is None:
+        raise ValueError("route_backward: the routing does not come from route()")
+    d = _dense(logits, "logits")
+    _want(routing.ids, "ids", "int32")
+    _want(grad_weights, "grad_weights", "float32")
+    if grad_weights.shape != routing.ids.shape or logits.shape[0] != routing.tokens:
+        raise ValueError("grad_weights: (tokens, top_k) is wanted")
+    out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    with torch.cuda.device(logits.device):
+        _check(load().spgemm_route_backward(_ref(d), _ref(routing.rule), routing.ids.data_ptr(),
+                                            grad_weights.data_ptr(), _ref(_dense(out, "grad_logits")),
+                                            _stream(stream, logits.device)), "spgemm_route_backward")
+    return out
+
+
+def group_rows(ids, groups: int, *, weights=None, stream=None) -> Routing:
+    """The Routing of given ids (tokens, top_k) or (tokens,) int32, -1 for none; weights default to
+    ones (see spgemm_group_rows)."""
+    import torch
+    _want(ids, "ids", "int32")
+    ids = ids if ids.dim() == 2 else ids[:, None]
+    dev = ids.device
+    offsets = torch.empty(groups + 1, dtype=torch.int32, device=dev)
+    order = torch.empty(ids.numel(), dtype=torch.int32, device=dev)
+    position = torch.empty_like(ids)
+    with torch.cuda.device(dev):
+        _check(load().spgemm_group_rows(ids.data_ptr(), ids.numel(), groups, offsets.data_ptr(), order.data_ptr(),
+                                        position.data_ptr(), _stream(stream, dev)), "spgemm_group_rows")
+    if weights is None:
+        weights = torch.ones(ids.shape, dtype=torch.float32, device=dev)
+    return Routing(ids, weights, offsets, order, position)
+
+
+def expert_product(x, w, routing: Routing, *, grouped: bool = False, out_dtype=None, stream=None):
+    """Rows times the matrix of their group: (slots, w.shape[1]) in group order.
+
+    x (tokens, d), or (slots, d) in group order with ``grouped``; w (groups, n, d).  See
+    spgemm_grouped_product."""
+    import torch
+    g = routing._grouping()
+    dx, dw = _dense(x, "x"), _weights(w, "w")
+    y = torch.empty((g.slots, w.shape[1]), dtype=out_dtype or x.dtype, device=x.device)
+    with torch.cuda.device(x.device):
+        _check(load().spgemm_grouped_product(_ref(g), _ref(dx), int(grouped), _ref(dw), _ref(_dense(y, "y")),
+                                             _stream(stream, x.device)), "spgemm_grouped_product")
+    return y
+
+
+def expert_product_backward(dy, x, w, routing: Routing, *, need_dx: bool = True, need_dw: bool = True, stream=None):
+    """(dx, dw) of ``expert_product`` with one row of x per token (see spgemm_grouped_product_backward)."""
+    import torch
+    g = routing._grouping()
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
+    dw = torch.empty(w.shape, dtype=w.dtype, device=x.device) if need_dw else None
+    with torch.cuda.device(x.device):
+        _check(load().spgemm_grouped_product_backward(
+            _ref(g), _ref(_dense(dy, "dy")), _ref(_dense(x, "x")), _ref(_weights(w, "w")),
+            _ref(_dense(dx, "dx")) if need_dx else None, _ref(_weights(dw, "dw")) if need_dw else None,
+            _stream(stream, x.device)), "spgemm_grouped_product_backward")
+    return dx, dw
+
+
+def combine(y, routing: Routing, *, out_dtype=None, stream=None):
+    """Weighted sum of a token's rows: (tokens, y.shape[1]) (see spgemm_combine)."""
+    import torch
+    g = routing._grouping()
+    out = torch.empty((routing.tokens, y.shape[1]), dtype=out_dtype or y.dtype, device=y.device)
+    with torch.cuda.device(y.device):
+        _check(load().spgemm_combine(_ref(g), routing.weights.data_ptr(), _ref(_dense(y, "y")),
+                                     _ref(_dense(out, "out")), _stream(stream, y.device)), "spgemm_combine")
+    return out
+
+
+def combine_backward(dout, y, routing: Routing, *, stream=None):
+    """(dy, dweights) of ``combine`` (see spgemm_combine_backward)."""
+    import torch
+    g = routing._grouping()
+    dy = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+    dweights = torch.empty(routing.ids.shape, dtype=torch.float32, device=y.device)
+    with torch.cuda.device(y.device):
+        _check(load().spgemm_combine_backward(_ref(g), routing.weights.data_ptr(), _ref(_dense(dout, "dout")),
+                                              _ref(_dense(y, "y")), _ref(_dense(dy, "dy")), dweights.data_ptr(),
+                                              _stream(stream, y.device)), "spgemm_combine_backward")
+    return dy, dweights
+
+
+def experts(x, w_up, w_down, routing: Routing, *, stream=None):
+    """A gated expert layer, (tokens, d) -> (tokens, w_down.shape[1]): w_up (groups, 2 * hidden, d)
+    holds the gate's rows, then up's; w_down (groups, n, hidden).  See spgemm_experts."""
+    import torch
+    g = routing._grouping()
+    out = torch.empty((x.shape[0], w_down.shape[1]), dtype=x.dtype, device=x.device)
+    with torch.cuda.device(x.device):
+        _check(load().spgemm_experts(_ref(g), routing.weights.data_ptr(), _ref(_dense(x, "x")),
+                                     _ref(_weights(w_up, "w_up")), _ref(_weights(w_down, "w_down")),
+                                     _ref(_dense(out, "out")), _stream(stream, x.device)), "spgemm_experts")
+    return out
+
+
+def adapted_product(x, w, a, b, ids, scale=None, *, stream=None):
+    """x w^T + scale[i] (x a[i]^T) b[i]^T with i = ids[token] (int32; -1: the projection alone).
+
+    x (tokens, d), w (n, d), a (adapters, rank, d), b (adapters, n, rank), scale (adapters)
+    float32.  See spgemm_adapted_product."""
+    import torch
+    _want(ids, "ids", "int32")
+    if ids.numel() != x.shape[0]:
+        raise ValueError("ids: one per row of x is wanted")
+    if scale is not None:
+        _want(scale, "scale", "float32")
+        if scale.numel() != a.shape[0]:
+            raise ValueError("scale: one value per adapter is wanted")
+    y = torch.empty((x.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
+    with torch.cuda.device(x.device):
+        _check(load().spgemm_adapted_product(_ref(_dense(x, "x")), _ref(_dense(w, "w")), _ref(_weights(a, "a")),
+                                             _ref(_weights(b, "b")), ids.data_ptr(),
+                                             scale.data_ptr() if scale is not None else None, _ref(_dense(y, "y")),
+                                             _stream(stream, x.device)), "spgemm_adapted_product")
+    return y
+
+
+def grouped_status(stream=None):
+    """Synchronise and raise SpgemmError if a device-side check of the calls above failed."""
+    import torch
+    s = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    binding.spgemm_grouped_status(s)

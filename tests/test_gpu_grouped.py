@@ -1,0 +1,482 @@
+"""Routing, expert products and adapters on the GPU against the formulas in 64 bits (numpy), at the
+sizes, masks, strides and types where they can go wrong.  Whole numbers have to be equal;
+floating results stay inside bounds derived from the arithmetic: half a spacing of the output type
+per rounding plus the rounding of the 32-bit sums over the absolute products."""
+import numpy as np
+import pytest
+
+from _grouped_ref import SUM, TINY, U, product, rounding, route, route_grad, scores, transpose
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+def _t(dtype):
+    import torch
+    return {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[dtype]
+
+
+def _gen(seed):
+    import torch
+    return torch.Generator().manual_seed(seed)
+
+
+def _normal(seed, *shape, dtype="bf16", std=1.0):
+    import torch
+    return (torch.randn(*shape, generator=_gen(seed)) * std).to(_t(dtype))
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _random_ids(seed, tokens, groups, top_k, empty=()):
+    """Ascending distinct ids per token, some slots and some tokens without a choice."""
+    rng = np.random.default_rng(seed)
+    allowed = [g for g in range(groups) if g not in empty]
+    ids = np.full((tokens, top_k), -1, np.int32)
+    for t in range(tokens):
+        n = top_k if rng.random() < 0.8 else rng.integers(0, top_k + 1)
+        n = min(n, len(allowed))
+        p = 1.0 / (1.0 + np.arange(len(allowed)))
+        ids[t, :n] = np.sort(rng.choice(allowed, n, replace=False, p=p / p.sum()))
+    return ids
+
+
+def _routing(gpu_lib, ids, groups, weights=None):
+    import torch
+    w = None if weights is None else torch.tensor(weights, dtype=torch.float32).cuda()
+    return gpu_lib.group_rows(torch.tensor(ids).cuda(), groups, weights=w)
+
+
+def _check_transpose(r, ids, groups):
+    offsets, order, position = transpose(ids, groups)
+    assert np.array_equal(r.offsets.cpu().numpy(), offsets)
+    assert np.array_equal(r.order.cpu().numpy(), order)
+    assert np.array_equal(r.position.cpu().numpy(), position)
+
+
+# ---- routing ---------------------------------------------------------------------------------
+def _grid_logits(seed, tokens, experts, dtype):
+    """Logits on a coarse grid (so that values are equal or well apart), with masked experts, a
+    fully masked row, a row of the type's lowest value, NaN and +inf."""
+    import torch
+    l = (torch.randint(-12, 13, (tokens, experts), generator=_gen(seed)) * 0.25).to(_t(dtype))
+    l[torch.rand(tokens, experts, generator=_gen(seed + 1)) < 0.1] = -INF
+    if tokens > 4:
+        l[1] = -INF
+        l[2] = torch.finfo(_t(dtype)).min
+        l[3, 0] = float("nan")
+        l[4, experts - 1] = INF
+        l[tokens - 1, 1:] = -INF
+    return l
+
+
+ROUTES = [
+    (1, 1, 1, dict()),
+    (1, 64, 6, dict()),
+    (7, 33, 5, dict(score="softmax", renormalise=False)),
+    (64, 8, 2, dict(score="sigmoid", scale=2.5)),
+    (65, 128, 8, dict(score="softmax", groups=8, groups_kept=3)),
+    (130, 96, 8, dict(score="sigmoid", groups=4, groups_kept=2)),
+    (67, 12, 12, dict(score="softmax")),
+    (66, 257, 32, dict(score="sigmoid", renormalise=False)),
+    (40, 1000, 8, dict(score="softmax", groups=10, groups_kept=1)),
+    (1500, 64, 6, dict(score="softmax")),
+]
+
+
+@pytest.mark.parametrize("tokens,experts,top_k,opt", ROUTES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_route_and_gradient(gpu_lib, tokens, experts, top_k, opt, dtype):
+    import torch
+    l = _grid_logits(tokens * experts, tokens, experts, dtype)
+    ids, weights, _ = route(l.double().numpy(), top_k, **opt)
+    r = gpu_lib.route(l.cuda(), top_k, **opt)
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+    # exp and the division are a few spacings off, the sum over `experts` terms one each
+    tol = (8 + experts) * 2.0 ** -23
+    assert np.allclose(_np(r.weights), weights, rtol=tol, atol=1e-37)
+    _check_transpose(r, ids, experts)
+    g = torch.randn(tokens, top_k, generator=_gen(5))
+    d = gpu_lib.route_backward(l.cuda(), r, g.cuda())
+    o = dict(score="softmax", renormalise=True, scale=1.0) | {k: v for k, v in opt.items() if k in ("score", "renormalise", "scale")}
+    want = route_grad(l.double().numpy(), ids, g.numpy(), **o)
+    _, s = scores(l.double().numpy(), o["score"])
+    # size of the terms that are subtracted from each other: |g| (and |g| / sum) times s
+    total = np.array([max(s[t, ids[t][ids[t] >= 0]].sum(), 1e-30) for t in range(tokens)])[:, None]
+    size = o["scale"] * np.abs(g.numpy()).max() * top_k * (1 / total if o["renormalise"] else 1.0) * s * 2
+    assert np.all(np.abs(_np(d) - want) <= rounding(dtype, want) + 4 * tol * size)
+    gpu_lib.grouped_status()
+
+
+@pytest.mark.parametrize("tokens,experts,top_k,opt", [
+    (50, 64, 6, dict(score="sigmoid", groups=8, groups_kept=4, group_score="top2")),
+    (33, 32, 4, dict(score="sigmoid")),
+    (21, 40, 3, dict(score="softmax", groups=20, groups_kept=7, group_score="top2")),
+    (20, 24, 4, dict(score="softmax", groups=3, groups_kept=2, group_score="max")),
+])
+def test_route_with_bias(gpu_lib, tokens, experts, top_k, opt):
+    import torch
+    for seed in range(6):
+        l = _grid_logits(seed + 70, tokens, experts, "f32")
+        bias = torch.randint(-60, 61, (experts,), generator=_gen(seed)) * 1e-3
+        ids, weights, gap = route(l.double().numpy(), top_k, bias=bias.double().numpy(), **opt)
+        if gap > 2e-6:  # compared values are equal or further apart than 32 bits can confuse
+            break
+    else:
+        pytest.fail("no seed keeps the compared values apart")
+    r = gpu_lib.route(l.cuda(), top_k, bias=bias.cuda(), **opt)
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+    assert np.allclose(_np(r.weights), weights, rtol=(8 + experts) * 2.0 ** -23, atol=1e-37)
+    _check_transpose(r, ids, experts)
+
+
+def test_route_top2_without_bias_and_strided_logits(gpu_lib):
+    import torch
+    big = _normal(3, 90, 200, dtype="f32")
+    l = big[:, 17:17 + 64]
+    ids, _, gap = route(l.double().numpy(), 4, groups=8, groups_kept=3, group_score="top2")
+    assert gap > 1e-7
+    r = gpu_lib.route(big.cuda()[:, 17:17 + 64], 4, groups=8, groups_kept=3, group_score="top2")
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+
+
+def test_route_gradient_against_differences(gpu_lib):
+    import torch
+    l = _normal(11, 9, 16, dtype="f32")
+    g = _normal(12, 9, 3, dtype="f32")
+    for score in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            r = gpu_lib.route(l.cuda(), 3, score=score, renormalise=renorm)
+            d = _np(gpu_lib.route_backward(l.cuda(), r, g.cuda()))
+            ids = r.ids.cpu().numpy()
+            h = 1e-5
+            for e in range(16):
+                vals = []
+                for sign in (1, -1):
+                    x = l.double().numpy().copy()
+                    x[:, e] += sign * h
+                    _, s = scores(x, score)
+                    w = np.take_along_axis(s, ids, 1)
+                    vals.append(((w / w.sum(1, keepdims=True) if renorm else w) * g.double().numpy()).sum(1))
+                # differences: h^2 / 6 of a third derivative below 10; the kernel: 32 bits of values below 10
+                assert np.allclose(d[:, e], (vals[0] - vals[1]) / (2 * h), atol=2e-5, rtol=0)
+
+
+def test_route_empty_batch(gpu_lib):
+    import torch
+    r = gpu_lib.route(torch.empty(0, 16, device="cuda"), 2)
+    assert r.ids.shape == (0, 2) and torch.all(r.offsets == 0)
+    x = torch.empty(0, 32, device="cuda", dtype=torch.bfloat16)
+    w = torch.ones(16, 24, 32, device="cuda", dtype=torch.bfloat16)
+    assert gpu_lib.expert_product(x, w, r).shape == (0, 24)
+    dx, dw = gpu_lib.expert_product_backward(torch.empty(0, 24, device="cuda", dtype=torch.bfloat16), x, w, r)
+    assert dx.shape == (0, 32) and torch.all(dw == 0)
+    assert gpu_lib.experts(x, torch.ones(16, 48, 32, device="cuda", dtype=torch.bfloat16),
+                           torch.ones(16, 32, 24, device="cuda", dtype=torch.bfloat16), r).shape == (0, 32)
+    assert gpu_lib.adapted_product(x, w[0], w[:, :8], w[:, :, :8], torch.empty(0, dtype=torch.int32, device="cuda")).shape == (0, 24)
+
+
+# ---- the transpose of given ids ----------------------------------------------------------------
+@pytest.mark.parametrize("tokens,groups,top_k", [(1, 1, 1), (5, 3, 2), (2049, 7, 1), (3000, 300, 4), (4097, 1024, 1), (31, 40, 32)])
+def test_group_rows(gpu_lib, tokens, groups, top_k):
+    rng = np.random.default_rng(tokens)
+    ids = rng.integers(-1, groups, (tokens, top_k)).astype(np.int32)  # repeats inside a token are allowed here
+    _check_transpose(_routing(gpu_lib, ids, groups), ids, groups)
+
+
+def test_group_rows_out_of_range_ids_are_reported(gpu_lib):
+    ids = np.array([[0, 5, 2, -7, 1]], np.int32).T.copy()
+    r = _routing(gpu_lib, ids, 3)
+    _check_transpose(r, np.where((ids < 3) & (ids >= 0), ids, -1), 3)
+    with pytest.raises(gpu_lib.SpgemmError) as e:
+        gpu_lib.grouped_status()
+    assert e.value.code == -6
+    gpu_lib.grouped_status()  # reading clears it
+
+
+# ---- products --------------------------------------------------------------------------------
+# tokens, groups, top_k, d, n: one token; a group longer than a tile; empty groups; sizes that end
+# inside every tile; rows that do not start on 16 bytes (odd d, odd n)
+PRODUCTS = [
+    (1, 1, 1, 8, 8), (1, 4, 2, 64, 128), (3, 5, 2, 72, 40), (17, 8, 4, 136, 264), (33, 64, 6, 256, 96),
+    (300, 3, 2, 128, 72), (700, 5, 3, 328, 392), (1000, 2, 1, 1000, 136), (90, 7, 2, 61, 33), (260, 4, 4, 64, 640),
+]
+
+
+@pytest.mark.parametrize("tokens,groups,top_k,d,n", PRODUCTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_expert_product_and_gradients(gpu_lib, tokens, groups, top_k, d, n, dtype):
+    import torch
+    ids = _random_ids(tokens + d, tokens, groups, min(top_k, groups), empty=(1,) if groups > 2 else ())
+    k = ids.shape[1]
+    r = _routing(gpu_lib, ids, groups)
+    offsets, order, position = transpose(ids, groups)
+    x, w = _normal(1, tokens, d, dtype=dtype), _normal(2, groups, n, d, dtype=dtype)
+    y = gpu_lib.expert_product(x.cuda(), w.cuda(), r)
+    xd, wd = _np(x), _np(w)
+    want, mag = product(xd, wd, ids, offsets, order)
+    assert np.all(np.abs(_np(y) - want) <= rounding(dtype, want) + SUM * d * mag)
+    assert torch.all(y[offsets[-1]:] == 0)
+    full = gpu_lib.expert_product(x.cuda(), w.cuda(), r, out_dtype=torch.float32)
+    assert np.all(np.abs(_np(full) - want) <= SUM * d * mag)
+    # rows already in group order
+    rows = torch.zeros(ids.size, d, dtype=x.dtype)
+    rows[:offsets[-1]] = x[torch.tensor(order[:offsets[-1]] // k, dtype=torch.long)]
+    again = gpu_lib.expert_product(rows.cuda(), w.cuda(), r, grouped=True)
+    assert np.all(np.abs(_np(again) - want) <= rounding(dtype, want) + SUM * d * mag)
+    # gradients
+    dy = _normal(3, ids.size, n, dtype=dtype)
+    dy[offsets[-1]:] = float("nan")  # rows without a slot take no part
+    dx, dw = gpu_lib.expert_product_backward(dy.cuda(), x.cuda(), w.cuda(), r)
+    dyd = _np(dy)
+    wx, mx = np.zeros((tokens, d)), np.zeros((tokens, d))
+    ww, mw, most = np.zeros((groups, n, d)), np.zeros((groups, n, d)), 1
+    for g in range(groups):
+        p = slice(offsets[g], offsets[g + 1])
+        tok = order[p] // k
+        np.add.at(wx, tok, dyd[p] @ wd[g])
+        np.add.at(mx, tok, np.abs(dyd[p]) @ np.abs(wd[g]))
+        ww[g], mw[g] = dyd[p].T @ xd[tok], np.abs(dyd[p]).T @ np.abs(xd[tok])
+        most = max(most, len(tok))
+    assert np.all(np.abs(_np(dx) - wx) <= rounding(dtype, wx) + SUM * (n + k) * mx)
+    assert np.all(np.abs(_np(dw) - ww) <= rounding(dtype, ww) + SUM * most * mw)
+    only = gpu_lib.expert_product_backward(dy.cuda(), x.cuda(), w.cuda(), r, need_dx=False)
+    assert only[0] is None and torch.equal(only[1], dw)
+    gpu_lib.grouped_status()
+
+
+def test_product_gradients_against_differences(gpu_lib):
+    import torch
+    ids = _random_ids(3, 12, 3, 2)
+    r = _routing(gpu_lib, ids, 3)
+    offsets, order, _ = transpose(ids, 3)
+    x, w, dy = _normal(1, 12, 16, dtype="f32"), _normal(2, 3, 8, 16, dtype="f32"), _normal(3, 24, 8, dtype="f32")
+    dx, dw = gpu_lib.expert_product_backward(dy.cuda(), x.cuda(), w.cuda(), r)
+    f = lambda a, b: (product(a, b, ids, offsets, order)[0] * _np(dy))[:offsets[-1]].sum()  # noqa: E731
+    rng = np.random.default_rng(0)
+    for _ in range(20):
+        u, v = rng.standard_normal((12, 16)), rng.standard_normal((3, 8, 16))
+        h = 1e-4  # the function is linear in each argument: differences have no error of their own
+        dfx = (f(_np(x) + h * u, _np(w)) - f(_np(x) - h * u, _np(w))) / (2 * h)
+        dfw = (f(_np(x), _np(w) + h * v) - f(_np(x), _np(w) - h * v)) / (2 * h)
+        assert abs((_np(dx) * u).sum() - dfx) <= 1e-4 * (1 + abs(dfx))
+        assert abs((_np(dw) * v).sum() - dfw) <= 1e-4 * (1 + abs(dfw))
+
+
+def test_product_strides_and_streams(gpu_lib):
+    """Column slices, padded group strides and a side stream."""
+    import torch
+    ids = _random_ids(8, 200, 6, 2)
+    r = _routing(gpu_lib, ids, 6)
+    offsets, order, _ = transpose(ids, 6)
+    for pad in (8, 3):  # rows on 16-byte boundaries, and not
+        xb, wb = _normal(1, 200, 128 + pad), _normal(2, 7, 100, 128 + pad)
+        x, w = xb[:, :128], wb[:6, 4:84, :128]
+        want, mag = product(_np(x), _np(w), ids, offsets, order)
+        xc, wc = xb.cuda(), wb.cuda()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        y = gpu_lib.expert_product(xc[:, :128], wc[:6, 4:84, :128], r, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert np.all(np.abs(_np(y) - want) <= rounding("bf16", want) + SUM * 128 * mag)
+
+
+def test_masked_values_stay_in_their_rows(gpu_lib):
+    """A NaN or infinite row of x reaches only its own slots, in every product."""
+    import torch
+    ids = _random_ids(4, 150, 4, 2)
+    r = _routing(gpu_lib, ids, 4)
+    x, w = _normal(1, 150, 64), _normal(2, 4, 48, 64)
+    clean = gpu_lib.expert_product(x.cuda(), w.cuda(), r)
+    x[7], x[99, 3] = float("nan"), INF
+    y = gpu_lib.expert_product(x.cuda(), w.cuda(), r)
+    hit = torch.zeros(300, dtype=torch.bool)
+    pos = r.position.cpu()
+    for t in (7, 99):
+        hit[pos[t][pos[t] >= 0].long()] = True
+    assert torch.equal(y.cpu()[~hit], clean.cpu()[~hit])
+    assert not torch.isfinite(y.cpu()[hit].float()).all(1).any()
+    # the gradient of one group's weights sees its own rows only
+    dy = _normal(3, 300, 48)
+    _, dw = gpu_lib.expert_product_backward(dy.cuda(), x.cuda(), w.cuda(), r, need_dx=False)
+    bad = {int(g) for t in (7, 99) for g in ids[t] if g >= 0}
+    for g in range(4):
+        assert torch.isfinite(dw[g].float()).all().item() == (g not in bad)
+
+
+# ---- weighted sums -----------------------------------------------------------------------------
+@pytest.mark.parametrize("tokens,groups,top_k,n", [(1, 1, 1, 8), (5, 4, 3, 40), (300, 16, 6, 264), (77, 9, 2, 33), (9, 32, 32, 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_combine_and_gradients(gpu_lib, tokens, groups, top_k, n, dtype):
+    import torch
+    ids = _random_ids(tokens, tokens, groups, top_k)
+    weights = np.random.default_rng(1).random(ids.shape).astype(np.float32)
+    r = _routing(gpu_lib, ids, groups, weights)
+    offsets, order, position = transpose(ids, groups)
+    y, dout = _normal(1, ids.size, n, dtype=dtype), _normal(2, tokens, n, dtype=dtype)
+    y[offsets[-1]:] = float("nan")
+    out = gpu_lib.combine(y.cuda(), r)
+    dy, dweights = gpu_lib.combine_backward(dout.cuda(), y.cuda(), r)
+    yd, dd = _np(y), _np(dout)
+    for t in range(tokens):
+        js = [j for j in range(top_k) if position[t, j] >= 0]
+        terms = np.array([weights[t, j] * yd[position[t, j]] for j in js]).reshape(len(js), n)
+        want = terms.sum(0)
+        assert np.all(np.abs(_np(out[t]) - want) <= rounding(dtype, want) + SUM * top_k * np.abs(terms).sum(0))
+        for j in range(top_k):
+            p = position[t, j]
+            if p < 0:
+                assert dweights[t, j] == 0
+                continue
+            assert abs(float(dweights[t, j]) - dd[t] @ yd[p]) <= SUM * n * (np.abs(dd[t]) @ np.abs(yd[p])) + 1e-30
+            want = weights[t, j] * dd[t]
+            assert np.all(np.abs(_np(dy[p]) - want) <= rounding(dtype, want) + 2.0 ** -24 * np.abs(want))
+    assert torch.all(dy[offsets[-1]:] == 0)
+
+
+# ---- the gated layer -----------------------------------------------------------------------------
+@pytest.mark.parametrize("tokens,groups,top_k,d,hidden,n", [
+    (1, 1, 1, 8, 8, 8), (1, 16, 4, 64, 96, 64), (9, 8, 3, 72, 40, 136), (200, 6, 2, 128, 64, 200), (700, 4, 2, 264, 328, 128),
+    (64, 64, 6, 256, 128, 256), (31, 5, 2, 37, 19, 41), (600, 3, 3, 512, 256, 512),
+])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_experts(gpu_lib, tokens, groups, top_k, d, hidden, n, dtype):
+    ids = _random_ids(tokens + 1, tokens, groups, top_k, empty=(0,) if groups > 4 else ())
+    weights = np.random.default_rng(1).random(ids.shape).astype(np.float32)
+    r = _routing(gpu_lib, ids, groups, weights)
+    x = _normal(1, tokens, d, dtype=dtype)
+    up, down = _normal(2, groups, 2 * hidden, d, dtype=dtype, std=d ** -0.5), _normal(3, groups, n, hidden, dtype=dtype, std=hidden ** -0.5)
+    out = _np(gpu_lib.experts(x.cuda(), up.cuda(), down.cuda(), r))
+    xd, ud, dd = _np(x), _np(up), _np(down)
+    want, tol = np.zeros((tokens, n)), np.zeros((tokens, n))
+    for t in range(tokens):
+        for j in range(top_k):
+            g = ids[t, j]
+            if g < 0:
+                continue
+            pre, mag = ud[g] @ xd[t], np.abs(ud[g]) @ np.abs(xd[t])
+            gate, u = pre[:hidden], pre[hidden:]
+            sig = 1 / (1 + np.exp(-gate))
+            h = gate * sig * u
+            # errors of the two products through silu (slope at most 1.1), exp and division, one rounding of h
+            eh = SUM * d * (1.1 * np.abs(u) * mag[:hidden] + np.abs(gate * sig) * mag[hidden:]) + (U[dtype] + 2.0 ** -20) * np.abs(h)
+            want[t] += weights[t, j] * (dd[g] @ h)
+            tol[t] += weights[t, j] * (np.abs(dd[g]) @ (eh + SUM * (hidden + top_k) * np.abs(h)))
+    small = TINY[dtype] * hidden  # roundings of h below the type's normal range
+    assert np.all(np.abs(out - want) <= rounding(dtype, want) + 1.01 * tol + small)
+    gpu_lib.grouped_status()
+
+
+# ---- adapters ------------------------------------------------------------------------------------
+@pytest.mark.parametrize("tokens,adapters,rank,d,n", [
+    (1, 1, 8, 64, 64), (1, 3, 16, 128, 72), (5, 2, 8, 40, 136), (64, 48, 16, 256, 264), (300, 3, 64, 512, 128),
+    (777, 5, 24, 200, 520), (140, 4, 128, 96, 64), (33, 4, 200, 64, 48), (50, 3, 7, 37, 21), (260, 1024, 8, 64, 64),
+])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_adapted_product(gpu_lib, tokens, adapters, rank, d, n, dtype, mixed):
+    import torch
+    rng = np.random.default_rng(tokens)
+    if mixed:  # any order of adapters
+        ids = rng.integers(-1, adapters, tokens).astype(np.int32)
+    else:  # runs of requests, one of them without an adapter
+        ids = np.sort(rng.integers(-1, adapters, tokens)).astype(np.int32)
+    x, w = _normal(1, tokens, d, dtype=dtype), _normal(2, n, d, dtype=dtype, std=d ** -0.5)
+    a, b = _normal(3, adapters, rank, d, dtype=dtype, std=d ** -0.5), _normal(4, adapters, n, rank, dtype=dtype, std=0.3)
+    scale = torch.rand(adapters, generator=_gen(9)) + 0.5
+    y = _np(gpu_lib.adapted_product(x.cuda(), w.cuda(), a.cuda(), b.cuda(), torch.tensor(ids).cuda(), scale.cuda()))
+    xd, wd, ad, bd = _np(x), _np(w), _np(a), _np(b)
+    want, tol = xd @ wd.T, SUM * (d + rank) * (np.abs(xd) @ np.abs(wd).T)
+    for t in range(tokens):
+        if ids[t] >= 0:
+            g, s = ids[t], float(scale[ids[t]])
+            v, mv = ad[g] @ xd[t], np.abs(ad[g]) @ np.abs(xd[t])
+            want[t] += s * (bd[g] @ v)
+            # v is rounded to the inputs' type once between the two small products
+            tol[t] += s * (np.abs(bd[g]) @ (SUM * (d + rank) * mv + (U[dtype] + 2.0 ** -22) * np.abs(v)))
+    assert np.all(np.abs(y - want) <= rounding(dtype, want) + 1.01 * tol)
+    gpu_lib.grouped_status()
+
+
+def test_adapters_without_scale_and_with_nan_rows(gpu_lib):
+    """No scale means ones; a row of NaN reaches no other row; unused adapters may hold anything."""
+    import torch
+    ids = torch.tensor([0, 2, -1, 2, 0, 1] * 20, dtype=torch.int32)
+    x, w = _normal(1, 120, 64), _normal(2, 48, 64, std=0.1)
+    a, b = _normal(3, 4, 16, 64, std=0.1), _normal(4, 4, 48, 16)
+    a[3], b[3] = float("nan"), float("nan")
+    y = gpu_lib.adapted_product(x.cuda(), w.cuda(), a.cuda(), b.cuda(), ids.cuda())
+    ones = gpu_lib.adapted_product(x.cuda(), w.cuda(), a.cuda(), b.cuda(), ids.cuda(), torch.ones(4).cuda())
+    assert torch.equal(y, ones) and torch.isfinite(y.float()).all()
+    x[5] = float("nan")
+    z = gpu_lib.adapted_product(x.cuda(), w.cuda(), a.cuda(), b.cuda(), ids.cuda())
+    keep = torch.arange(120) != 5
+    assert torch.equal(z.cpu()[keep], y.cpu()[keep]) and torch.isnan(z[5].float()).all()
+
+
+def test_results_repeat_bit_for_bit(gpu_lib):
+    import torch
+    l = _normal(1, 3000, 32, dtype="f32").cuda()
+    x, w = _normal(2, 3000, 128).cuda(), _normal(3, 32, 96, 128).cuda()
+    first = None
+    for _ in range(3):
+        r = gpu_lib.route(l, 4)
+        y = gpu_lib.expert_product(x, w, r)
+        out = gpu_lib.combine(y, r)
+        dy, dwt = gpu_lib.combine_backward(out, y, r)
+        dx, dw = gpu_lib.expert_product_backward(dy, x, w, r)
+        now = [r.ids, r.weights, r.order, y, out, dy, dwt, dx, dw]
+        first = first or now
+        assert all(torch.equal(a, b) for a, b in zip(first, now))
+
+
+def test_routing_as_sparse_matrices(gpu_lib):
+    """The choice and its transpose as CSR, multiplied by the library's SpGEMM: how often two experts
+    serve the same token."""
+    ids = _random_ids(5, 400, 12, 3)
+    r = _routing(gpu_lib, ids, 12)
+    rp, col, val = gpu_lib.multiply(r.transposed_csr(), r.to_csr()).to_host()
+    got = np.zeros((12, 12))
+    for i in range(12):
+        got[i, col[rp[i]:rp[i + 1]]] = val[rp[i]:rp[i + 1]]
+    one = np.zeros((400, 12))
+    for t in range(400):
+        one[t, ids[t][ids[t] >= 0]] = 1
+    assert np.array_equal(got, one.T @ one)
+
+
+def test_refusals(gpu_lib):
+    import torch
+    l = torch.zeros(4, 8, device="cuda")
+    for kw in (dict(top_k=9), dict(top_k=0), dict(top_k=2, groups=3), dict(top_k=2, groups=2, groups_kept=3),
+               dict(top_k=2, scale=INF)):
+        with pytest.raises(gpu_lib.SpgemmError) as e:
+            gpu_lib.route(l, **kw)
+        assert e.value.code == -1
+    with pytest.raises(ValueError):
+        gpu_lib.route(l, 2, score="relu")
+    with pytest.raises(TypeError):
+        gpu_lib.route(l.double(), 2)
+    with pytest.raises(ValueError):
+        gpu_lib.route(l.t(), 2)
+    r = gpu_lib.route(l, 2)
+    x, w = torch.zeros(4, 16, device="cuda"), torch.zeros(8, 24, 16, device="cuda")
+    with pytest.raises(gpu_lib.SpgemmError):
+        gpu_lib.expert_product(x, w[:7], r)
+    with pytest.raises(gpu_lib.SpgemmError):
+        gpu_lib.expert_product(x, w.half(), r)
+    with pytest.raises(gpu_lib.SpgemmError):
+        gpu_lib.expert_product(x[:3], w, r)
+    with pytest.raises(gpu_lib.SpgemmError):
+        gpu_lib.experts(x, w, w, r)
+    with pytest.raises(gpu_lib.SpgemmError):
+        gpu_lib.combine(torch.zeros(7, 24, device="cuda"), r)
+    with pytest.raises(ValueError):
+        gpu_lib.adapted_product(x, w[0], w[:, :2], w[:, :, :2], torch.zeros(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        gpu_lib.expert_product(x.cpu(), w, r)
+    with pytest.raises(ValueError):
+        gpu_lib.route_backward(l, gpu_lib.group_rows(r.ids, 8), torch.zeros(4, 2, device="cuda"))

@@ -1,0 +1,160 @@
+"""The grouped-product entry points without a GPU: layouts of their structures, and calls that are
+refused before any device work."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+
+import sparse_gemm_irregular_gb300 as sg
+from _grouped_ref import route, route_grad, scores, transpose
+from sparse_gemm_irregular_gb300 import binding as b
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(__file__)), "include")
+
+
+def test_struct_layouts_match_the_header(tmp_path):
+    if not shutil.which("gcc"):
+        pytest.skip("no host C compiler")
+    structs = [b.spgemm_dense, b.spgemm_weights, b.spgemm_grouping, b.spgemm_route_rule]
+    lines = ['#include <stdio.h>', '#include <stddef.h>', '#include "spgemm.h"', "int main(void) {"]
+    for cls in structs:
+        lines.append('printf("%%zu\\n", sizeof(%s));' % cls.__name__)
+        lines += ['printf("%%zu\\n", offsetof(%s, %s));' % (cls.__name__, f) for f, _ in cls._fields_]
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text("\n".join(lines + ["return 0; }"]))
+    subprocess.check_call(["gcc", "-std=c99", "-I", HEADER, str(src), "-o", str(exe)])
+    got = [int(v) for v in subprocess.check_output([str(exe)], text=True).split()]
+    want = []
+    for cls in structs:
+        want += [ctypes.sizeof(cls)] + [getattr(cls, f).offset for f, _ in cls._fields_]
+    assert got == want
+
+
+def dense(rows, cols, stride=None, dtype=1, data=16):
+    return b.spgemm_dense(data, rows, cols, cols if stride is None else stride, dtype, 0)
+
+
+def weights(groups, rows, cols, dtype=1):
+    return b.spgemm_weights(16, groups, rows, cols, rows * cols, cols, dtype, 0)
+
+
+def grouping(slots, top_k, groups):
+    return b.spgemm_grouping(slots, top_k, groups, 16, 16, 16)
+
+
+def rule(**kw):
+    d = dict(top_k=2, score=0, groups=1, groups_kept=1, group_score=0, renormalise=1, scale=1.0, reserved=0) | kw
+    return b.spgemm_route_rule(*[d[f] for f, _ in b.spgemm_route_rule._fields_])
+
+
+R = ctypes.byref
+
+
+@pytest.mark.parametrize("kw", [dict(top_k=0), dict(top_k=9), dict(score=2), dict(score=-1), dict(groups=3), dict(groups=0),
+                                dict(groups=2, groups_kept=3), dict(groups_kept=0), dict(group_score=5),
+                                dict(scale=float("nan")), dict(scale=float("inf"))])
+def test_route_refuses_rules(kw):
+    lib = sg.load()
+    assert lib.spgemm_route(R(dense(4, 8)), R(rule(**kw)), None, 16, 16, 16, 16, 16, None) == -1
+    assert lib.spgemm_route_backward(R(dense(4, 8)), R(rule(**kw)), 16, 16, R(dense(4, 8)), None) == -1
+
+
+def test_route_refuses_matrices():
+    lib = sg.load()
+    ok = rule()
+    for l in (dense(4, 0), dense(4, 1025), dense(-1, 8), dense(4, 8, stride=7), dense(4, 8, dtype=3), dense(4, 8, data=0)):
+        assert lib.spgemm_route(R(l), R(ok), None, 16, 16, 16, 16, 16, None) == -1
+    assert lib.spgemm_route(None, R(ok), None, 16, 16, 16, 16, 16, None) == -1
+    assert lib.spgemm_route(R(dense(4, 8)), None, None, 16, 16, 16, 16, 16, None) == -1
+    assert lib.spgemm_route(R(dense(4, 8)), R(ok), None, None, 16, 16, 16, 16, None) == -1
+    assert lib.spgemm_route(R(dense(4, 8)), R(ok), None, 16, 16, None, 16, 16, None) == -1
+    assert lib.spgemm_route(R(dense(1 << 31, 8)), R(ok), None, 16, 16, 16, 16, 16, None) == -5
+    assert lib.spgemm_route_backward(R(dense(4, 8)), R(ok), 16, 16, R(dense(4, 7)), None) == -1
+    assert lib.spgemm_route_backward(R(dense(4, 8)), R(ok), 16, 16, R(dense(4, 8, dtype=0)), None) == -1
+    assert "gradient" in sg.spgemm_last_error()
+
+
+def test_group_rows_refuses():
+    lib = sg.load()
+    assert lib.spgemm_group_rows(16, -1, 4, 16, 16, 16, None) == -1
+    assert lib.spgemm_group_rows(16, 4, 0, 16, 16, 16, None) == -1
+    assert lib.spgemm_group_rows(16, 4, 1025, 16, 16, 16, None) == -1
+    assert lib.spgemm_group_rows(None, 4, 4, 16, 16, 16, None) == -1
+    assert lib.spgemm_group_rows(16, 1 << 31, 4, 16, 16, 16, None) == -5
+
+
+def test_products_refuse():
+    lib = sg.load()
+    g, x, w, y = grouping(8, 2, 3), dense(4, 16), weights(3, 24, 16), dense(8, 24)
+    call = lambda g=g, x=x, flag=0, w=w, y=y: lib.spgemm_grouped_product(R(g), R(x), flag, R(w), R(y), None)  # noqa: E731
+    for kw in (dict(g=grouping(8, 2, 4)), dict(g=grouping(8, 0, 3)), dict(g=grouping(8, 33, 3)), dict(g=grouping(9, 2, 3)),
+               dict(x=dense(4, 15)), dict(x=dense(5, 16)), dict(x=dense(4, 16, dtype=2)), dict(w=weights(3, 24, 17)),
+               dict(w=weights(2, 24, 16)), dict(y=dense(8, 23)), dict(y=dense(7, 24)), dict(y=dense(8, 24, dtype=2)),
+               dict(flag=1), dict(x=dense(4, 16, data=0))):
+        assert call(**kw) == -1, kw
+    back = lambda g=g, dy=y, x=x, w=w, dx=x, dw=w: lib.spgemm_grouped_product_backward(  # noqa: E731
+        R(g), R(dy), R(x), R(w), R(dx), R(dw), None)
+    for kw in (dict(dy=dense(8, 25)), dict(dy=dense(7, 24)), dict(dx=dense(4, 15)), dict(dx=dense(4, 16, dtype=0)),
+               dict(dw=weights(3, 24, 8)), dict(x=dense(3, 16)), dict(w=weights(3, 24, 16, dtype=2))):
+        assert back(**kw) == -1, kw
+
+
+def test_layers_refuse():
+    lib = sg.load()
+    g, x, up, down, out = grouping(8, 2, 3), dense(4, 16), weights(3, 48, 16), weights(3, 40, 24), dense(4, 40)
+    call = lambda g=g, wt=16, x=x, up=up, down=down, out=out: lib.spgemm_experts(  # noqa: E731
+        R(g), wt, R(x), R(up), R(down), R(out), None)
+    for kw in (dict(wt=None), dict(up=weights(3, 47, 16)), dict(down=weights(3, 40, 23)), dict(out=dense(4, 41)),
+               dict(out=dense(5, 40)), dict(x=dense(4, 16, dtype=0)), dict(g=grouping(8, 2, 2))):
+        assert call(**kw) == -1, kw
+    w, a, bb, y = dense(24, 16), weights(5, 4, 16), weights(5, 24, 4), dense(4, 24)
+    call = lambda x=x, w=w, a=a, bb=bb, ids=16, y=y: lib.spgemm_adapted_product(  # noqa: E731
+        R(x), R(w), R(a), R(bb), ids, None, R(y), None)
+    for kw in (dict(ids=None), dict(w=dense(24, 15)), dict(a=weights(4, 4, 16)), dict(a=weights(5, 3, 16)),
+               dict(bb=weights(5, 23, 4)), dict(y=dense(4, 23)), dict(y=dense(3, 24)), dict(a=weights(5, 4, 16, dtype=2)),
+               dict(a=weights(1025, 4, 16), bb=weights(1025, 24, 4))):
+        assert call(**kw) == -1, kw
+    c = lambda g=g, y=dense(8, 40), o=out: lib.spgemm_combine(R(g), 16, R(y), R(o), None)  # noqa: E731
+    for kw in (dict(y=dense(7, 40)), dict(y=dense(8, 39)), dict(o=dense(3, 40)), dict(g=grouping(8, 3, 3))):
+        assert c(**kw) == -1, kw
+    assert lib.spgemm_combine_backward(R(g), 16, R(out), R(dense(8, 40)), R(dense(8, 39)), 16, None) == -1
+    assert lib.spgemm_combine_backward(R(g), 16, R(out), R(dense(8, 40)), R(dense(8, 40)), None, None) == -1
+
+
+# ---- the reference of the GPU tests, pinned by closed forms -------------------------------------
+def test_reference_route_closed_forms():
+    ids, w, _ = route(np.array([[0.0, np.log(2.0), np.log(4.0), -np.inf]]), 2)
+    assert ids.tolist() == [[1, 2]] and np.allclose(w, [[1 / 3, 2 / 3]])
+    ids, w, _ = route(np.zeros((1, 6)), 3, renormalise=False)
+    assert ids.tolist() == [[0, 1, 2]] and np.allclose(w, 1 / 6)
+    ids, _, _ = route(np.array([[5.0, 0.0, 3.0, 3.0]]), 2, groups=2, groups_kept=1, group_score="top2", score="sigmoid",
+                      bias=np.zeros(4))
+    assert ids.tolist() == [[2, 3]]
+    ids, w, _ = route(np.full((1, 4), -np.inf), 2)
+    assert ids.tolist() == [[-1, -1]] and w.tolist() == [[0, 0]]
+
+
+def test_reference_gradient_against_differences():
+    rng = np.random.default_rng(0)
+    l, g = rng.standard_normal((4, 7)), rng.standard_normal((4, 3))
+    for score in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            ids, _, _ = route(l, 3, score=score, renormalise=renorm)
+            d = route_grad(l, ids, g, score, renorm, 1.5)
+            for e in range(7):
+                v = []
+                for sign in (1, -1):
+                    x = l.copy()
+                    x[:, e] += sign * 1e-6
+                    w = np.take_along_axis(scores(x, score)[1], ids, 1)
+                    v.append((1.5 * (w / w.sum(1, keepdims=True) if renorm else w) * g).sum(1))
+                assert np.allclose(d[:, e], (v[0] - v[1]) / 2e-6, atol=1e-7)
+
+
+def test_reference_transpose():
+    off, order, pos = transpose(np.array([[1, 2], [-1, -1], [0, 2]]), 3)
+    assert off.tolist() == [0, 1, 2, 4] and order.tolist() == [4, 0, 1, 5, -1, -1]
+    assert pos.tolist() == [[1, 2], [-1, -1], [0, 3]]
