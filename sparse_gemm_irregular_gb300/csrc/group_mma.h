@@ -1,0 +1,40 @@
+// Launchers of the tensor-core grouped products (k_group_mma.cu).
+#pragma once
+
+#include "groups.h"
+
+namespace sg {
+
+enum MmaMode { kMmaForward = 0, kMmaGated = 1, kMmaDx = 2, kMmaDw = 3, kMmaAdapted = 4 };
+
+struct MmaArgs {
+  const int32_t* offsets;  // NULL: one group of all rows
+  const int32_t* order;
+  int slots, groups, top_k;
+  int rows;                // rows of the gathered matrix: the index that reads as zeros
+  int gather, scatter;
+  int bf16;
+  int m, n, depth;         // M side, N side (Dw only), contracted length
+  int tile_n, box_rows;
+  int stages, stage_bytes;
+  void* out;
+  int64_t out_stride, out_group;
+  int out_type;
+  const float* scale;      // per group (scatter)
+  uint32_t* err;
+};
+
+// whether the copy engine can fetch rows of this matrix: 16-bit, 16-byte aligned rows
+bool mma_takes(const spgemm_dense& m);
+bool mma_takes(const spgemm_weights& w);
+
+// The same contracts as the launch_plain_* functions; false: the launch failed (cudaGetLastError
+// or the encoding of a copy descriptor).
+bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool gather, const spgemm_weights& w,
+                        bool gated, const spgemm_dense& y, cudaStream_t s);
+bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_weights& w, float* dx,
+                   cudaStream_t s);
+bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_dense& x, const spgemm_weights& dw,
+                   cudaStream_t s);
+
+}  // namespace sg

@@ -2,7 +2,7 @@
 // stream-ordered pool, and the choice between the tensor-core and the CUDA-core kernels.
 #include <algorithm>
 
-#include "groups.h"
+#include "group_mma.h"
 
 namespace sg {
 
@@ -58,6 +58,13 @@ class Scratch {
 int bad(const char* what) {
   set_last_error(what);
   return SPGEMM_ERR_INVALID_ARG;
+}
+
+int launch_failed(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return check_cuda(e, what);
+  set_last_error(std::string(what) + ": a copy descriptor could not be encoded");
+  return SPGEMM_ERR_CUDA;
 }
 
 bool dense_ok(const spgemm_dense* d) {
@@ -168,7 +175,11 @@ int spgemm_grouped_product(const spgemm_grouping* g, const spgemm_dense* x, int3
   if (w->dtype != x->dtype || (y->dtype != x->dtype && y->dtype != SPGEMM_DTYPE_F32))
     return bad("grouped product: types differ");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  launch_plain_forward(*g, *x, !x_grouped, *w, *y, st);
+  if (mma_takes(*x) && mma_takes(*w)) {
+    if (!launch_mma_forward(*g, *x, !x_grouped, *w, false, *y, st)) return launch_failed("grouped product");
+  } else {
+    launch_plain_forward(*g, *x, !x_grouped, *w, *y, st);
+  }
   return check_cuda(cudaGetLastError(), "grouped product");
 }
 
@@ -188,14 +199,18 @@ int spgemm_grouped_product_backward(const spgemm_grouping* g, const spgemm_dense
     return bad("grouped product backward: types differ");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Scratch scratch(st);
+  const bool mma = g->slots > 0 && mma_takes(*x) && mma_takes(*dy) && mma_takes(*w);
   if (dx && dx->rows > 0) {
     // one 32-bit row per position, summed per token afterwards: the sum is rounded once
     spgemm_dense rows = dense(scratch.get(4 * g->slots * w->cols), g->slots, w->cols, SPGEMM_DTYPE_F32);
     if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
-    launch_plain_dx(*g, *dy, *w, static_cast<float*>(rows.data), st);
+    float* r = static_cast<float*>(rows.data);
+    if (!mma) launch_plain_dx(*g, *dy, *w, r, st);
+    else if (!launch_mma_dx(*g, *dy, *w, r, st)) return launch_failed("grouped product backward");
     launch_combine(*g, nullptr, rows, *dx, st);
   }
-  if (dw) launch_plain_dw(*g, *dy, *x, *dw, st);
+  if (dw && !mma) launch_plain_dw(*g, *dy, *x, *dw, st);
+  else if (dw && !launch_mma_dw(*g, *dy, *x, *dw, st)) return launch_failed("grouped product backward");
   return check_cuda(cudaGetLastError(), "grouped product backward");
 }
 
@@ -241,11 +256,17 @@ int spgemm_experts(const spgemm_grouping* g, const float* weights, const spgemm_
   const spgemm_dense h = dense(scratch.get(g->slots * hidden * dtype_size(x->dtype)), g->slots, hidden, x->dtype);
   // the down product's rows stay in 32 bits: the weighted sum is rounded once
   const spgemm_dense y = dense(scratch.get(4 * g->slots * out->cols), g->slots, out->cols, SPGEMM_DTYPE_F32);
-  const spgemm_dense pre = dense(scratch.get(8 * g->slots * hidden), g->slots, 2 * hidden, SPGEMM_DTYPE_F32);
-  if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
-  launch_plain_forward(*g, *x, true, *w_up, pre, st);
-  launch_gated(static_cast<float*>(pre.data), g->slots, hidden, h, st);
-  launch_plain_forward(*g, h, false, *w_down, y, st);
+  if (mma_takes(*x) && mma_takes(*w_up) && mma_takes(h) && mma_takes(*w_down)) {
+    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
+    if (!launch_mma_forward(*g, *x, true, *w_up, true, h, st) || !launch_mma_forward(*g, h, false, *w_down, false, y, st))
+      return launch_failed("experts");
+  } else {
+    const spgemm_dense pre = dense(scratch.get(8 * g->slots * hidden), g->slots, 2 * hidden, SPGEMM_DTYPE_F32);
+    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
+    launch_plain_forward(*g, *x, true, *w_up, pre, st);
+    launch_gated(static_cast<float*>(pre.data), g->slots, hidden, h, st);
+    launch_plain_forward(*g, h, false, *w_down, y, st);
+  }
   launch_combine(*g, weights, y, *out, st);
   return check_cuda(cudaGetLastError(), "experts");
 }

@@ -1,0 +1,587 @@
+// Grouped products on the tensor cores (tcgen05, 16-bit inputs, 32-bit sums in tensor memory).
+//
+// One kernel computes D[m, j] = sum_k A[m, k] B[j, k] for five products.  The dense, always long
+// side is M (weight rows or columns); the ragged side, the rows of a group, is N, because the
+// instruction takes any N that is a multiple of 16: a group of 5 rows costs an instruction of 16
+// columns, not a tile of 128, and the last tile of each group only what it holds.
+//
+//   mode      A (M side)                      B (N side)                       contracted k
+//   Forward   w[g] rows                       x rows, gathered or in order     columns of x
+//   Gated     64 gate rows + 64 up rows       x rows, gathered                 columns of x
+//   Dx        w[g]^T (columns of w[g])        dy rows                          rows of w[g]
+//   Dw        x^T (columns of gathered x)     dy^T (columns of dy)             the group's positions
+//   Adapted   w rows, then b[i] rows          x rows, then v rows of adapter i columns of x, then rank
+//
+// Operands go to shared memory in 64-deep slices by bulk copies: 128-byte swizzled boxes, rows of x
+// picked by gathering copies straight from the routing's order (no permuted copy of x exists).  A
+// gathered row index past the matrix reads as zeros: that masks the positions behind a group's end (Dw,
+// where they are contracted, on both operands, so that a NaN there cannot leak) and, in Adapted, the
+// tokens of other adapters.
+//
+// Six warps: a producer (copies), an issuer (matrix instructions, one thread), four that empty
+// the accumulators while the next tile is computed into the other half of tensor memory.  The
+// accumulator's lanes are consecutive columns of the output, so a warp's store is contiguous.
+// Persistent blocks; tiles of one group that share its rows are neighbours.
+//
+// Every wait is bounded: a role that gives up sets the status word, the others see it, copies in
+// flight are drained, tensor memory is freed, the kernel returns.
+#include <algorithm>
+
+#include "group_mma.h"
+#include "tc.cuh"
+
+namespace sg {
+
+namespace {
+
+constexpr int kThreads = 192;      // producer, issuer, four epilogue warps
+constexpr int kEpilogue = 128;
+constexpr int kDeep = 64;          // contracted elements of a slice: 128 bytes, one swizzle row
+constexpr int kMaxStages = 12;
+constexpr int kABytes = 128 * 128; // A's part of a stage: 128 rows of 128 bytes
+constexpr int kBox = 64 * 128;     // a 64 x 64 box
+constexpr int kTmemCols = 512;
+constexpr int kSmemMost = 227 * 1024;
+
+struct Control {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t acc_full[2], acc_empty[2], drain;
+  uint32_t tmem;
+  int failed;
+  int go[2];                       // Gated: whether the four epilogue warps take the next tile
+  int last[kMaxStages];            // 1: the stage holds the last slice of its tile
+  int scan[33];
+  int first[kMaxGroups + 1];       // first position of each group (clamped to [0, slots])
+  int tiles[kMaxGroups + 1];       // N-side tiles before each group
+  float swap[4 * 16 * 32];         // Gated: halves that the gate and up warps exchange
+};
+
+struct Tile {
+  int g;       // group
+  int m0;      // first M index
+  int j0;      // first position (Dw: first column of dy)
+  int n;       // N indices that count
+  int k0, k;   // contracted range: first position and length (Dw), else 0 and the depth
+};
+
+}  // namespace
+
+struct MmaMaps {
+  CUtensorMap a, b, c, d;  // Forward: w, x; Dw: gathered x, dy boxes, gathered dy; Adapted: w, x, b[i], gathered v
+};
+
+template <int MODE, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant__ MmaMaps maps,
+                                                           const __grid_constant__ MmaArgs p) {
+  using namespace tc;
+  extern __shared__ char smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  Control& c = *reinterpret_cast<Control*>(smem_raw + (base - smem_u32(smem_raw)) + p.stages * p.stage_bytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  constexpr int kSide = PAIR ? 2 : 1;
+  constexpr bool kDw = MODE == kMmaDw;
+  volatile int* failed = &c.failed;
+
+  // ---- set-up: barriers, tensor memory, the groups' first positions and tile counts -----------
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(smem_u32(&c.full[s]), 1);
+      mbar_init(smem_u32(&c.empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&c.acc_full[b]), 1);
+      mbar_init(smem_u32(&c.acc_empty[b]), kEpilogue * kSide);
+    }
+    mbar_init(smem_u32(&c.drain), 1);
+    c.failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<PAIR>(smem_u32(&c.tmem), kTmemCols);
+  // offsets are used as a non-decreasing sequence inside [0, slots], whatever the array holds
+  {
+    int run = 0, top = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += kThreads) {
+      const int g = g0 + static_cast<int>(threadIdx.x);
+      int lo = 0, hi = 0;
+      if (g < p.groups) {
+        lo = p.offsets ? min(max(p.offsets[g], 0), p.slots) : 0;
+        hi = p.offsets ? min(max(p.offsets[g + 1], lo), p.slots) : p.slots;
+        c.first[g] = lo;
+      }
+      const int n = kDw ? 0 : (hi - lo + p.tile_n - 1) / p.tile_n;
+      const int incl = block_incl_scan(n, c.scan, &top);
+      if (g < p.groups) {
+        c.tiles[g] = run + incl - n;
+        if (g == p.groups - 1) c.first[p.groups] = hi;
+      }
+      run += top;
+    }
+    if (threadIdx.x == 0) c.tiles[p.groups] = run;
+  }
+  fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync();
+  fence_after();
+  const uint32_t tmem = c.tmem;
+  const int m_per_tile = (MODE == kMmaGated ? 64 : 128) * kSide;
+  const int mt = (p.m + m_per_tile - 1) / m_per_tile;
+  const int nt = kDw ? (p.n + p.tile_n - 1) / p.tile_n : 0;
+  const int64_t total = kDw ? static_cast<int64_t>(p.groups) * mt * nt : static_cast<int64_t>(c.tiles[p.groups]) * mt;
+  const int64_t worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, workers = PAIR ? gridDim.x >> 1 : gridDim.x;
+
+  auto tile_at = [&](int64_t i) {
+    Tile t;
+    if (kDw) {
+      t.g = static_cast<int>(i / (static_cast<int64_t>(mt) * nt));
+      const int r = static_cast<int>(i - static_cast<int64_t>(t.g) * mt * nt);
+      t.m0 = (r % mt) * m_per_tile;
+      t.j0 = (r / mt) * p.tile_n;
+      t.n = min(p.n - t.j0, p.tile_n);
+      t.k0 = c.first[t.g];
+      t.k = max(c.first[t.g + 1] - t.k0, 0);
+    } else {
+      const int r = static_cast<int>(i / mt);
+      t.m0 = static_cast<int>(i - static_cast<int64_t>(r) * mt) * m_per_tile;
+      int lo = 0, hi = p.groups;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (c.tiles[mid] <= r) lo = mid;
+        else hi = mid;
+      }
+      t.g = lo;
+      const int lastp = p.offsets ? min(max(p.offsets[lo + 1], c.first[lo]), p.slots) : p.slots;
+      t.j0 = c.first[lo] + (r - c.tiles[lo]) * p.tile_n;
+      t.n = min(lastp - t.j0, p.tile_n);
+      t.k0 = 0;
+      t.k = p.depth;
+    }
+    return t;
+  };
+  // columns of the instruction: a multiple of 16 per block of the pair
+  auto columns = [&](int n) { return (n + 16 * kSide - 1) / (16 * kSide) * (16 * kSide); };
+
+  if (warp == 0) {
+    // ---- producer ------------------------------------------------------------------------------
+    int s = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t i = worker; i < total && ok; i += workers) {
+      const Tile t = tile_at(i);
+      const int cols = columns(t.n), half = cols / kSide;
+      const int jr = t.j0 + static_cast<int>(rank) * half;  // first N index of this block
+      // rows that this lane gathers: quads `lane` and `lane + 32` of this block's N side
+      int4 quad[2];
+      if ((MODE == kMmaForward || MODE == kMmaGated) && p.gather) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          int r[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = jr + (lane + 32 * h) * 4 + e;
+            const int slot = j < t.j0 + t.n ? p.order[j] : -1;
+            const int row = slot >= 0 ? slot / p.top_k : p.rows;
+            r[e] = min(row, p.rows);
+          }
+          quad[h] = make_int4(r[0], r[1], r[2], r[3]);
+        }
+      }
+      // one slice: waits for a free stage and announces its bytes; returns the stage's address
+      auto open = [&](uint32_t bytes, bool last) -> uint32_t {
+        ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && lane == 0) {
+          c.last[s] = last ? 1 : 0;
+          if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), bytes * kSide);
+        }
+        __syncwarp();
+        return base + s * p.stage_bytes;
+      };
+      auto bar = [&]() { return PAIR ? map_rank(smem_u32(&c.full[s]), 0) : smem_u32(&c.full[s]); };
+      auto close = [&]() {
+        if (++s == p.stages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      };
+
+      if (kDw) {
+        const int slices = (t.k + kDeep - 1) / kDeep;
+        const int nb = (half + 63) / 64;  // 64-column blocks of dy
+        int next[4];                      // order entries of this lane's quad in the next slice
+        auto fetch = [&](int k0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int q = k0 + (lane & 15) * 4 + e;
+            const int slot = q < t.k ? p.order[t.k0 + q] : -1;
+            next[e] = slot >= 0 ? min(slot / p.top_k, p.rows) : p.rows;
+          }
+        };
+        fetch(0);
+        for (int q = 0; q < slices && ok; ++q) {
+          const int4 mine = make_int4(next[0], next[1], next[2], next[3]);
+          if (q + 1 < slices) fetch((q + 1) * kDeep);
+          const uint32_t a = open(static_cast<uint32_t>((2 + nb) * kBox), q + 1 == slices), b = a + kABytes;
+          if (!ok) break;
+          const uint32_t fb = bar();
+          const int m0 = t.m0 + static_cast<int>(rank) * 128;
+          // x: 2 blocks of 64 columns, 16 quads of rows each: one quad per lane
+          load_rows4<PAIR>(a + (lane >> 4) * kBox + (lane & 15) * 512, &maps.a, m0 + (lane >> 4) * 64, mine, fb);
+          const int k0 = q * kDeep;
+          if (k0 + kDeep <= t.k) {
+            if (lane < nb) load_2d<PAIR>(b + lane * kBox, &maps.b, jr + lane * 64, t.k0 + k0, fb);
+          } else {  // the group ends inside the slice: dy's rows past it read as zeros too
+            int r[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int o = k0 + (lane & 15) * 4 + e;
+              r[e] = o < t.k ? t.k0 + o : p.slots;
+            }
+            for (int blk = lane >> 4; blk < nb; blk += 2)
+              load_rows4<PAIR>(b + blk * kBox + (lane & 15) * 512, &maps.c, jr + blk * 64,
+                               make_int4(r[0], r[1], r[2], r[3]), fb);
+          }
+          close();
+        }
+        continue;
+      }
+
+      const int boxes = (half + p.box_rows - 1) / p.box_rows;
+      const bool gather = (MODE == kMmaForward || MODE == kMmaGated) && p.gather;
+      const uint32_t bytes = kABytes + (gather ? half : boxes * p.box_rows) * 128;
+      const int slices = (t.k + kDeep - 1) / kDeep;
+      for (int q = 0; q < slices && ok; ++q) {
+        const uint32_t a = open(bytes, MODE != kMmaAdapted && q + 1 == slices), b = a + kABytes;
+        if (!ok) break;
+        const uint32_t fb = bar();
+        const int k0 = q * kDeep;
+        if (lane < 2) {
+          const int m0 = t.m0 + static_cast<int>(rank) * (MODE == kMmaGated ? 64 : 128);
+          if (MODE == kMmaDx) load_3d<PAIR>(a + lane * kBox, &maps.a, m0 + lane * 64, k0, t.g, fb);
+          else if (MODE == kMmaGated) load_3d<PAIR>(a + lane * kBox, &maps.a, k0, m0 + lane * p.m, t.g, fb);
+          else load_3d<PAIR>(a + lane * kBox, &maps.a, k0, m0 + lane * 64, t.g, fb);
+        }
+        if (gather) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if ((lane + 32 * h) * 4 < half) load_rows4<PAIR>(b + (lane + 32 * h) * 512, &maps.b, k0, quad[h], fb);
+        } else if (lane < boxes) {
+          load_2d<PAIR>(b + lane * p.box_rows * 128, &maps.b, k0, jr + lane * p.box_rows, fb);
+        }
+        close();
+      }
+    }
+    // after a failure nothing consumes the stages any more: wait for the copies in flight
+    if (*failed) {
+      for (int q = 0; q < p.stages; ++q) {
+        mbar_drain(smem_u32(&c.full[s]), phase ^ 1u);
+        if (++s == p.stages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---- issuer ----------------------------------------------------------------------------------
+    int s = 0, it = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    constexpr bool kARows = MODE == kMmaDx || MODE == kMmaDw, kBRows = MODE == kMmaDw;
+    if (lane == 0) {
+      for (int64_t i = worker; i < total && ok; i += workers) {
+        const Tile t = tile_at(i);
+        if (t.k == 0) continue;  // an empty group's gradient: the epilogue writes zeros
+        const uint32_t idesc = instruction(p.bf16, kARows, kBRows, 128 * kSide, columns(t.n));
+        const uint32_t acc = tmem + (it & 1) * p.tile_n;
+        ok = mbar_wait(smem_u32(&c.acc_empty[it & 1]), ((it >> 1) & 1) ^ 1u, failed, p.err);
+        fence_after();
+        bool last = false;
+        for (bool first = true; ok && !last; first = false) {
+          ok = mbar_wait(smem_u32(&c.full[s]), phase, failed, p.err);
+          if (!ok) break;
+          fence_after();
+          last = c.last[s] != 0;
+          const uint32_t a = base + s * p.stage_bytes, b = a + kABytes;
+#pragma unroll
+          for (int q = 0; q < kDeep / 16; ++q)
+            mma<PAIR>(acc, operand(a + (kARows ? q * 2048 : q * 32), kBox), operand(b + (kBRows ? q * 2048 : q * 32), kBox),
+                      idesc, !(first && q == 0));
+          commit<PAIR>(smem_u32(&c.empty[s]));
+          if (last) commit<PAIR>(smem_u32(&c.acc_full[it & 1]));
+          if (++s == p.stages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+        ++it;
+      }
+      if (*failed) {
+        commit<false>(smem_u32(&c.drain));
+        mbar_drain(smem_u32(&c.drain), 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 2) {
+    // ---- epilogue ----------------------------------------------------------------------------------
+    const int quarter = warp & 3;  // the lanes of tensor memory that this warp can read
+    const int ml = quarter * 32 + lane;
+    int it = 0;
+    bool ok = true;
+    for (int64_t i = worker; i < total; i += workers) {
+      const Tile t = tile_at(i);
+      const bool zero = t.k == 0;
+      if (!zero) {
+        ok = mbar_wait(smem_u32(&c.acc_full[it & 1]), (it >> 1) & 1, failed, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (MODE == kMmaGated) {  // the warps meet below: they go on together or not at all
+          if (warp == 2 && lane == 0) c.go[it & 1] = ok;
+          asm volatile("bar.sync 1, %0;" ::"n"(kEpilogue) : "memory");
+          if (!c.go[it & 1]) break;
+        } else if (!ok) {
+          break;
+        }
+        fence_after();
+      }
+      const uint32_t acc = tmem + (it & 1) * p.tile_n + (static_cast<uint32_t>(quarter * 32) << 16);
+      for (int j = 0; j < t.n; j += 32) {
+        uint32_t r[32];
+        if (zero) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0u;
+        } else {
+          tmem_load32(acc + j, r);
+        }
+        const int n = min(32, t.n - j);
+        if (MODE == kMmaGated) {
+          // gate warps (lanes 0..63) finish columns 0..15, up warps (64..127) columns 16..31
+          const bool up = quarter >= 2;
+          float* mine = c.swap + quarter * 512;
+          const float* theirs = c.swap + (quarter ^ 2) * 512;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) mine[e * 32 + lane] = __uint_as_float(up ? r[e] : r[16 + e]);
+          asm volatile("bar.sync 1, %0;" ::"n"(kEpilogue) : "memory");
+          const int m = t.m0 + static_cast<int>(rank) * 64 + (quarter & 1) * 32 + lane;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int jj = j + (up ? 16 : 0) + e;
+            const float other = theirs[e * 32 + lane];
+            const float own = __uint_as_float(up ? r[16 + e] : r[e]);
+            const float h = up ? gated_silu(other, own) : gated_silu(own, other);
+            if (jj < t.n && m < p.m) {
+              const int64_t o = static_cast<int64_t>(t.j0 + jj) * p.out_stride + m;
+              if (p.out_type == SPGEMM_DTYPE_BF16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(h);
+              else static_cast<__half*>(p.out)[o] = __float2half_rn(h);
+            }
+          }
+          asm volatile("bar.sync 1, %0;" ::"n"(kEpilogue) : "memory");
+        } else {
+          const int m = t.m0 + static_cast<int>(rank) * 128 + ml;
+          int64_t o = (kDw ? t.g * p.out_group : 0) + static_cast<int64_t>(t.j0 + j) * p.out_stride + m;
+          int token = 0;
+          float f = 1.0f;
+          if (MODE == kMmaForward && p.scatter) {  // rows leave in the tokens' order
+            token = lane < n ? max(p.order[t.j0 + j + lane], 0) / p.top_k : 0;
+            if (p.scale) f = p.scale[t.g];
+          }
+          auto put = [&](auto type) {
+            using T = decltype(type);
+            T* out = static_cast<T*>(p.out);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (MODE == kMmaForward && p.scatter) {
+                const int64_t row = __shfl_sync(0xffffffffu, token, e);
+                if (e < n && m < p.m) out[row * p.out_stride + m] = from_f32<T>(f * __uint_as_float(r[e]));
+              } else {
+                if (e < n && m < p.m) out[o] = from_f32<T>(__uint_as_float(r[e]));
+                o += p.out_stride;
+              }
+            }
+          };
+          if (p.out_type == SPGEMM_DTYPE_F32) put(float());
+          else if (p.out_type == SPGEMM_DTYPE_BF16) put(__nv_bfloat16());
+          else put(__half());
+        }
+      }
+      if (!zero) {
+        fence_before();
+        if (PAIR) mbar_arrive_cluster(map_rank(smem_u32(&c.acc_empty[it & 1]), 0));
+        else mbar_arrive(smem_u32(&c.acc_empty[it & 1]));
+        ++it;
+      }
+    }
+    // rows behind the last group
+    if ((MODE == kMmaForward || MODE == kMmaGated) && !p.scatter) {
+      for (int64_t r = c.first[p.groups] + blockIdx.x; r < p.slots; r += gridDim.x)
+        for (int m = static_cast<int>(threadIdx.x) - 64; m < p.m; m += kEpilogue) {
+          const int64_t o = r * p.out_stride + m;
+          if (p.out_type == SPGEMM_DTYPE_F32) static_cast<float*>(p.out)[o] = 0.0f;
+          else static_cast<uint16_t*>(p.out)[o] = 0;
+        }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync();
+  fence_after();
+  if (warp == 1) tmem_free<PAIR>(tmem, kTmemCols);
+}
+
+namespace {
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+Encode encoder() {
+  static const Encode fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<Encode>(f);
+  }();
+  return fn;
+}
+
+// rank 2 or 3 map of 16-bit elements with 128-byte swizzle; dims[0] is contiguous
+bool encode(CUtensorMap* map, int32_t dtype, const void* data, int rank, const int64_t* dims, const int64_t* strides,
+            uint32_t box_cols, uint32_t box_rows) {
+  const Encode fn = encoder();
+  if (!fn) return false;
+  cuuint64_t d[3], st[2];
+  const cuuint32_t box[3] = {box_cols, box_rows, 1}, ones[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) d[i] = static_cast<cuuint64_t>(dims[i]);
+  for (int i = 0; i + 1 < rank; ++i) st[i] = static_cast<cuuint64_t>(strides[i]) * 2;
+  return fn(map, dtype == SPGEMM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            static_cast<cuuint32_t>(rank), const_cast<void*>(data), d, st, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+bool encode_rows(CUtensorMap* map, const spgemm_dense& m, uint32_t box_rows) {
+  const int64_t dims[2] = {m.cols, m.rows}, strides[1] = {m.stride};
+  return encode(map, m.dtype, m.data, 2, dims, strides, kDeep, box_rows);
+}
+bool encode_weights(CUtensorMap* map, const spgemm_weights& w) {
+  // a single group may carry any group stride: a map wants a multiple of 16 bytes
+  const int64_t dims[3] = {w.cols, w.rows, w.groups};
+  const int64_t strides[2] = {w.row_stride, w.groups > 1 ? w.group_stride : w.row_stride * w.rows};
+  return encode(map, w.dtype, w.data, 3, dims, strides, kDeep, 64);
+}
+
+int sm_count() {
+  int dev = 0, sms = 1;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+template <int MODE, bool PAIR>
+bool launch(const MmaMaps& maps, MmaArgs a, cudaStream_t s) {
+  a.stage_bytes = kABytes + std::max(a.tile_n / (PAIR ? 2 : 1), MODE == kMmaDw ? 64 : 16) * 128;
+  const int control = static_cast<int>(sizeof(Control));
+  a.stages = std::min<int>(kMaxStages, (kSmemMost - 1024 - control) / a.stage_bytes);
+  const int smem = 1024 + a.stages * a.stage_bytes + control;
+  auto kern = k_group_mma<MODE, PAIR>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(sm_count() / 2 * 2));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {PAIR ? 2u : 1u, 1u, 1u};
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kern, maps, a) == cudaSuccess;
+}
+
+// N-side tile: a power of two of about twice the average group, so that most groups are one tile
+int pick_tile(int64_t slots, int64_t groups, int most) {
+  int n = 16;
+  while (n < most && n < 2 * slots / groups) n *= 2;
+  return n;
+}
+
+MmaArgs base_args(const spgemm_grouping& g, int32_t dtype) {
+  MmaArgs a = {};
+  a.offsets = g.offsets;
+  a.order = g.order;
+  a.slots = static_cast<int>(g.slots);
+  a.groups = g.groups;
+  a.top_k = g.top_k;
+  a.bf16 = dtype == SPGEMM_DTYPE_BF16;
+  a.err = grouped_err();
+  return a;
+}
+
+bool aligned(const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0; }
+
+}  // namespace
+
+bool mma_takes(const spgemm_dense& m) { return m.dtype != SPGEMM_DTYPE_F32 && aligned(m.data, m.stride) && m.rows < (1LL << 31) && m.cols < (1LL << 31); }
+bool mma_takes(const spgemm_weights& w) {
+  return w.dtype != SPGEMM_DTYPE_F32 && aligned(w.data, w.row_stride) && (w.groups == 1 || (w.group_stride > 0 && w.group_stride % 8 == 0)) &&
+         w.rows < (1LL << 30) && w.cols < (1LL << 30);
+}
+
+bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool gather, const spgemm_weights& w,
+                        bool gated, const spgemm_dense& y, cudaStream_t s) {
+  if (g.slots == 0) return true;
+  MmaArgs a = base_args(g, x.dtype);
+  a.rows = static_cast<int>(x.rows);
+  a.gather = gather;
+  a.m = static_cast<int>(y.cols);
+  a.depth = static_cast<int>(x.cols);
+  a.tile_n = pick_tile(g.slots, g.groups, 256);
+  a.box_rows = std::min(a.tile_n, 64);
+  a.out = y.data;
+  a.out_stride = y.stride;
+  a.out_type = y.dtype;
+  MmaMaps maps;
+  if (!encode_weights(&maps.a, w) || !encode_rows(&maps.b, x, gather ? 1 : a.box_rows)) return false;
+  maps.c = maps.d = maps.b;
+  return gated ? launch<kMmaGated, false>(maps, a, s) : launch<kMmaForward, false>(maps, a, s);
+}
+
+bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_weights& w, float* dx,
+                   cudaStream_t s) {
+  if (g.slots == 0) return true;
+  MmaArgs a = base_args(g, dy.dtype);
+  a.rows = static_cast<int>(dy.rows);
+  a.m = static_cast<int>(w.cols);
+  a.depth = static_cast<int>(w.rows);
+  a.tile_n = pick_tile(g.slots, g.groups, 256);
+  a.box_rows = std::min(a.tile_n, 64);
+  a.out = dx;
+  a.out_stride = w.cols;
+  a.out_type = SPGEMM_DTYPE_F32;
+  MmaMaps maps;
+  if (!encode_weights(&maps.a, w) || !encode_rows(&maps.b, dy, a.box_rows)) return false;
+  maps.c = maps.d = maps.b;
+  return launch<kMmaDx, false>(maps, a, s);
+}
+
+bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_dense& x, const spgemm_weights& dw,
+                   cudaStream_t s) {
+  MmaArgs a = base_args(g, x.dtype);
+  a.rows = static_cast<int>(x.rows);
+  a.m = static_cast<int>(dw.cols);
+  a.n = static_cast<int>(dw.rows);
+  a.tile_n = dw.rows > 128 ? 256 : dw.rows > 64 ? 128 : 64;
+  a.out = dw.data;
+  a.out_stride = dw.row_stride;
+  a.out_group = dw.group_stride;
+  a.out_type = dw.dtype;
+  MmaMaps maps;
+  if (!encode_rows(&maps.a, x, 1) || !encode_rows(&maps.b, dy, 64) || !encode_rows(&maps.c, dy, 1)) return false;
+  maps.d = maps.a;
+  return launch<kMmaDw, false>(maps, a, s);
+}
+
+}  // namespace sg
