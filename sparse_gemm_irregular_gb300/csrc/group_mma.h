@@ -21,6 +21,8 @@ struct MmaArgs {
   int64_t out_stride, out_group;
   int out_type;
   const float* scale;      // per group (scatter)
+  const int32_t* ids;      // Adapted: the adapter of each row
+  int adapters, rank;
   uint32_t* err;
 };
 
@@ -36,5 +38,11 @@ bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
                    cudaStream_t s);
 bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_dense& x, const spgemm_weights& dw,
                    cudaStream_t s);
+// v[t, :] = scale[i] * x[t] * a[i]^T, rounded to x's type, for the rows of every adapter i
+bool launch_mma_shrink(const spgemm_grouping& g, const spgemm_dense& x, const spgemm_weights& a, const float* scale,
+                       const spgemm_dense& v, cudaStream_t s);
+// y[t, :] = x[t] * w^T + v[t] * b[ids[t]]^T
+bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spgemm_weights& b, const int32_t* ids,
+                        const spgemm_dense& v, const spgemm_dense& y, cudaStream_t s);
 
 }  // namespace sg

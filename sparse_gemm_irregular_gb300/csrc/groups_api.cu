@@ -297,18 +297,26 @@ int spgemm_adapted_product(const spgemm_dense* x, const spgemm_dense* w, const s
   int32_t* order = static_cast<int32_t*>(scratch.get(4 * t));
   int32_t* position = static_cast<int32_t*>(scratch.get(4 * t));
   void* ws = scratch.get(group_scratch_bytes(t, adapters));
-  const spgemm_dense v = dense(scratch.get(4 * t * rank), t, rank, SPGEMM_DTYPE_F32);
-  const spgemm_dense base = dense(scratch.get(4 * t * y->cols), t, y->cols, SPGEMM_DTYPE_F32);
-  int32_t* one = static_cast<int32_t*>(scratch.get(8));
-  if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
-  launch_group_rows(ids, t, adapters, offsets, order, position, ws, st);
   const spgemm_grouping g{t, 1, adapters, offsets, order, position};
-  launch_plain_forward(g, *x, true, *a, v, st);
-  const int32_t all[2] = {0, static_cast<int32_t>(t)};
-  SG_TRY(check_cuda(cudaMemcpyAsync(one, all, sizeof(all), cudaMemcpyHostToDevice, st), "adapted product"));
-  const spgemm_weights shared{w->data, 1, w->rows, w->cols, 0, w->stride, w->dtype, 0};
-  launch_plain_forward(spgemm_grouping{t, 1, 1, one, nullptr, nullptr}, *x, false, shared, base, st);
-  launch_plain_adapter_add(g, ids, scale, static_cast<float*>(base.data), static_cast<float*>(v.data), rank, *b, *y, st);
+  const spgemm_dense v16{nullptr, t, rank, ceil_div(rank, 8) * 8, x->dtype, 0};
+  if (mma_takes(*x) && mma_takes(*w) && mma_takes(*a) && mma_takes(*b) && mma_takes(v16)) {
+    spgemm_dense v = v16;
+    v.data = scratch.get(2 * t * v.stride);
+    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
+    launch_group_rows(ids, t, adapters, offsets, order, position, ws, st);
+    if (!launch_mma_shrink(g, *x, *a, scale, v, st) || !launch_mma_adapted(*x, *w, *b, ids, v, *y, st))
+      return launch_failed("adapted product");
+  } else {
+    const spgemm_dense v = dense(scratch.get(4 * t * rank), t, rank, SPGEMM_DTYPE_F32);
+    const spgemm_dense base = dense(scratch.get(4 * t * y->cols), t, y->cols, SPGEMM_DTYPE_F32);
+    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
+    launch_group_rows(ids, t, adapters, offsets, order, position, ws, st);
+    launch_plain_forward(g, *x, true, *a, v, st);
+    const spgemm_weights shared{w->data, 1, w->rows, w->cols, 0, w->stride, w->dtype, 0};
+    launch_plain_forward(spgemm_grouping{t, 1, 1, nullptr, nullptr, nullptr}, *x, false, shared, base, st);
+    launch_plain_adapter_add(g, ids, scale, static_cast<float*>(base.data), static_cast<float*>(v.data), rank, *b, *y,
+                             st);
+  }
   return check_cuda(cudaGetLastError(), "adapted product");
 }
 

@@ -250,8 +250,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
       const bool gather = (MODE == kMmaForward || MODE == kMmaGated) && p.gather;
       const uint32_t bytes = kABytes + (gather ? half : boxes * p.box_rows) * 128;
       const int slices = (t.k + kDeep - 1) / kDeep;
+      // Adapted: the adapters of the tile's tokens (lane, lane + 32, ...), in ascending order
+      int ids[8];
+      auto id_of = [&](int j) {
+        const int id = j < t.j0 + t.n ? p.ids[j] : -1;
+        return id >= 0 && id < p.adapters ? id : -1;
+      };
+      auto following = [&](int before) {
+        uint32_t least = 0xffffffffu;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (ids[e] > before) least = min(least, static_cast<uint32_t>(ids[e]));
+        return static_cast<int>(__reduce_min_sync(0xffffffffu, least));  // -1: none left
+      };
+      int adapter = -1;
+      if (MODE == kMmaAdapted) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ids[e] = lane + 32 * e < t.n ? id_of(t.j0 + lane + 32 * e) : -1;
+        adapter = following(-1);
+      }
       for (int q = 0; q < slices && ok; ++q) {
-        const uint32_t a = open(bytes, MODE != kMmaAdapted && q + 1 == slices), b = a + kABytes;
+        const uint32_t a = open(bytes, q + 1 == slices && adapter < 0), b = a + kABytes;
         if (!ok) break;
         const uint32_t fb = bar();
         const int k0 = q * kDeep;
@@ -269,6 +288,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
           load_2d<PAIR>(b + lane * p.box_rows * 128, &maps.b, k0, jr + lane * p.box_rows, fb);
         }
         close();
+      }
+      // then, per adapter, its b against the v rows of its own tokens (the others' read as zeros)
+      while (MODE == kMmaAdapted && ok && adapter >= 0) {
+        const int after = following(adapter);
+        int4 rows[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          int r[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = jr + (lane + 32 * h) * 4 + e;
+            r[e] = id_of(j) == adapter ? j : p.rows;
+          }
+          rows[h] = make_int4(r[0], r[1], r[2], r[3]);
+        }
+        for (int k0 = 0; k0 < p.rank && ok; k0 += kDeep) {
+          const uint32_t a = open(kABytes + half * 128, k0 + kDeep >= p.rank && after < 0), b = a + kABytes;
+          if (!ok) break;
+          const uint32_t fb = bar();
+          if (lane < 2)
+            load_3d<PAIR>(a + lane * kBox, &maps.c, k0, t.m0 + static_cast<int>(rank) * 128 + lane * 64, adapter, fb);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if ((lane + 32 * h) * 4 < half) load_rows4<PAIR>(b + (lane + 32 * h) * 512, &maps.d, k0, rows[h], fb);
+          close();
+        }
+        adapter = after;
       }
     }
     // after a failure nothing consumes the stages any more: wait for the copies in flight
@@ -582,6 +628,47 @@ bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
   if (!encode_rows(&maps.a, x, 1) || !encode_rows(&maps.b, dy, 64) || !encode_rows(&maps.c, dy, 1)) return false;
   maps.d = maps.a;
   return launch<kMmaDw, false>(maps, a, s);
+}
+
+bool launch_mma_shrink(const spgemm_grouping& g, const spgemm_dense& x, const spgemm_weights& a_w, const float* scale,
+                       const spgemm_dense& v, cudaStream_t s) {
+  MmaArgs a = base_args(g, x.dtype);
+  a.rows = static_cast<int>(x.rows);
+  a.gather = a.scatter = 1;
+  a.m = static_cast<int>(v.cols);
+  a.depth = static_cast<int>(x.cols);
+  a.tile_n = 32;
+  a.box_rows = 32;
+  a.out = v.data;
+  a.out_stride = v.stride;
+  a.out_type = v.dtype;
+  a.scale = scale;
+  MmaMaps maps;
+  if (!encode_weights(&maps.a, a_w) || !encode_rows(&maps.b, x, 1)) return false;
+  maps.c = maps.d = maps.b;
+  return launch<kMmaForward, false>(maps, a, s);
+}
+
+bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spgemm_weights& b, const int32_t* ids,
+                        const spgemm_dense& v, const spgemm_dense& y, cudaStream_t s) {
+  MmaArgs a = base_args(spgemm_grouping{x.rows, 1, 1, nullptr, nullptr, nullptr}, x.dtype);
+  a.rows = static_cast<int>(x.rows);
+  a.ids = ids;
+  a.adapters = static_cast<int>(b.groups);
+  a.rank = static_cast<int>(b.cols);
+  a.m = static_cast<int>(y.cols);
+  a.depth = static_cast<int>(x.cols);
+  a.tile_n = pick_tile(x.rows, 2, 256);
+  a.box_rows = std::min(a.tile_n, 64);
+  a.out = y.data;
+  a.out_stride = y.stride;
+  a.out_type = y.dtype;
+  const spgemm_weights shared{w.data, 1, w.rows, w.cols, 0, w.stride, w.dtype, 0};
+  MmaMaps maps;
+  if (!encode_weights(&maps.a, shared) || !encode_rows(&maps.b, x, a.box_rows) || !encode_weights(&maps.c, b) ||
+      !encode_rows(&maps.d, v, 1))
+    return false;
+  return launch<kMmaAdapted, false>(maps, a, s);
 }
 
 }  // namespace sg

@@ -33,7 +33,9 @@ struct Rows {           // the rows of an operand: x by token, or a matrix by po
 };
 
 // Offsets as they are used: inside [0, slots] and not decreasing, whatever the array holds.
+// No array: one group of all positions.
 __device__ __forceinline__ int64_t clamped(const int32_t* offsets, int g, int64_t slots) {
+  if (!offsets) return g == 0 ? 0 : slots;
   return min(max(static_cast<int64_t>(offsets[g]), int64_t(0)), slots);
 }
 
