@@ -30,12 +30,16 @@ struct MmaArgs {
 bool mma_takes(const spgemm_dense& m);
 bool mma_takes(const spgemm_weights& w);
 
+// whether so few rows per group are expected that gathering copies keep up with the weights
+bool mma_gathers(const spgemm_grouping& g);
+
 // The same contracts as the launch_plain_* functions; false: the launch failed (cudaGetLastError
 // or the encoding of a copy descriptor).
 bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool gather, const spgemm_weights& w,
                         bool gated, const spgemm_dense& y, cudaStream_t s);
 bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_weights& w, float* dx,
                    cudaStream_t s);
+// x with one row per position here
 bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_dense& x, const spgemm_weights& dw,
                    cudaStream_t s);
 // v[t, :] = scale[i] * x[t] * a[i]^T, rounded to x's type, for the rows of every adapter i

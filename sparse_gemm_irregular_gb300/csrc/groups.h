@@ -62,6 +62,10 @@ void launch_combine(const spgemm_grouping& g, const float* weights, const spgemm
 void launch_combine_backward(const spgemm_grouping& g, const float* weights, const spgemm_dense& dout,
                              const spgemm_dense& y, const spgemm_dense& dy, float* dweights, cudaStream_t s);
 
+// out[position of slot] = x[slot's token] for every slot with a group (16-bit, 16-byte aligned rows);
+// rows of out behind the last group are not written
+void launch_spread_rows(const spgemm_grouping& g, const spgemm_dense& x, const spgemm_dense& out, cudaStream_t s);
+
 // ---- grouped products on CUDA cores, any type, stride and alignment (k_group_plain.cu) --------
 // y[p, :] = x[row(p), :] * w[g]^T for every position p of group g; row(p) = order[p] / top_k when
 // gather, else p; rows of y past the last group are set to zero.  y may be 32-bit.

@@ -108,6 +108,22 @@ spgemm_dense dense(void* data, int64_t rows, int64_t cols, int32_t dtype) {
   return spgemm_dense{data, rows, cols, cols, dtype, 0};
 }
 
+// x laid out in group order (scratch), its rows padded to 16 bytes
+spgemm_dense spread(const spgemm_grouping& g, const spgemm_dense& x, Scratch* scratch, cudaStream_t s) {
+  const int64_t stride = ceil_div(x.cols, 8) * 8;
+  const spgemm_dense rows{scratch->get(2 * g.slots * stride), g.slots, x.cols, stride, x.dtype, 0};
+  if (rows.data) launch_spread_rows(g, x, rows, s);
+  return rows;
+}
+
+// y = rows * w[g]^T on the tensor cores with x by token or by position
+bool mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool by_token, const spgemm_weights& w, bool gated,
+                 const spgemm_dense& y, Scratch* scratch, cudaStream_t s) {
+  if (!by_token || mma_gathers(g)) return launch_mma_forward(g, x, by_token, w, gated, y, s);
+  const spgemm_dense rows = spread(g, x, scratch, s);
+  return rows.data && launch_mma_forward(g, rows, false, w, gated, y, s);
+}
+
 }  // namespace
 }  // namespace sg
 
@@ -176,7 +192,9 @@ int spgemm_grouped_product(const spgemm_grouping* g, const spgemm_dense* x, int3
     return bad("grouped product: types differ");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (mma_takes(*x) && mma_takes(*w)) {
-    if (!launch_mma_forward(*g, *x, !x_grouped, *w, false, *y, st)) return launch_failed("grouped product");
+    Scratch scratch(st);
+    if (!mma_forward(*g, *x, !x_grouped, *w, false, *y, &scratch, st))
+      return scratch.ok() ? launch_failed("grouped product") : SPGEMM_ERR_OUT_OF_MEMORY;
   } else {
     launch_plain_forward(*g, *x, !x_grouped, *w, *y, st);
   }
@@ -209,8 +227,13 @@ int spgemm_grouped_product_backward(const spgemm_grouping* g, const spgemm_dense
     else if (!launch_mma_dx(*g, *dy, *w, r, st)) return launch_failed("grouped product backward");
     launch_combine(*g, nullptr, rows, *dx, st);
   }
-  if (dw && !mma) launch_plain_dw(*g, *dy, *x, *dw, st);
-  else if (dw && !launch_mma_dw(*g, *dy, *x, *dw, st)) return launch_failed("grouped product backward");
+  if (dw && !mma) {
+    launch_plain_dw(*g, *dy, *x, *dw, st);
+  } else if (dw) {
+    const spgemm_dense rows = spread(*g, *x, &scratch, st);
+    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
+    if (!launch_mma_dw(*g, *dy, rows, *dw, st)) return launch_failed("grouped product backward");
+  }
   return check_cuda(cudaGetLastError(), "grouped product backward");
 }
 
@@ -258,8 +281,9 @@ int spgemm_experts(const spgemm_grouping* g, const float* weights, const spgemm_
   const spgemm_dense y = dense(scratch.get(4 * g->slots * out->cols), g->slots, out->cols, SPGEMM_DTYPE_F32);
   if (mma_takes(*x) && mma_takes(*w_up) && mma_takes(h) && mma_takes(*w_down)) {
     if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
-    if (!launch_mma_forward(*g, *x, true, *w_up, true, h, st) || !launch_mma_forward(*g, h, false, *w_down, false, y, st))
-      return launch_failed("experts");
+    if (!mma_forward(*g, *x, true, *w_up, true, h, &scratch, st) ||
+        !mma_forward(*g, h, false, *w_down, false, y, &scratch, st))
+      return scratch.ok() ? launch_failed("experts") : SPGEMM_ERR_OUT_OF_MEMORY;
   } else {
     const spgemm_dense pre = dense(scratch.get(8 * g->slots * hidden), g->slots, 2 * hidden, SPGEMM_DTYPE_F32);
     if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;

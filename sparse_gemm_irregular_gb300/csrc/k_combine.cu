@@ -57,6 +57,21 @@ __global__ void __launch_bounds__(kThreads) k_combine(const int32_t* __restrict_
   }
 }
 
+// One thread per 16 bytes of a token's row: read once, written to each of its positions.
+__global__ void __launch_bounds__(kThreads) k_spread_rows(const int32_t* __restrict__ position, int64_t tokens, int top_k,
+                                                          int64_t slots, const uint4* __restrict__ x, int64_t x_stride,
+                                                          uint4* __restrict__ out, int64_t out_stride, int per) {
+  const int c = blockIdx.y * kThreads + threadIdx.x;
+  if (c >= per) return;
+  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+    const uint4 v = x[t * x_stride + c];
+    for (int j = 0; j < top_k; ++j) {
+      const int64_t p = position[t * top_k + j];
+      if (p >= 0 && p < slots) out[p * out_stride + c] = v;
+    }
+  }
+}
+
 // One block per token: the row of dout is read once per slot from L1.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) k_combine_backward(
@@ -121,6 +136,15 @@ void launch_combine(const spgemm_grouping& g, const float* weights, const spgemm
       else go(std::integral_constant<int, 1>());
     });
   });
+}
+
+void launch_spread_rows(const spgemm_grouping& g, const spgemm_dense& x, const spgemm_dense& out, cudaStream_t s) {
+  if (g.slots == 0) return;
+  const int per = static_cast<int>(ceil_div(x.cols, 8));  // strides are multiples of 8: a row's last 16 bytes are its own
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(x.rows, 1 << 20)), static_cast<unsigned>(ceil_div(per, kThreads)));
+  note_launch();
+  k_spread_rows<<<grid, kThreads, 0, s>>>(g.position, x.rows, g.top_k, g.slots, static_cast<const uint4*>(x.data),
+                                          x.stride / 8, static_cast<uint4*>(out.data), out.stride / 8, per);
 }
 
 void launch_combine_backward(const spgemm_grouping& g, const float* weights, const spgemm_dense& dout,

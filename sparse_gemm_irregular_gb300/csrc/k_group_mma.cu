@@ -9,14 +9,18 @@
 //   Forward   w[g] rows                       x rows, gathered or in order     columns of x
 //   Gated     64 gate rows + 64 up rows       x rows, gathered                 columns of x
 //   Dx        w[g]^T (columns of w[g])        dy rows                          rows of w[g]
-//   Dw        x^T (columns of gathered x)     dy^T (columns of dy)             the group's positions
+//   Dw        x^T (columns of x, in order)    dy^T (columns of dy)             the group's positions
 //   Adapted   w rows, then b[i] rows          x rows, then v rows of adapter i columns of x, then rank
 //
-// Operands go to shared memory in 64-deep slices by bulk copies: 128-byte swizzled boxes, rows of x
-// picked by gathering copies straight from the routing's order (no permuted copy of x exists).  A
-// gathered row index past the matrix reads as zeros: that masks the positions behind a group's end (Dw,
-// where they are contracted, on both operands, so that a NaN there cannot leak) and, in Adapted, the
-// tokens of other adapters.
+// Operands go to shared memory in 64-deep slices by bulk copies: 128-byte swizzled boxes.  Rows in
+// any order come by gathering copies, four rows each.  These take about 40 cycles per four rows of a
+// slice where the matrix instruction takes 8, so they serve what is bound by the weights (up to
+// mma_gathers() rows per group, straight from the routing's order) and the ends of groups; for more rows x is
+// laid out in group order first (k_spread_rows).  Measured at 65536 rows, 2048 x 2048: 2.13 ms gathering
+// throughout, 0.41 ms from ordered rows, 0.06 ms to order them.
+// A gathered row index past the matrix reads as zeros: that masks the positions behind a group's
+// end (Dw, where they are contracted, on both operands, so that a NaN there cannot leak) and, in Adapted,
+// the tokens of other adapters.
 //
 // Six warps: a producer (copies), an issuer (matrix instructions, one thread), four that empty
 // the accumulators while the next tile is computed into the other half of tensor memory.  The
@@ -67,7 +71,7 @@ struct Tile {
 }  // namespace
 
 struct MmaMaps {
-  CUtensorMap a, b, c, d;  // Forward: w, x; Dw: gathered x, dy boxes, gathered dy; Adapted: w, x, b[i], gathered v
+  CUtensorMap a, b, c, d;  // Forward, Dx: weights, rows; Dw: x, dy, then rows of dy and of x; Adapted: w, x, b[i], v rows
 };
 
 template <int MODE, bool PAIR>
@@ -208,38 +212,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
       if (kDw) {
         const int slices = (t.k + kDeep - 1) / kDeep;
         const int nb = (half + 63) / 64;  // 64-column blocks of dy
-        int next[4];                      // order entries of this lane's quad in the next slice
-        auto fetch = [&](int k0) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int q = k0 + (lane & 15) * 4 + e;
-            const int slot = q < t.k ? p.order[t.k0 + q] : -1;
-            next[e] = slot >= 0 ? min(slot / p.top_k, p.rows) : p.rows;
-          }
-        };
-        fetch(0);
         for (int q = 0; q < slices && ok; ++q) {
-          const int4 mine = make_int4(next[0], next[1], next[2], next[3]);
-          if (q + 1 < slices) fetch((q + 1) * kDeep);
           const uint32_t a = open(static_cast<uint32_t>((2 + nb) * kBox), q + 1 == slices), b = a + kABytes;
           if (!ok) break;
           const uint32_t fb = bar();
-          const int m0 = t.m0 + static_cast<int>(rank) * 128;
-          // x: 2 blocks of 64 columns, 16 quads of rows each: one quad per lane
-          load_rows4<PAIR>(a + (lane >> 4) * kBox + (lane & 15) * 512, &maps.a, m0 + (lane >> 4) * 64, mine, fb);
-          const int k0 = q * kDeep;
+          const int m0 = t.m0 + static_cast<int>(rank) * 128, k0 = q * kDeep;
           if (k0 + kDeep <= t.k) {
-            if (lane < nb) load_2d<PAIR>(b + lane * kBox, &maps.b, jr + lane * 64, t.k0 + k0, fb);
-          } else {  // the group ends inside the slice: dy's rows past it read as zeros too
+            if (lane < 2) load_2d<PAIR>(a + lane * kBox, &maps.a, m0 + lane * 64, t.k0 + k0, fb);
+            else if (lane - 2 < nb) load_2d<PAIR>(b + (lane - 2) * kBox, &maps.b, jr + (lane - 2) * 64, t.k0 + k0, fb);
+          } else {  // the group ends inside the slice: rows past it read as zeros, on both sides
             int r[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int o = k0 + (lane & 15) * 4 + e;
               r[e] = o < t.k ? t.k0 + o : p.slots;
             }
+            const int4 rows = make_int4(r[0], r[1], r[2], r[3]);
+            const uint32_t in_box = (lane & 15) * 512;
+            load_rows4<PAIR>(a + (lane >> 4) * kBox + in_box, &maps.d, m0 + (lane >> 4) * 64, rows, fb);
             for (int blk = lane >> 4; blk < nb; blk += 2)
-              load_rows4<PAIR>(b + blk * kBox + (lane & 15) * 512, &maps.c, jr + blk * 64,
-                               make_int4(r[0], r[1], r[2], r[3]), fb);
+              load_rows4<PAIR>(b + blk * kBox + in_box, &maps.c, jr + blk * 64, rows, fb);
           }
           close();
         }
@@ -570,6 +562,8 @@ bool aligned(const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>
 
 }  // namespace
 
+bool mma_gathers(const spgemm_grouping& g) { return pick_tile(g.slots, g.groups, 256) <= 32; }
+
 bool mma_takes(const spgemm_dense& m) { return m.dtype != SPGEMM_DTYPE_F32 && aligned(m.data, m.stride) && m.rows < (1LL << 31) && m.cols < (1LL << 31); }
 bool mma_takes(const spgemm_weights& w) {
   return w.dtype != SPGEMM_DTYPE_F32 && aligned(w.data, w.row_stride) && (w.groups == 1 || (w.group_stride > 0 && w.group_stride % 8 == 0)) &&
@@ -616,7 +610,6 @@ bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
 bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_dense& x, const spgemm_weights& dw,
                    cudaStream_t s) {
   MmaArgs a = base_args(g, x.dtype);
-  a.rows = static_cast<int>(x.rows);
   a.m = static_cast<int>(dw.cols);
   a.n = static_cast<int>(dw.rows);
   a.tile_n = dw.rows > 128 ? 256 : dw.rows > 64 ? 128 : 64;
@@ -625,8 +618,9 @@ bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
   a.out_group = dw.group_stride;
   a.out_type = dw.dtype;
   MmaMaps maps;
-  if (!encode_rows(&maps.a, x, 1) || !encode_rows(&maps.b, dy, 64) || !encode_rows(&maps.c, dy, 1)) return false;
-  maps.d = maps.a;
+  if (!encode_rows(&maps.a, x, 64) || !encode_rows(&maps.b, dy, 64) || !encode_rows(&maps.c, dy, 1) ||
+      !encode_rows(&maps.d, x, 1))
+    return false;
   return launch<kMmaDw, false>(maps, a, s);
 }
 
