@@ -30,6 +30,29 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 // silu(g) * u in 32 bits.  exp overflows to +inf for g below -88: g / inf = -0, the limit.
 __device__ __forceinline__ float gated_silu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
+// Launches of one call follow each other without a gap: a kernel may be started while the one before it
+// ends.  Every kernel launched this way calls pdl_wait before its first access to global memory (it
+// returns when everything before it on the stream is complete and visible), and pdl_go once to let
+// the next one start.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline bool launch_next(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess;
+}
+
 inline int dtype_size(int32_t d) { return d == SPGEMM_DTYPE_F32 ? 4 : 2; }
 
 template <typename F>

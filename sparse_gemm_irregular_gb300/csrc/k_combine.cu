@@ -34,6 +34,8 @@ __global__ void __launch_bounds__(kThreads) k_combine(const int32_t* __restrict_
                                                       int64_t slots, const float* __restrict__ weights,
                                                       const TY* __restrict__ y, int64_t y_stride, TO* __restrict__ out,
                                                       int64_t out_stride, int64_t cols) {
+  pdl_wait();
+  pdl_go();
   const int64_t per = cols / V;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < tokens * per;
        i += static_cast<int64_t>(gridDim.x) * kThreads) {
@@ -61,6 +63,8 @@ __global__ void __launch_bounds__(kThreads) k_combine(const int32_t* __restrict_
 __global__ void __launch_bounds__(kThreads) k_spread_rows(const int32_t* __restrict__ position, int64_t tokens, int top_k,
                                                           int64_t slots, const uint4* __restrict__ x, int64_t x_stride,
                                                           uint4* __restrict__ out, int64_t out_stride, int per) {
+  pdl_wait();
+  pdl_go();
   const int c = blockIdx.y * kThreads + threadIdx.x;
   if (c >= per) return;
   for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
@@ -80,6 +84,8 @@ __global__ void __launch_bounds__(kThreads) k_combine_backward(
     const T* __restrict__ y, int64_t y_stride, T* __restrict__ dy, int64_t dy_stride, float* __restrict__ dweights,
     int64_t cols) {
   __shared__ float s_part[kThreads / 32];
+  pdl_wait();
+  pdl_go();
   for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
     for (int j = 0; j < top_k; ++j) {
       const int64_t p = position[t * top_k + j];
@@ -126,10 +132,8 @@ void launch_combine(const spgemm_grouping& g, const float* weights, const spgemm
       auto go = [&](auto v) {
         constexpr int V = decltype(v)::value;
         const int64_t blocks = std::min<int64_t>(ceil_div(tokens * (out.cols / V), kThreads), 1 << 20);
-        note_launch();
-        k_combine<TY, TO, V><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
-            g.position, tokens, g.top_k, g.slots, weights, static_cast<const TY*>(y.data), y.stride,
-            static_cast<TO*>(out.data), out.stride, out.cols);
+        launch_next(k_combine<TY, TO, V>, static_cast<unsigned>(blocks), kThreads, 0, s, g.position, tokens, g.top_k, g.slots,
+                    weights, static_cast<const TY*>(y.data), y.stride, static_cast<TO*>(out.data), out.stride, out.cols);
       };
       constexpr int W = 16 / (sizeof(TY) > sizeof(TO) ? sizeof(TY) : sizeof(TO));
       if (packs<TY>(y, W) && packs<TO>(out, W)) go(std::integral_constant<int, W>());
@@ -142,9 +146,8 @@ void launch_spread_rows(const spgemm_grouping& g, const spgemm_dense& x, const s
   if (g.slots == 0) return;
   const int per = static_cast<int>(ceil_div(x.cols, 8));  // strides are multiples of 8: a row's last 16 bytes are its own
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(x.rows, 1 << 20)), static_cast<unsigned>(ceil_div(per, kThreads)));
-  note_launch();
-  k_spread_rows<<<grid, kThreads, 0, s>>>(g.position, x.rows, g.top_k, g.slots, static_cast<const uint4*>(x.data),
-                                          x.stride / 8, static_cast<uint4*>(out.data), out.stride / 8, per);
+  launch_next(k_spread_rows, grid, kThreads, 0, s, g.position, x.rows, g.top_k, g.slots, static_cast<const uint4*>(x.data),
+              x.stride / 8, static_cast<uint4*>(out.data), out.stride / 8, per);
 }
 
 void launch_combine_backward(const spgemm_grouping& g, const float* weights, const spgemm_dense& dout,
@@ -155,11 +158,10 @@ void launch_combine_backward(const spgemm_grouping& g, const float* weights, con
     using T = decltype(ty);
     auto go = [&](auto v) {
       constexpr int V = decltype(v)::value;
-      note_launch();
-      k_combine_backward<T, V><<<static_cast<unsigned>(std::min<int64_t>(tokens, 1 << 20)), kThreads, 0, s>>>(
-          g.offsets, g.groups, g.position, tokens, g.top_k, g.slots, weights, static_cast<const T*>(dout.data),
-          dout.stride, static_cast<const T*>(y.data), y.stride, static_cast<T*>(dy.data), dy.stride, dweights,
-          dout.cols);
+      launch_next(k_combine_backward<T, V>, static_cast<unsigned>(std::min<int64_t>(tokens, 1 << 20)), kThreads, 0, s,
+                  g.offsets, g.groups, g.position, tokens, g.top_k, g.slots, weights, static_cast<const T*>(dout.data),
+                  dout.stride, static_cast<const T*>(y.data), y.stride, static_cast<T*>(dy.data), dy.stride, dweights,
+                  dout.cols);
     };
     constexpr int W = 16 / sizeof(T);
     if (packs<T>(dout, W) && packs<T>(y, W) && packs<T>(dy, W)) go(std::integral_constant<int, W>());

@@ -102,6 +102,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<PAIR>(smem_u32(&c.tmem), kTmemCols);
+  pdl_wait();
+  pdl_go();
   // offsets are used as a non-decreasing sequence inside [0, slots], whatever the array holds
   {
     int run = 0, top = 0;
@@ -530,11 +532,13 @@ bool launch(const MmaMaps& maps, MmaArgs a, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {PAIR ? 2u : 1u, 1u, 1u};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {PAIR ? 2u : 1u, 1u, 1u};
   cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 1 : 0;
+  cfg.numAttrs = PAIR ? 2 : 1;
   note_launch();
   return cudaLaunchKernelEx(&cfg, kern, maps, a) == cudaSuccess;
 }

@@ -6,17 +6,19 @@
 //   rise with l, so comparing l is the same choice without its rounding);  the k largest c among
 //   the kept expert groups;  w = s / sum of the chosen s * scale.
 //
-// One warp per token: lane i holds experts i, i + 32, ... in registers, so a row is read once,
-// coalesced, and softmax, group scores and the k rounds of "largest remaining" are warp
-// reductions.  A float is compared through an integer with the same order, which makes each
-// round two warp-wide integer reductions (largest key, then lowest index that has it).
-// The chosen experts leave in ascending order for free: ballots over the register index.
+// L lanes hold a token's row, V consecutive experts each (8 lanes x 8 up to 64 experts, 16 x 8, 32 x 8,
+// then 32 x 16 and 32 x 32): a row is read once in 16-byte pieces, and a warp works on 32 / L tokens at
+// once, which is what a router is bound by: instructions, not bytes.  A float is compared through an
+// integer with the same order; each round of "largest remaining" is a maximum over the L lanes and a
+// ballot, whose lowest set bit is the lowest index because lanes hold consecutive experts.  For the same
+// reason the chosen experts leave in ascending order after one prefix sum of their counts.
 //
 // The transpose is a stable counting sort.  Each warp owns consecutive tokens and counts per
-// expert in its own row of shared memory; the count before the increment is the slot's rank in
-// the warp (the experts of one token differ, so no two lanes meet).  The block adds its warps up
-// and writes its counts; k_block_offsets scans them over the blocks, k_group_scatter over the experts.
-// Sums of ranks and scans are integers: the result does not depend on the order of the blocks.
+// expert in its own row of shared memory; the count before a slot plus the earlier tokens of the
+// same step (a ballot over the lanes that hold the same expert) is its rank in the warp.  The block adds its
+// warps up and writes its counts; k_block_offsets scans them over the blocks, k_group_scatter
+// over the experts.  Few tokens (one block's worth) finish in the first kernel.
+// Ranks and scans are integers: the result does not depend on the order of the blocks.
 #include <algorithm>
 
 #include "groups.h"
@@ -25,9 +27,11 @@ namespace sg {
 
 namespace {
 
-constexpr int kWarps = 8;              // warps of a block
-constexpr int kTokensPerWarp = 8;      // consecutive tokens of a warp (route)
-constexpr int kSlotsPerWarp = 256;     // consecutive slots of a warp (given ids)
+constexpr int kWarps = 8;               // warps of a block
+constexpr int kWarpsOne = 32;           // of the block that does everything
+constexpr int kSteps = 4;               // most steps (32 / L tokens each) of a warp
+constexpr int kSlotsPerWarp = 256;      // consecutive slots of a warp (given ids)
+constexpr int kOneExperts = 256;        // most experts whose counts the single block keeps (32 KB)
 constexpr float kNegInf = -INFINITY;
 
 // An unsigned integer with the order of the floats; 0 is kept for "not selectable".
@@ -39,221 +43,323 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
 }
 
-__device__ __forceinline__ float warp_max_f(float v) {
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
 }
-
-// A row of logits into registers (element v of lane i is expert 32 v + i), then its scores.
-template <typename T, int NV>
-__device__ __forceinline__ void row_scores(const T* __restrict__ row, int experts, int score, float (&l)[NV],
-                                           float (&s)[NV]) {
-  const int lane = threadIdx.x & 31;
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if (L == 32) return __reduce_max_sync(0xffffffffu, v);
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int e = v * 32 + lane;
-    float x = e < experts ? to_f32(row[e]) : kNegInf;
-    x = x != x ? kNegInf : fminf(x, 3.402823466e+38f);
-    l[v] = x;
+  for (int d = L / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_max_f(float v) {
+#pragma unroll
+  for (int d = L / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+// the lanes of this token in a ballot
+template <int L>
+__device__ __forceinline__ uint32_t lanes_of(uint32_t ballot) {
+  return L == 32 ? ballot : (ballot >> (lane_id() & ~(L - 1))) & ((1u << (L & 31)) - 1u);
+}
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V > 16 ? 16 : sizeof(T) * V) Piece {
+  T v[V];
+};
+
+// A row of logits into registers (element v of the token's lane i is expert i V + v).  `row` NULL: no token.
+template <typename T, int L, int V>
+__device__ __forceinline__ void load_row(const T* __restrict__ row, int experts, bool pieces, float (&l)[V]) {
+  const int e0 = (lane_id() & (L - 1)) * V;
+  if (row && pieces && e0 + V <= experts) {
+    const Piece<T, V> p = *reinterpret_cast<const Piece<T, V>*>(row + e0);
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = to_f32(p.v[v]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = row && e0 + v < experts ? to_f32(row[e0 + v]) : kNegInf;
   }
+#pragma unroll
+  for (int v = 0; v < V; ++v) l[v] = l[v] != l[v] ? kNegInf : fminf(l[v], 3.402823466e+38f);
+}
+
+template <int L, int V>
+__device__ __forceinline__ void row_scores(int score, const float (&l)[V], float (&s)[V]) {
   if (score == SPGEMM_SCORE_SIGMOID) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) s[v] = 1.0f / (1.0f + expf(-l[v]));
+    for (int v = 0; v < V; ++v) s[v] = 1.0f / (1.0f + expf(-l[v]));
     return;
   }
   float top = l[0];
 #pragma unroll
-  for (int v = 1; v < NV; ++v) top = fmaxf(top, l[v]);
-  top = warp_max_f(top);
+  for (int v = 1; v < V; ++v) top = fmaxf(top, l[v]);
+  top = lanes_max_f<L>(top);
   float sum = 0.0f;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
+  for (int v = 0; v < V; ++v) {
     s[v] = l[v] > kNegInf ? expf(l[v] - top) : 0.0f;
     sum += s[v];
   }
-  sum = warp_sum(sum);
+  sum = lanes_sum<L>(sum);
 #pragma unroll
-  for (int v = 0; v < NV; ++v) s[v] = sum > 0.0f ? s[v] / sum : 0.0f;
+  for (int v = 0; v < V; ++v) s[v] = sum > 0.0f ? s[v] / sum : 0.0f;
 }
 
-// Clears the keys of the expert groups that are not kept.
-template <int NV>
-__device__ __forceinline__ void keep_groups(const spgemm_route_rule& r, int experts, bool by_scores, const float (&s)[NV],
-                                            uint32_t (&key)[NV]) {
-  const int lane = threadIdx.x & 31;
-  const int per = experts / r.groups;
-  float mine = kNegInf;  // lane g: the score of group g
-  for (int g = 0; g < r.groups; ++g) {
+// best and second of two pairs (second may equal best)
+__device__ __forceinline__ void merge_two(uint32_t& best, uint32_t& second, uint32_t b, uint32_t s) {
+  second = max(min(best, b), max(second, s));
+  best = max(best, b);
+}
+
+// Clears the keys of the expert groups that are not kept.  `val`: 32 floats of this token.
+template <int L, int V>
+__device__ __forceinline__ void keep_groups(const spgemm_route_rule& r, int per, bool by_scores, const float (&s)[V],
+                                            uint32_t (&key)[V], float* val) {
+  const int me = lane_id() & (L - 1), e0 = me * V;
+  const bool top2 = r.group_score == SPGEMM_GROUP_TOP2;
+  auto score_of = [&](uint32_t best, uint32_t second) {
+    float f = best ? key_value(best) : kNegInf;
+    if (top2 && second) f += key_value(second);
+    return f;
+  };
+  const int wide = per / V;  // lanes of a group, when groups are whole lanes
+  if (per % V == 0 && (wide & (wide - 1)) == 0 && wide <= L) {
     uint32_t best = 0, second = 0;
-    int at = 0x7fffffff;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int e = v * 32 + lane;
-      if (e / per != g || e >= experts || key[v] == 0) continue;
-      const uint32_t k = by_scores ? order_key(s[v]) : key[v];
-      if (k > best) {
-        second = best;
-        best = k;
-        at = e;
-      } else if (k > second) {
-        second = k;
+    for (int v = 0; v < V; ++v) {
+      const uint32_t k = key[v] == 0 ? 0u : by_scores ? order_key(s[v]) : key[v];
+      merge_two(best, second, k, 0u);
+    }
+    for (int d = 1; d < wide; d <<= 1)
+      merge_two(best, second, __shfl_xor_sync(0xffffffffu, best, d), __shfl_xor_sync(0xffffffffu, second, d));
+    if (me % wide == 0 && e0 / per < r.groups) val[e0 / per] = score_of(best, second);
+  } else {
+    for (int g = 0; g < r.groups; ++g) {
+      uint32_t best = 0, second = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const bool in = e0 + v >= g * per && e0 + v < (g + 1) * per && key[v] != 0;
+        const uint32_t k = !in ? 0u : by_scores ? order_key(s[v]) : key[v];
+        merge_two(best, second, k, 0u);
       }
-    }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    float val = top ? key_value(top) : kNegInf;
-    if (r.group_score == SPGEMM_GROUP_TOP2 && top) {
-      const int first = static_cast<int>(
-          __reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(at) : 0xffffffffu));
-      const uint32_t next = __reduce_max_sync(0xffffffffu, (best == top && at == first) ? second : best);
-      if (next) val += key_value(next);
-    }
-    if (lane == g) mine = val;
-  }
-  int rank = 0;
-  for (int g = 0; g < r.groups; ++g) {
-    const float o = __shfl_sync(0xffffffffu, mine, g);
-    if (o > mine || (o == mine && g < lane)) ++rank;
-  }
-  const uint32_t kept = __ballot_sync(0xffffffffu, lane < r.groups && rank < r.groups_kept);
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int e = v * 32 + lane;
-    if (e < experts && !((kept >> (e / per)) & 1u)) key[v] = 0;
+      for (int d = 1; d < L; d <<= 1)
+        merge_two(best, second, __shfl_xor_sync(0xffffffffu, best, d), __shfl_xor_sync(0xffffffffu, second, d));
+      if (me == 0) val[g] = score_of(best, second);
+    }
   }
+  __syncwarp();
+  uint32_t kept = 0;
+  for (int g = me; g < r.groups; g += L) {
+    const float mine = val[g];
+    int rank = 0;
+    for (int o = 0; o < r.groups; ++o) rank += val[o] > mine || (val[o] == mine && o < g) ? 1 : 0;
+    if (rank < r.groups_kept) kept |= 1u << g;
+  }
+#pragma unroll
+  for (int d = L / 2; d > 0; d >>= 1) kept |= __shfl_xor_sync(0xffffffffu, kept, d);
+  int g = e0 / per, left = (g + 1) * per - e0;  // group of expert e0 + v, and experts of it still to come
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (!((kept >> (g & 31)) & 1u)) key[v] = 0;
+    if (--left == 0) {
+      ++g;
+      left = per;
+    }
+  }
+  __syncwarp();
 }
 
-// The choice of one token; writes ids and weights of its row and, with `rank`, the rank of each
-// slot among the warp's earlier slots of the same expert (counted in cnt[experts]).
-template <typename T, int NV>
-__device__ __forceinline__ void route_token(const T* __restrict__ row, int experts, const spgemm_route_rule& r,
-                                            const float* __restrict__ bias, int32_t* __restrict__ ids,
-                                            float* __restrict__ weights, int32_t* __restrict__ rank, int* cnt) {
-  const int lane = threadIdx.x & 31;
-  float l[NV], s[NV];
-  row_scores<T, NV>(row, experts, r.score, l, s);
-  uint32_t key[NV];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int e = v * 32 + lane;
-    const float c = bias && e < experts ? s[v] + bias[e] : l[v];
-    key[v] = l[v] > kNegInf && c > kNegInf ? order_key(c) : 0u;
+// cnt[w * groups + e] (counts of warp w) -> exclusive prefix over the warps; the sum of e.
+__device__ __forceinline__ int warp_prefix(int* cnt, int groups, int warps, int e) {
+  int sum = 0;
+  for (int w = 0; w < warps; ++w) {
+    const int c = cnt[w * groups + e];
+    cnt[w * groups + e] = sum;
+    sum += c;
   }
-  if (r.groups_kept < r.groups)
-    keep_groups<NV>(r, experts, !bias && r.group_score == SPGEMM_GROUP_TOP2, s, key);
-  uint32_t chosen = 0;  // bit v: expert 32 v + lane
-  uint32_t best = 0;
-  int at = 0;
-  bool stale = true;
-  for (int j = 0; j < r.top_k; ++j) {
-    if (stale) {  // only the lane whose expert was taken looks again
-      best = 0;
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (key[v] > best) {
-          best = key[v];
-          at = v;
-        }
-      stale = false;
-    }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    if (top == 0) break;
-    const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(at * 32 + lane) : 0xffffffffu);
-    if ((e & 31u) == static_cast<uint32_t>(lane)) {
-      chosen |= 1u << at;
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (v == at) key[v] = 0;
-      stale = true;
-    }
-  }
-  float f = r.scale;
-  if (r.renormalise) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-      if ((chosen >> v) & 1u) sum += s[v];
-    sum = warp_sum(sum);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) s[v] = sum > 0.0f ? s[v] / sum : 0.0f;
-  }
-  int n = 0;
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const bool c = (chosen >> v) & 1u;
-    const uint32_t b = __ballot_sync(0xffffffffu, c);
-    if (c) {
-      const int j = n + __popc(b & lanemask_lt());
-      const int e = v * 32 + lane;
-      ids[j] = e;
-      weights[j] = s[v] * f;
-      rank[j] = cnt[e]++;
-    }
-    n += __popc(b);
-  }
-  if (lane >= n && lane < r.top_k) {
-    ids[lane] = -1;
-    weights[lane] = 0.0f;
-    rank[lane] = -1;
-  }
+  return sum;
 }
 
-// cnt[w * groups + e] (counts of warp w) -> exclusive prefix over the warps; total[e] = block sum.
-__device__ __forceinline__ void warp_prefix(int* cnt, int groups, int32_t* total) {
-  for (int e = threadIdx.x; e < groups; e += blockDim.x) {
-    int sum = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      const int c = cnt[w * groups + e];
-      cnt[w * groups + e] = sum;
-      sum += c;
-    }
-    total[e] = sum;
+// s_off[e] = first position of group e from its total (`of(e)`); returns the sum.  All threads call it.
+template <typename F>
+__device__ __forceinline__ int group_offsets(int groups, int* s_off, int* s_tmp, F of) {
+  int run = 0;
+  for (int e0 = 0; e0 < groups; e0 += blockDim.x) {
+    const int e = e0 + static_cast<int>(threadIdx.x);
+    const int c = e < groups ? of(e) : 0;
+    int sum;
+    const int incl = block_incl_scan(c, s_tmp, &sum);
+    if (e < groups) s_off[e] = run + incl - c;
+    run += sum;
   }
+  if (threadIdx.x == 0) s_off[groups] = run;
+  __syncthreads();
+  return run;
 }
 
 }  // namespace
 
-// ids, weights; position[slot] = the slot's rank among the block's slots of the same expert;
-// counts[block * experts + e] = the block's slots of expert e.
-template <typename T, int NV>
-__global__ void __launch_bounds__(kWarps * 32) k_route(const T* __restrict__ logits, int64_t stride, int64_t tokens,
-                                                       int experts, spgemm_route_rule r,
-                                                       const float* __restrict__ bias, int32_t* __restrict__ ids,
-                                                       float* __restrict__ weights, int32_t* __restrict__ position,
-                                                       int32_t* __restrict__ counts) {
-  extern __shared__ int s_cnt[];  // kWarps x experts
+// ids and weights.  ONE: also offsets, order and position (one block).  Otherwise position[slot] = the
+// slot's rank among the block's slots of the same expert and counts[e * blocks + block] = the block's
+// slots of expert e.
+template <typename T, int L, int V, bool ONE>
+__global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32)
+    k_route(const T* __restrict__ logits, int64_t stride, int64_t tokens, int experts, int pieces, int steps,
+            const __grid_constant__ spgemm_route_rule r, const float* __restrict__ bias, int32_t* __restrict__ ids,
+            float* __restrict__ weights, int32_t* __restrict__ position, int32_t* __restrict__ counts,
+            int32_t* __restrict__ offsets, int32_t* __restrict__ order) {
+  constexpr int kW = ONE ? kWarpsOne : kWarps, kPer = 32 / L;
+  extern __shared__ int s_cnt[];  // kW x experts, then (ONE) experts + 1 offsets
+  __shared__ float s_val[kW][kPer][32];
+  __shared__ int s_tmp[33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kWarps * experts; i += blockDim.x) s_cnt[i] = 0;
+  const int me = lane & (L - 1), sub = lane / L, e0 = me * V;
+  pdl_wait();
+  pdl_go();
+  for (int i = threadIdx.x; i < kW * experts; i += blockDim.x) s_cnt[i] = 0;
   __syncthreads();
-  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTokensPerWarp;
-  const int64_t t1 = min(tokens, t0 + kTokensPerWarp);
-  for (int64_t t = t0; t < t1; ++t) {
-    const int64_t o = t * r.top_k;
-    route_token<T, NV>(logits + t * stride, experts, r, bias, ids + o, weights + o, position + o,
-                       s_cnt + warp * experts);
+  int* cnt = s_cnt + warp * experts;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kW + warp) * (steps * kPer);
+  const int64_t t1 = min(tokens, t0 + steps * kPer);
+  const int per = experts / r.groups;
+  for (int64_t tw = t0; tw < t1; tw += kPer) {
+    const int64_t t = tw + sub;
+    const bool there = t < t1;
+    float l[V], s[V];
+    load_row<T, L, V>(there ? logits + t * stride : nullptr, experts, pieces, l);
+    row_scores<L, V>(r.score, l, s);
+    uint32_t key[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float c = bias && e0 + v < experts ? s[v] + bias[e0 + v] : l[v];
+      key[v] = l[v] > kNegInf && c > kNegInf ? order_key(c) : 0u;
+    }
+    if (r.groups_kept < r.groups)
+      keep_groups<L, V>(r, per, !bias && r.group_score == SPGEMM_GROUP_TOP2, s, key, s_val[warp][sub]);
+    uint32_t chosen = 0;  // bit v: expert e0 + v
+    uint32_t best = 0;
+    int at = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (key[v] > best) {
+        best = key[v];
+        at = v;
+      }
+    for (int j = 0; j < r.top_k; ++j) {
+      const uint32_t top = lanes_max<L>(best);
+      const uint32_t have = lanes_of<L>(__ballot_sync(0xffffffffu, best == top && top != 0));
+      if (have && __ffs(have) - 1 == me) {  // this lane's expert is taken: look for its next best
+        chosen |= 1u << at;
+        best = 0;
+        const int was = at;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (v == was) key[v] = 0;
+          if (key[v] > best) {
+            best = key[v];
+            at = v;
+          }
+        }
+      }
+    }
+    if (r.renormalise) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if ((chosen >> v) & 1u) sum += s[v];
+      sum = lanes_sum<L>(sum);
+#pragma unroll
+      for (int v = 0; v < V; ++v) s[v] = sum > 0.0f ? s[v] / sum : 0.0f;
+    }
+    int before = __popc(chosen);  // chosen experts of the lower lanes
+    const int mine = before;
+#pragma unroll
+    for (int d = 1; d < L; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, before, d, L);
+      if (me >= d) before += o;
+    }
+    const int n = __shfl_sync(0xffffffffu, before, L - 1, L);
+    int64_t o = t * r.top_k + before - mine;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool c = (chosen >> v) & 1u;
+      int rank = 0, all = c ? 1 : 0;
+      if (L < 32) {  // the lanes of the other tokens that hold the same expert
+        uint32_t same = 0;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) same |= 1u << (q * L);
+        same = __ballot_sync(0xffffffffu, c) & (same << me);
+        rank = __popc(same & lanemask_lt());
+        all = __popc(same);
+      }
+      int base = 0;
+      if (all) base = cnt[e0 + v];
+      if (L < 32) __syncwarp();
+      if (c) {
+        ids[o] = e0 + v;
+        weights[o] = s[v] * r.scale;
+        position[o] = base + rank;
+        ++o;
+        if (rank == 0) cnt[e0 + v] = base + all;
+      }
+      if (L < 32) __syncwarp();
+    }
+    for (int j = n + me; there && j < r.top_k; j += L) {
+      ids[t * r.top_k + j] = -1;
+      weights[t * r.top_k + j] = 0.0f;
+      position[t * r.top_k + j] = -1;
+    }
     __syncwarp();
   }
   __syncthreads();
-  warp_prefix(s_cnt, experts, counts + static_cast<int64_t>(blockIdx.x) * experts);
-  __syncthreads();
-  for (int64_t i = t0 * r.top_k + lane; i < t1 * r.top_k; i += 32) {
-    const int e = ids[i];
-    if (e >= 0) position[i] += s_cnt[warp * experts + e];
+  const int64_t i0 = t0 * r.top_k + lane, i1 = t1 * r.top_k;
+  if (!ONE) {
+    for (int e = threadIdx.x; e < experts; e += blockDim.x)
+      counts[static_cast<int64_t>(e) * gridDim.x + blockIdx.x] = warp_prefix(s_cnt, experts, kW, e);
+    __syncthreads();
+    for (int64_t i = i0; i < i1; i += 32) {
+      const int e = ids[i];
+      if (e >= 0) position[i] += cnt[e];
+    }
+  } else {
+    int* s_off = s_cnt + kW * experts;
+    const int total = group_offsets(experts, s_off, s_tmp, [&](int e) { return warp_prefix(s_cnt, experts, kW, e); });
+    for (int e = threadIdx.x; e <= experts; e += blockDim.x) offsets[e] = s_off[e];
+    for (int64_t i = i0; i < i1; i += 32) {
+      const int e = ids[i];
+      if (e >= 0) {
+        const int p = position[i] + cnt[e] + s_off[e];
+        position[i] = p;
+        order[p] = static_cast<int32_t>(i);
+      }
+      if (i >= total) order[i] = -1;
+    }
   }
 }
 
-// The same counts and ranks for given ids: equal ids among 32 consecutive slots are ranked by a
-// warp match.
-__global__ void __launch_bounds__(kWarps * 32) k_count_ids(const int32_t* __restrict__ ids, int64_t slots, int groups,
-                                                           int32_t* __restrict__ position, int32_t* __restrict__ counts,
-                                                           uint32_t* err) {
-  extern __shared__ int s_cnt[];  // kWarps x groups
+// The same for given ids: equal ids among 32 consecutive slots are ranked by a warp match.
+template <bool ONE>
+__global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32)
+    k_count_ids(const int32_t* __restrict__ ids, int64_t slots, int per_warp, int groups, int32_t* __restrict__ position,
+                int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ order, uint32_t* err) {
+  constexpr int kW = ONE ? kWarpsOne : kWarps;
+  extern __shared__ int s_cnt[];  // kW x groups, then (ONE) groups + 1 offsets
+  __shared__ int s_tmp[33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kWarps * groups; i += blockDim.x) s_cnt[i] = 0;
+  pdl_wait();
+  pdl_go();
+  for (int i = threadIdx.x; i < kW * groups; i += blockDim.x) s_cnt[i] = 0;
   __syncthreads();
   int* cnt = s_cnt + warp * groups;
-  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kSlotsPerWarp;
-  const int64_t i1 = min(slots, i0 + kSlotsPerWarp);
+  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * kW + warp) * per_warp;
+  const int64_t i1 = min(slots, i0 + per_warp);
   for (int64_t b = i0; b < i1; b += 32) {
     const int64_t i = b + lane;
     int e = i < i1 ? ids[i] : -1;
@@ -270,27 +376,45 @@ __global__ void __launch_bounds__(kWarps * 32) k_count_ids(const int32_t* __rest
     if (i < i1) position[i] = e >= 0 ? base + before : -1;
   }
   __syncthreads();
-  warp_prefix(s_cnt, groups, counts + static_cast<int64_t>(blockIdx.x) * groups);
-  __syncthreads();
-  for (int64_t i = i0 + lane; i < i1; i += 32)
-    if (position[i] >= 0) position[i] += cnt[ids[i]];
+  if (!ONE) {
+    for (int e = threadIdx.x; e < groups; e += blockDim.x)
+      counts[static_cast<int64_t>(e) * gridDim.x + blockIdx.x] = warp_prefix(s_cnt, groups, kW, e);
+    __syncthreads();
+    for (int64_t i = i0 + lane; i < i1; i += 32)
+      if (position[i] >= 0) position[i] += cnt[ids[i]];
+  } else {
+    int* s_off = s_cnt + kW * groups;
+    const int total = group_offsets(groups, s_off, s_tmp, [&](int e) { return warp_prefix(s_cnt, groups, kW, e); });
+    for (int e = threadIdx.x; e <= groups; e += blockDim.x) offsets[e] = s_off[e];
+    for (int64_t i = i0 + lane; i < i1; i += 32) {
+      if (position[i] >= 0) {
+        const int e = ids[i], p = position[i] + cnt[e] + s_off[e];
+        position[i] = p;
+        order[p] = static_cast<int32_t>(i);
+      }
+      if (i >= total) order[i] = -1;
+    }
+  }
 }
 
-// counts[b * groups + e] -> the slots of group e in the blocks before b; total[e] = all of them.
-// One warp per group.
-__global__ void __launch_bounds__(kWarps * 32) k_block_offsets(int32_t* __restrict__ counts, int64_t blocks, int groups,
-                                                               int32_t* __restrict__ total) {
-  const int e = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (e >= groups) return;
+// counts[e * blocks + b] -> the slots of group e in the blocks before b; total[e] = all of them.
+// One block per group.
+__global__ void __launch_bounds__(256) k_block_offsets(int32_t* __restrict__ counts, int64_t blocks,
+                                                       int32_t* __restrict__ total) {
+  __shared__ int s_tmp[33];
+  int32_t* c = counts + blockIdx.x * blocks;
+  pdl_wait();
+  pdl_go();
   int run = 0;
-  for (int64_t b0 = 0; b0 < blocks; b0 += 32) {
-    const int64_t b = b0 + lane;
-    const int c = b < blocks ? counts[b * groups + e] : 0;
-    const int incl = warp_incl_scan(c);
-    if (b < blocks) counts[b * groups + e] = run + incl - c;
-    run += __shfl_sync(0xffffffffu, incl, 31);
+  for (int64_t b0 = 0; b0 < blocks; b0 += blockDim.x) {
+    const int64_t b = b0 + threadIdx.x;
+    const int n = b < blocks ? c[b] : 0;
+    int sum;
+    const int incl = block_incl_scan(n, s_tmp, &sum);
+    if (b < blocks) c[b] = run + incl - n;
+    run += sum;
   }
-  if (lane == 0) total[e] = run;
+  if (threadIdx.x == 0) total[blockIdx.x] = run;
 }
 
 // position: rank in the block -> position; order: its inverse; offsets.  per_block consecutive
@@ -301,28 +425,22 @@ __global__ void __launch_bounds__(kWarps * 32) k_group_scatter(const int32_t* __
                                                                const int32_t* __restrict__ total,
                                                                int32_t* __restrict__ offsets, int32_t* __restrict__ order,
                                                                int32_t* __restrict__ position) {
-  extern __shared__ int s_off[];  // groups + 1
+  extern __shared__ int s_off[];  // groups + 1, then the block's base of each group
   __shared__ int s_tmp[33];
-  int run = 0;
-  for (int e0 = 0; e0 < groups; e0 += blockDim.x) {
-    const int e = e0 + threadIdx.x;
-    const int c = e < groups ? total[e] : 0;
-    int sum;
-    const int incl = block_incl_scan(c, s_tmp, &sum);
-    if (e < groups) s_off[e] = run + incl - c;
-    run += sum;
-  }
-  if (threadIdx.x == 0) s_off[groups] = run;
-  __syncthreads();
+  pdl_wait();
+  pdl_go();
+  int* s_base = s_off + groups + 1;
+  for (int e = threadIdx.x; e < groups; e += blockDim.x)
+    s_base[e] = counts[static_cast<int64_t>(e) * gridDim.x + blockIdx.x];
+  const int run = group_offsets(groups, s_off, s_tmp, [&](int e) { return total[e]; });
   if (blockIdx.x == 0)
     for (int e = threadIdx.x; e <= groups; e += blockDim.x) offsets[e] = s_off[e];
-  const int32_t* base = counts + static_cast<int64_t>(blockIdx.x) * groups;
   const int64_t i1 = min(slots, (static_cast<int64_t>(blockIdx.x) + 1) * per_block);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x; i < i1; i += blockDim.x) {
     const int r = position[i];
     if (r >= 0) {
       const int e = ids[i];
-      const int p = s_off[e] + base[e] + r;
+      const int p = s_off[e] + s_base[e] + r;
       position[i] = p;
       order[p] = static_cast<int32_t>(i);
     }
@@ -330,120 +448,199 @@ __global__ void __launch_bounds__(kWarps * 32) k_group_scatter(const int32_t* __
   }
 }
 
-// Gradient of the logits.  One warp per token; the row's scores are computed again.
-template <typename T, int NV>
+// Gradient of the logits; the row's scores are computed again.  A token's chosen gradients meet its row
+// through shared memory.  Bound by instructions per row, like the choice.
+template <typename T, int L, int V>
 __global__ void __launch_bounds__(kWarps * 32) k_route_backward(const T* __restrict__ logits, int64_t stride,
-                                                                int64_t tokens, int experts, spgemm_route_rule r,
+                                                                int64_t tokens, int experts, int pieces,
+                                                                const __grid_constant__ spgemm_route_rule r,
                                                                 const int32_t* __restrict__ ids,
                                                                 const float* __restrict__ grad_w, T* __restrict__ out,
-                                                                int64_t out_stride) {
-  __shared__ float s_row[kWarps][kMaxGroups > NV * 32 ? NV * 32 : kMaxGroups];
+                                                                int64_t out_stride, int out_pieces) {
+  constexpr int kPer = 32 / L;
+  __shared__ float s_row[kWarps][kPer][L * V];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* full = s_row[warp];  // scores, then gradients of the scores, of the whole row
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < tokens;
-       t += static_cast<int64_t>(gridDim.x) * kWarps) {
-    float l[NV], s[NV];
-    row_scores<T, NV>(logits + t * stride, experts, r.score, l, s);
-    int e = lane < r.top_k ? ids[t * r.top_k + lane] : -1;
-    if (e >= experts) e = -1;
-    float ds = e >= 0 ? grad_w[t * r.top_k + lane] * r.scale : 0.0f;
-    if (r.renormalise) {  // w = s / sum: ds = (dw - sum of dw * w) / sum
+  const int me = lane & (L - 1), sub = lane / L, e0 = me * V;
+  float* full = s_row[warp][sub];  // gradients of the scores of the whole row
+  pdl_wait();
+  pdl_go();
 #pragma unroll
-      for (int v = 0; v < NV; ++v) full[v * 32 + lane] = s[v];
-      __syncwarp();
-      const float mine = e >= 0 ? full[e] : 0.0f;
-      const float sum = warp_sum(mine);
-      const float dot = sum > 0.0f ? warp_sum(ds * (mine / sum)) : 0.0f;
-      ds = e >= 0 && sum > 0.0f ? (ds - dot) / sum : 0.0f;
-      __syncwarp();
+  for (int v = 0; v < V; ++v) full[e0 + v] = 0.0f;
+  __syncwarp();
+  for (int64_t tw = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kPer; tw < tokens;
+       tw += static_cast<int64_t>(gridDim.x) * kWarps * kPer) {
+    const int64_t t = tw + sub;
+    const bool there = t < tokens;
+    float l[V], s[V], d[V];
+    load_row<T, L, V>(there ? logits + t * stride : nullptr, experts, pieces, l);
+    row_scores<L, V>(r.score, l, s);
+    uint32_t chosen = 0;
+    for (int j = me; there && j < r.top_k; j += L) {
+      const int e = ids[t * r.top_k + j];
+      if (e >= 0 && e < experts) full[e] = grad_w[t * r.top_k + j] * r.scale;
     }
+    // which experts were chosen: a mark per expert in the row's own lanes
+    __syncwarp();
 #pragma unroll
-    for (int v = 0; v < NV; ++v) full[v * 32 + lane] = 0.0f;
-    __syncwarp();
-    if (e >= 0) full[e] = ds;
-    __syncwarp();
+    for (int v = 0; v < V; ++v) d[v] = full[e0 + v];
+    if (r.renormalise) {  // w = s / sum: ds = (dw - sum of dw * w) / sum, over the chosen ones
+      float sum = 0.0f, dot = 0.0f;
+      for (int j = 0; j < r.top_k; ++j) {
+        const int e = there ? ids[t * r.top_k + j] : -1;
+        if (e >= e0 && e < e0 + V && e < experts) chosen |= 1u << (e - e0);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if ((chosen >> v) & 1u) {
+          sum += s[v];
+          dot += d[v] * s[v];
+        }
+      sum = lanes_sum<L>(sum);
+      dot = lanes_sum<L>(dot);
+      const float mean = sum > 0.0f ? dot / sum : 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] = (chosen >> v) & 1u && sum > 0.0f ? (d[v] - mean) / sum : 0.0f;
+    }
     float dot = 0.0f;
     if (r.score == SPGEMM_SCORE_SOFTMAX) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) dot += full[v * 32 + lane] * s[v];
-      dot = warp_sum(dot);
+      for (int v = 0; v < V; ++v) dot += d[v] * s[v];
+      dot = lanes_sum<L>(dot);
     }
+    Piece<T, V> o;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int i = v * 32 + lane;
-      const float d = full[i];
-      const float g = r.score == SPGEMM_SCORE_SOFTMAX ? s[v] * (d - dot) : d * s[v] * (1.0f - s[v]);
-      if (i < experts) out[t * out_stride + i] = from_f32<T>(g);
+    for (int v = 0; v < V; ++v)
+      o.v[v] = from_f32<T>(r.score == SPGEMM_SCORE_SOFTMAX ? s[v] * (d[v] - dot) : d[v] * s[v] * (1.0f - s[v]));
+    if (there) {
+      if (out_pieces && e0 + V <= experts) {
+        *reinterpret_cast<Piece<T, V>*>(out + t * out_stride + e0) = o;
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (e0 + v < experts) out[t * out_stride + e0 + v] = o.v[v];
+      }
     }
+    __syncwarp();
+#pragma unroll
+    for (int v = 0; v < V; ++v) full[e0 + v] = 0.0f;
     __syncwarp();
   }
 }
 
 namespace {
 
-// f(integral constant NV) for the smallest number of registers per lane that holds a row
+template <int L_, int V_>
+struct Width {
+  static constexpr int L = L_, V = V_;
+};
+
+// f(Width) for the fewest lanes, then the fewest registers, that hold a row
 template <typename F>
 void for_width(int experts, F f) {
-  if (experts <= 32) f(std::integral_constant<int, 1>());
-  else if (experts <= 64) f(std::integral_constant<int, 2>());
-  else if (experts <= 128) f(std::integral_constant<int, 4>());
-  else if (experts <= 256) f(std::integral_constant<int, 8>());
-  else if (experts <= 512) f(std::integral_constant<int, 16>());
-  else f(std::integral_constant<int, 32>());
+  if (experts <= 64) f(Width<8, 8>());
+  else if (experts <= 128) f(Width<16, 8>());
+  else if (experts <= 256) f(Width<32, 8>());
+  else if (experts <= 512) f(Width<32, 16>());
+  else f(Width<32, 32>());
+}
+int tokens_per_step(int experts) { return experts <= 64 ? 4 : experts <= 128 ? 2 : 1; }
+
+// whether rows may be read in pieces of V elements (at most 16 bytes each)
+template <typename T>
+bool in_pieces(const spgemm_dense& d) {
+  return reinterpret_cast<uintptr_t>(d.data) % 16 == 0 && (d.stride * static_cast<int64_t>(sizeof(T))) % 16 == 0;
 }
 
-int64_t scratch_bytes(int64_t blocks, int64_t groups) { return 4 * (blocks * groups + groups); }
+struct Shape {
+  bool one;
+  int steps;
+  int64_t blocks;
+};
+
+// One block while its warps have few steps each; else up to kSteps steps per warp once there are two
+// blocks per SM.
+Shape route_shape(int64_t tokens, int experts) {
+  const int64_t step = tokens_per_step(experts);
+  const int64_t one = ceil_div(tokens, kWarpsOne * step);
+  if (one <= kSteps && experts <= kOneExperts) return {true, static_cast<int>(std::max<int64_t>(one, 1)), 1};
+  const int64_t steps = std::min<int64_t>(kSteps, std::max<int64_t>(1, tokens / (kWarps * step * 304)));
+  return {false, static_cast<int>(steps), ceil_div(tokens, kWarps * step * steps)};
+}
+
+// One block while its warps have at most four turns of 32 slots.
+Shape group_shape(int64_t slots, int groups) {
+  if (slots <= kWarpsOne * 128 && groups <= kOneExperts)
+    return {true, static_cast<int>(std::max<int64_t>(32, ceil_div(slots, kWarpsOne * 32) * 32)), 1};
+  return {false, kSlotsPerWarp, ceil_div(slots, kWarps * kSlotsPerWarp)};
+}
+
+int64_t scratch_bytes(const Shape& s, int64_t groups) { return s.one ? 0 : 4 * (s.blocks * groups + groups); }
 
 void transpose(const int32_t* ids, int64_t slots, int64_t per_block, int64_t blocks, int groups, int32_t* counts,
                int32_t* offsets, int32_t* order, int32_t* position, cudaStream_t s) {
   int32_t* total = counts + blocks * groups;
-  note_launch();
-  k_block_offsets<<<static_cast<unsigned>(ceil_div(groups, kWarps)), kWarps * 32, 0, s>>>(counts, blocks, groups, total);
-  note_launch();
-  k_group_scatter<<<static_cast<unsigned>(std::max<int64_t>(blocks, 1)), kWarps * 32, sizeof(int) * (groups + 1), s>>>(
-      ids, slots, per_block, groups, counts, total, offsets, order, position);
+  launch_next(k_block_offsets, static_cast<unsigned>(groups), 256, 0, s, counts, blocks, total);
+  launch_next(k_group_scatter, static_cast<unsigned>(blocks), kWarps * 32, sizeof(int) * (2 * groups + 1), s, ids, slots,
+              per_block, groups, static_cast<const int32_t*>(counts), static_cast<const int32_t*>(total), offsets, order,
+              position);
 }
 
 }  // namespace
 
-int64_t route_scratch_bytes(int64_t tokens, int32_t experts) {
-  return scratch_bytes(ceil_div(tokens, kWarps * kTokensPerWarp), experts);
-}
-int64_t group_scratch_bytes(int64_t slots, int32_t groups) {
-  return scratch_bytes(ceil_div(slots, kWarps * kSlotsPerWarp), groups);
-}
+int64_t route_scratch_bytes(int64_t tokens, int32_t experts) { return scratch_bytes(route_shape(tokens, experts), experts); }
+int64_t group_scratch_bytes(int64_t slots, int32_t groups) { return scratch_bytes(group_shape(slots, groups), groups); }
 
 void launch_route(const spgemm_dense& logits, const spgemm_route_rule& rule, const float* bias, const RouteOut& out,
                   void* scratch, cudaStream_t s) {
   const int64_t tokens = logits.rows;
   const int experts = static_cast<int>(logits.cols);
   int32_t* counts = static_cast<int32_t*>(scratch);
-  const int64_t blocks = ceil_div(tokens, kWarps * kTokensPerWarp);
-  if (blocks > 0)
-    for_dtype(logits.dtype, [&](auto type) {
-      for_width(experts, [&](auto nv) {
-        using T = decltype(type);
-        note_launch();
-        k_route<T, nv.value><<<static_cast<unsigned>(blocks), kWarps * 32, sizeof(int) * kWarps * experts, s>>>(
-            static_cast<const T*>(logits.data), logits.stride, tokens, experts, rule, bias, out.ids, out.weights,
-            out.position, counts);
-      });
+  const Shape shape = route_shape(tokens, experts);
+  const int step = tokens_per_step(experts);
+  if (tokens == 0) {
+    cudaMemsetAsync(out.offsets, 0, sizeof(int32_t) * (experts + 1), s);
+    return;
+  }
+  for_dtype(logits.dtype, [&](auto type) {
+    for_width(experts, [&](auto w) {
+      using T = decltype(type);
+      using W = decltype(w);
+      auto go = [&](auto kern, int warps, size_t smem) {
+        launch_next(kern, static_cast<unsigned>(shape.blocks), warps * 32, smem, s, static_cast<const T*>(logits.data),
+                    logits.stride, tokens, experts, in_pieces<T>(logits) ? 1 : 0, shape.steps, rule, bias, out.ids,
+                    out.weights, out.position, counts, out.offsets, out.order);
+      };
+      if constexpr (W::V == 8) {
+        if (shape.one) {
+          go(k_route<T, W::L, W::V, true>, kWarpsOne, sizeof(int) * (kWarpsOne * experts + experts + 1));
+          return;
+        }
+      }
+      go(k_route<T, W::L, W::V, false>, kWarps, sizeof(int) * kWarps * experts);
     });
-  transpose(out.ids, tokens * rule.top_k, static_cast<int64_t>(kWarps) * kTokensPerWarp * rule.top_k, blocks, experts,
-            counts, out.offsets, out.order, out.position, s);
+  });
+  if (!shape.one)
+    transpose(out.ids, tokens * rule.top_k, static_cast<int64_t>(kWarps) * shape.steps * step * rule.top_k, shape.blocks,
+              experts, counts, out.offsets, out.order, out.position, s);
 }
 
 void launch_group_rows(const int32_t* ids, int64_t slots, int32_t groups, int32_t* offsets, int32_t* order,
                        int32_t* position, void* scratch, cudaStream_t s) {
   int32_t* counts = static_cast<int32_t*>(scratch);
-  const int64_t blocks = ceil_div(slots, kWarps * kSlotsPerWarp);
-  if (blocks > 0) {
-    note_launch();
-    k_count_ids<<<static_cast<unsigned>(blocks), kWarps * 32, sizeof(int) * kWarps * groups, s>>>(
-        ids, slots, groups, position, counts, grouped_err());
+  const Shape shape = group_shape(slots, groups);
+  if (shape.one) {
+    launch_next(k_count_ids<true>, 1u, kWarpsOne * 32, sizeof(int) * (kWarpsOne * groups + groups + 1), s, ids, slots,
+                shape.steps, static_cast<int>(groups), position, counts, offsets, order, grouped_err());
+    return;
   }
-  transpose(ids, slots, static_cast<int64_t>(kWarps) * kSlotsPerWarp, blocks, groups, counts, offsets, order, position,
-            s);
+  if (shape.blocks == 0) {
+    cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (groups + 1), s);
+    return;
+  }
+  launch_next(k_count_ids<false>, static_cast<unsigned>(shape.blocks), kWarps * 32, sizeof(int) * kWarps * groups, s, ids,
+              slots, shape.steps, static_cast<int>(groups), position, counts, offsets, order, grouped_err());
+  transpose(ids, slots, static_cast<int64_t>(kWarps) * kSlotsPerWarp, shape.blocks, groups, counts, offsets, order,
+            position, s);
 }
 
 void launch_route_backward(const spgemm_dense& logits, const spgemm_route_rule& rule, const int32_t* ids,
@@ -451,14 +648,14 @@ void launch_route_backward(const spgemm_dense& logits, const spgemm_route_rule& 
   const int64_t tokens = logits.rows;
   const int experts = static_cast<int>(logits.cols);
   if (tokens == 0) return;
-  const int64_t blocks = std::min<int64_t>(ceil_div(tokens, kWarps), 1 << 20);
+  const int64_t blocks = std::min<int64_t>(ceil_div(tokens, kWarps * tokens_per_step(experts)), 1 << 20);
   for_dtype(logits.dtype, [&](auto type) {
-    for_width(experts, [&](auto nv) {
+    for_width(experts, [&](auto w) {
       using T = decltype(type);
-      note_launch();
-      k_route_backward<T, nv.value><<<static_cast<unsigned>(blocks), kWarps * 32, 0, s>>>(
-          static_cast<const T*>(logits.data), logits.stride, tokens, experts, rule, ids, grad_w,
-          static_cast<T*>(out.data), out.stride);
+      using W = decltype(w);
+      launch_next(k_route_backward<T, W::L, W::V>, static_cast<unsigned>(blocks), kWarps * 32, 0, s,
+                  static_cast<const T*>(logits.data), logits.stride, tokens, experts, in_pieces<T>(logits) ? 1 : 0, rule,
+                  ids, grad_w, static_cast<T*>(out.data), out.stride, in_pieces<T>(out) ? 1 : 0);
     });
   });
 }
