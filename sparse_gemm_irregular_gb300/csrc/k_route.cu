@@ -14,8 +14,8 @@
 // reason the chosen experts leave in ascending order after one prefix sum of their counts.
 //
 // The transpose is a stable counting sort.  Each warp owns consecutive tokens and counts per
-// expert in its own row of shared memory; the count before a slot plus the earlier tokens of the
-// same step (a ballot over the lanes that hold the same expert) is its rank in the warp.  The block adds its
+// expert in its own row of shared memory, its tokens one after the other: the count before a slot is
+// its rank in the warp.  The block adds its
 // warps up and writes its counts; k_block_offsets scans them over the blocks, k_group_scatter
 // over the experts.  Few tokens (one block's worth) finish in the first kernel.
 // Ranks and scans are integers: the result does not depend on the order of the blocks.
@@ -89,12 +89,14 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int experts,
   for (int v = 0; v < V; ++v) l[v] = l[v] != l[v] ? kNegInf : fminf(l[v], 3.402823466e+38f);
 }
 
+// Scores of a row are s[v] * (the returned factor): softmax's division by the sum is left to the few
+// values that need it.
 template <int L, int V>
-__device__ __forceinline__ void row_scores(int score, const float (&l)[V], float (&s)[V]) {
+__device__ __forceinline__ float row_scores(int score, const float (&l)[V], float (&s)[V]) {
   if (score == SPGEMM_SCORE_SIGMOID) {
 #pragma unroll
     for (int v = 0; v < V; ++v) s[v] = 1.0f / (1.0f + expf(-l[v]));
-    return;
+    return 1.0f;
   }
   float top = l[0];
 #pragma unroll
@@ -107,8 +109,7 @@ __device__ __forceinline__ void row_scores(int score, const float (&l)[V], float
     sum += s[v];
   }
   sum = lanes_sum<L>(sum);
-#pragma unroll
-  for (int v = 0; v < V; ++v) s[v] = sum > 0.0f ? s[v] / sum : 0.0f;
+  return sum > 0.0f ? 1.0f / sum : 0.0f;
 }
 
 // best and second of two pairs (second may equal best)
@@ -234,7 +235,12 @@ __global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32)
     const bool there = t < t1;
     float l[V], s[V];
     load_row<T, L, V>(there ? logits + t * stride : nullptr, experts, pieces, l);
-    row_scores<L, V>(r.score, l, s);
+    float f = row_scores<L, V>(r.score, l, s);
+    if (bias || r.group_score == SPGEMM_GROUP_TOP2) {  // scores are compared or added: they want their division
+#pragma unroll
+      for (int v = 0; v < V; ++v) s[v] *= f;
+      f = 1.0f;
+    }
     uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -275,9 +281,9 @@ __global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32)
       for (int v = 0; v < V; ++v)
         if ((chosen >> v) & 1u) sum += s[v];
       sum = lanes_sum<L>(sum);
-#pragma unroll
-      for (int v = 0; v < V; ++v) s[v] = sum > 0.0f ? s[v] / sum : 0.0f;
+      f = sum > 0.0f ? 1.0f / sum : 0.0f;  // the row's own factor cancels
     }
+    f *= r.scale;
     int before = __popc(chosen);  // chosen experts of the lower lanes
     const int mine = before;
 #pragma unroll
@@ -287,29 +293,21 @@ __global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32)
     }
     const int n = __shfl_sync(0xffffffffu, before, L - 1, L);
     int64_t o = t * r.top_k + before - mine;
+    // tokens of a step take their ranks one after the other; a lane has few chosen experts
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const bool c = (chosen >> v) & 1u;
-      int rank = 0, all = c ? 1 : 0;
-      if (L < 32) {  // the lanes of the other tokens that hold the same expert
-        uint32_t same = 0;
+    for (int q = 0; q < kPer; ++q) {
+      if (kPer == 1 || sub == q)
+        for (uint32_t left = chosen; left; left &= left - 1, ++o) {
+          const int v = __ffs(left) - 1;
+          float w = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) same |= 1u << (q * L);
-        same = __ballot_sync(0xffffffffu, c) & (same << me);
-        rank = __popc(same & lanemask_lt());
-        all = __popc(same);
-      }
-      int base = 0;
-      if (all) base = cnt[e0 + v];
-      if (L < 32) __syncwarp();
-      if (c) {
-        ids[o] = e0 + v;
-        weights[o] = s[v] * r.scale;
-        position[o] = base + rank;
-        ++o;
-        if (rank == 0) cnt[e0 + v] = base + all;
-      }
-      if (L < 32) __syncwarp();
+          for (int i = 0; i < V; ++i) w = i == v ? s[i] : w;
+          const int rank = cnt[e0 + v]++;
+          ids[o] = e0 + v;
+          weights[o] = w * f;
+          position[o] = rank;
+        }
+      if (kPer > 1) __syncwarp();
     }
     for (int j = n + me; there && j < r.top_k; j += L) {
       ids[t * r.top_k + j] = -1;
@@ -473,7 +471,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_backward(const T* __restr
     const bool there = t < tokens;
     float l[V], s[V], d[V];
     load_row<T, L, V>(there ? logits + t * stride : nullptr, experts, pieces, l);
-    row_scores<L, V>(r.score, l, s);
+    const float f = row_scores<L, V>(r.score, l, s);
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] *= f;
     uint32_t chosen = 0;
     for (int j = me; there && j < r.top_k; j += L) {
       const int e = ids[t * r.top_k + j];

@@ -12,13 +12,13 @@ from dataclasses import dataclass
 from typing import Any
 
 from . import binding
-from .binding import _check, _vp, load, spgemm_dense, spgemm_grouping, spgemm_route_rule, spgemm_weights
+from .binding import _check, load, spgemm_dense, spgemm_grouping, spgemm_route_rule, spgemm_weights
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _GROUP_SCORES = {"max": 0, "top2": 1}
 
 
-@dataclass
+@dataclass(frozen=True)
 class Routing:
     """The choice of every token and its transpose, in device memory.
 
@@ -32,6 +32,22 @@ class Routing:
     order: Any
     position: Any
     rule: Any = None
+
+    def __post_init__(self):
+        import torch
+        i32 = torch.int32
+        n = self.ids.numel()
+        for t, name, dtype, size in ((self.ids, "ids", i32, n), (self.weights, "weights", torch.float32, n),
+                                     (self.offsets, "offsets", i32, -1), (self.order, "order", i32, n),
+                                     (self.position, "position", i32, n)):
+            _want(t, name, dtype)
+            if size >= 0 and t.numel() != size:
+                raise ValueError("routing: ids, weights, order and position want tokens * top_k entries each")
+        if self.ids.dim() != 2:
+            raise ValueError("ids: (tokens, top_k) is wanted")
+        object.__setattr__(self, "_grouping", spgemm_grouping(n, self.ids.shape[1], self.offsets.numel() - 1,
+                                                              self.offsets.data_ptr(), self.order.data_ptr(),
+                                                              self.position.data_ptr()))
 
     @property
     def tokens(self) -> int:
@@ -65,53 +81,55 @@ class Routing:
         return DeviceCSR(self.groups, self.tokens, self.offsets.long(), (slot // self.top_k).int(),
                          self.weights.reshape(-1)[slot].double())
 
-    def _grouping(self) -> spgemm_grouping:
-        for t, name in ((self.ids, "ids"), (self.offsets, "offsets"), (self.order, "order"), (self.position, "position")):
-            _want(t, name, "int32")
-        _want(self.weights, "weights", "float32")
-        n = self.ids.numel()
-        if self.ids.dim() != 2 or self.position.numel() != n or self.order.numel() != n or self.weights.numel() != n:
-            raise ValueError("routing: ids, weights, order and position want tokens * top_k entries each")
-        return spgemm_grouping(n, self.ids.shape[1], self.groups, self.offsets.data_ptr(), self.order.data_ptr(),
-                               self.position.data_ptr())
-
 
 def _dtype(t, name: str) -> int:
     import torch
-    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    d = t.dtype
+    code = 1 if d is torch.bfloat16 else 2 if d is torch.float16 else 0 if d is torch.float32 else None
     if code is None:
-        raise TypeError("%s: float32, bfloat16 or float16 wanted, got %s" % (name, t.dtype))
+        raise TypeError("%s: float32, bfloat16 or float16 wanted, got %s" % (name, d))
     if not t.is_cuda:
         raise ValueError("%s: a CUDA tensor is wanted" % name)
     return code
 
 
-def _want(t, name: str, dtype: str):
-    if str(t.dtype) != "torch." + dtype or not t.is_cuda or not t.is_contiguous():
+def _want(t, name: str, dtype):
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s: a contiguous CUDA tensor of %s is wanted" % (name, dtype))
 
 
 def _dense(t, name: str) -> spgemm_dense:
     code = _dtype(t, name)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, step = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and step[1] != 1):
         raise ValueError("%s: a matrix whose rows are contiguous is wanted" % name)
-    return spgemm_dense(t.data_ptr(), t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]), code, 0)
+    return spgemm_dense(t.data_ptr(), shape[0], shape[1], max(step[0], shape[1]), code, 0)
 
 
 def _weights(t, name: str) -> spgemm_weights:
     code = _dtype(t, name)
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    shape, step = t.shape, t.stride()
+    if len(shape) != 3 or (shape[2] > 1 and step[2] != 1):
         raise ValueError("%s: (groups, rows, columns) with contiguous rows is wanted" % name)
-    return spgemm_weights(t.data_ptr(), t.shape[0], t.shape[1], t.shape[2], t.stride(0), max(t.stride(1), t.shape[2]), code, 0)
+    return spgemm_weights(t.data_ptr(), shape[0], shape[1], shape[2], step[0], max(step[1], shape[2]), code, 0)
 
 
-def _stream(stream, device):
+_ref = ctypes.byref
+
+
+def _call(name: str, device, stream, *args):
+    """Call an entry point with `device` current and the given or the current stream as last argument."""
     import torch
-    return _vp((stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
-
-
-def _ref(s):
-    return ctypes.byref(s)
+    index = device.index
+    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc:
+        _check(rc, name)
 
 
 def route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int = 1, groups_kept: int = 1,
@@ -128,7 +146,7 @@ def route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int 
     rule = spgemm_route_rule(top_k, _SCORES[score], groups, groups_kept, _GROUP_SCORES[group_score], bool(renormalise),
                              scale, 0)
     if bias is not None:
-        _want(bias, "bias", "float32")
+        _want(bias, "bias", torch.float32)
         if bias.numel() != logits.shape[1]:
             raise ValueError("bias: one value per expert is wanted")
     t, dev, k = logits.shape[0], logits.device, max(int(top_k), 1)
@@ -137,10 +155,8 @@ def route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int 
     offsets = torch.empty(logits.shape[1] + 1, dtype=torch.int32, device=dev)
     order = torch.empty(t * k, dtype=torch.int32, device=dev)
     position = torch.empty((t, k), dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        _check(load().spgemm_route(_ref(d), _ref(rule), bias.data_ptr() if bias is not None else None, ids.data_ptr(),
-                                   weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
-                                   _stream(stream, dev)), "spgemm_route")
+    _call("spgemm_route", dev, stream, _ref(d), _ref(rule), bias.data_ptr() if bias is not None else None,
+          ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), position.data_ptr())
     return Routing(ids, weights, offsets, order, position, rule)
 
 
@@ -150,15 +166,12 @@ def route_backward(logits, routing: Routing, grad_weights, *, stream=None):
     if routing.rule is None:
         raise ValueError("route_backward: the routing does not come from route()")
     d = _dense(logits, "logits")
-    _want(routing.ids, "ids", "int32")
-    _want(grad_weights, "grad_weights", "float32")
+    _want(grad_weights, "grad_weights", torch.float32)
     if grad_weights.shape != routing.ids.shape or logits.shape[0] != routing.tokens:
         raise ValueError("grad_weights: (tokens, top_k) is wanted")
     out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    with torch.cuda.device(logits.device):
-        _check(load().spgemm_route_backward(_ref(d), _ref(routing.rule), routing.ids.data_ptr(),
-                                            grad_weights.data_ptr(), _ref(_dense(out, "grad_logits")),
-                                            _stream(stream, logits.device)), "spgemm_route_backward")
+    _call("spgemm_route_backward", logits.device, stream, _ref(d), _ref(routing.rule), routing.ids.data_ptr(),
+          grad_weights.data_ptr(), _ref(_dense(out, "grad_logits")))
     return out
 
 
@@ -166,15 +179,14 @@ def group_rows(ids, groups: int, *, weights=None, stream=None) -> Routing:
     """The Routing of given ids (tokens, top_k) or (tokens,) int32, -1 for none; weights default to
     ones (see spgemm_group_rows)."""
     import torch
-    _want(ids, "ids", "int32")
+    _want(ids, "ids", torch.int32)
     ids = ids if ids.dim() == 2 else ids[:, None]
     dev = ids.device
     offsets = torch.empty(groups + 1, dtype=torch.int32, device=dev)
     order = torch.empty(ids.numel(), dtype=torch.int32, device=dev)
     position = torch.empty_like(ids)
-    with torch.cuda.device(dev):
-        _check(load().spgemm_group_rows(ids.data_ptr(), ids.numel(), groups, offsets.data_ptr(), order.data_ptr(),
-                                        position.data_ptr(), _stream(stream, dev)), "spgemm_group_rows")
+    _call("spgemm_group_rows", dev, stream, ids.data_ptr(), ids.numel(), groups, offsets.data_ptr(),
+          order.data_ptr(), position.data_ptr())
     if weights is None:
         weights = torch.ones(ids.shape, dtype=torch.float32, device=dev)
     return Routing(ids, weights, offsets, order, position)
@@ -186,50 +198,43 @@ def expert_product(x, w, routing: Routing, *, grouped: bool = False, out_dtype=N
     x (tokens, d), or (slots, d) in group order with ``grouped``; w (groups, n, d).  See
     spgemm_grouped_product."""
     import torch
-    g = routing._grouping()
+    g = routing._grouping
     dx, dw = _dense(x, "x"), _weights(w, "w")
     y = torch.empty((g.slots, w.shape[1]), dtype=out_dtype or x.dtype, device=x.device)
-    with torch.cuda.device(x.device):
-        _check(load().spgemm_grouped_product(_ref(g), _ref(dx), int(grouped), _ref(dw), _ref(_dense(y, "y")),
-                                             _stream(stream, x.device)), "spgemm_grouped_product")
+    _call("spgemm_grouped_product", x.device, stream, _ref(g), _ref(dx), int(grouped), _ref(dw), _ref(_dense(y, "y")))
     return y
 
 
 def expert_product_backward(dy, x, w, routing: Routing, *, need_dx: bool = True, need_dw: bool = True, stream=None):
     """(dx, dw) of ``expert_product`` with one row of x per token (see spgemm_grouped_product_backward)."""
     import torch
-    g = routing._grouping()
+    g = routing._grouping
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
     dw = torch.empty(w.shape, dtype=w.dtype, device=x.device) if need_dw else None
-    with torch.cuda.device(x.device):
-        _check(load().spgemm_grouped_product_backward(
-            _ref(g), _ref(_dense(dy, "dy")), _ref(_dense(x, "x")), _ref(_weights(w, "w")),
-            _ref(_dense(dx, "dx")) if need_dx else None, _ref(_weights(dw, "dw")) if need_dw else None,
-            _stream(stream, x.device)), "spgemm_grouped_product_backward")
+    _call("spgemm_grouped_product_backward", x.device, stream, _ref(g), _ref(_dense(dy, "dy")), _ref(_dense(x, "x")),
+          _ref(_weights(w, "w")), _ref(_dense(dx, "dx")) if need_dx else None,
+          _ref(_weights(dw, "dw")) if need_dw else None)
     return dx, dw
 
 
 def combine(y, routing: Routing, *, out_dtype=None, stream=None):
     """Weighted sum of a token's rows: (tokens, y.shape[1]) (see spgemm_combine)."""
     import torch
-    g = routing._grouping()
+    g = routing._grouping
     out = torch.empty((routing.tokens, y.shape[1]), dtype=out_dtype or y.dtype, device=y.device)
-    with torch.cuda.device(y.device):
-        _check(load().spgemm_combine(_ref(g), routing.weights.data_ptr(), _ref(_dense(y, "y")),
-                                     _ref(_dense(out, "out")), _stream(stream, y.device)), "spgemm_combine")
+    _call("spgemm_combine", y.device, stream, _ref(g), routing.weights.data_ptr(), _ref(_dense(y, "y")),
+          _ref(_dense(out, "out")))
     return out
 
 
 def combine_backward(dout, y, routing: Routing, *, stream=None):
     """(dy, dweights) of ``combine`` (see spgemm_combine_backward)."""
     import torch
-    g = routing._grouping()
+    g = routing._grouping
     dy = torch.empty(y.shape, dtype=y.dtype, device=y.device)
     dweights = torch.empty(routing.ids.shape, dtype=torch.float32, device=y.device)
-    with torch.cuda.device(y.device):
-        _check(load().spgemm_combine_backward(_ref(g), routing.weights.data_ptr(), _ref(_dense(dout, "dout")),
-                                              _ref(_dense(y, "y")), _ref(_dense(dy, "dy")), dweights.data_ptr(),
-                                              _stream(stream, y.device)), "spgemm_combine_backward")
+    _call("spgemm_combine_backward", y.device, stream, _ref(g), routing.weights.data_ptr(),
+          _ref(_dense(dout, "dout")), _ref(_dense(y, "y")), _ref(_dense(dy, "dy")), dweights.data_ptr())
     return dy, dweights
 
 
@@ -237,12 +242,10 @@ def experts(x, w_up, w_down, routing: Routing, *, stream=None):
     """A gated expert layer, (tokens, d) -> (tokens, w_down.shape[1]): w_up (groups, 2 * hidden, d)
     holds the gate's rows, then up's; w_down (groups, n, hidden).  See spgemm_experts."""
     import torch
-    g = routing._grouping()
+    g = routing._grouping
     out = torch.empty((x.shape[0], w_down.shape[1]), dtype=x.dtype, device=x.device)
-    with torch.cuda.device(x.device):
-        _check(load().spgemm_experts(_ref(g), routing.weights.data_ptr(), _ref(_dense(x, "x")),
-                                     _ref(_weights(w_up, "w_up")), _ref(_weights(w_down, "w_down")),
-                                     _ref(_dense(out, "out")), _stream(stream, x.device)), "spgemm_experts")
+    _call("spgemm_experts", x.device, stream, _ref(g), routing.weights.data_ptr(), _ref(_dense(x, "x")),
+          _ref(_weights(w_up, "w_up")), _ref(_weights(w_down, "w_down")), _ref(_dense(out, "out")))
     return out
 
 
@@ -252,19 +255,17 @@ def adapted_product(x, w, a, b, ids, scale=None, *, stream=None):
     x (tokens, d), w (n, d), a (adapters, rank, d), b (adapters, n, rank), scale (adapters)
     float32.  See spgemm_adapted_product."""
     import torch
-    _want(ids, "ids", "int32")
+    _want(ids, "ids", torch.int32)
     if ids.numel() != x.shape[0]:
         raise ValueError("ids: one per row of x is wanted")
     if scale is not None:
-        _want(scale, "scale", "float32")
+        _want(scale, "scale", torch.float32)
         if scale.numel() != a.shape[0]:
             raise ValueError("scale: one value per adapter is wanted")
     y = torch.empty((x.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
-    with torch.cuda.device(x.device):
-        _check(load().spgemm_adapted_product(_ref(_dense(x, "x")), _ref(_dense(w, "w")), _ref(_weights(a, "a")),
-                                             _ref(_weights(b, "b")), ids.data_ptr(),
-                                             scale.data_ptr() if scale is not None else None, _ref(_dense(y, "y")),
-                                             _stream(stream, x.device)), "spgemm_adapted_product")
+    _call("spgemm_adapted_product", x.device, stream, _ref(_dense(x, "x")), _ref(_dense(w, "w")),
+          _ref(_weights(a, "a")), _ref(_weights(b, "b")), ids.data_ptr(),
+          scale.data_ptr() if scale is not None else None, _ref(_dense(y, "y")))
     return y
 
 
