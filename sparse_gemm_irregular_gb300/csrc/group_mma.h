@@ -23,6 +23,7 @@ struct MmaArgs {
   const float* scale;      // per group (scatter)
   const int32_t* ids;      // Adapted: the adapter of each row
   int adapters, rank;
+  int split;               // blocks that share a tile's contracted range
   uint32_t* err;
 };
 

@@ -33,7 +33,8 @@ class Scratch {
   }
   void* get(int64_t bytes) {
     void* p = nullptr;
-    if (n_ == kMost || cudaMallocFromPoolAsync(&p, static_cast<size_t>(std::max<int64_t>(bytes, 16)), pool_, s_) !=
+    if (bytes == 0) return p;
+    if (n_ == kMost || cudaMallocFromPoolAsync(&p, static_cast<size_t>(bytes), pool_, s_) !=
                            cudaSuccess) {
       cudaGetLastError();
       ok_ = false;

@@ -22,10 +22,15 @@
 // end (Dw, where they are contracted, on both operands, so that a NaN there cannot leak) and, in Adapted,
 // the tokens of other adapters.
 //
-// Six warps: a producer (copies), an issuer (matrix instructions, one thread), four that empty
-// the accumulators while the next tile is computed into the other half of tensor memory.  The
-// accumulator's lanes are consecutive columns of the output, so a warp's store is contiguous.
-// Persistent blocks; tiles of one group that share its rows are neighbours.
+// Nine warps: four producers (a warp issues its lanes' copies one after the other, so a slice's copies are
+// dealt over four), an issuer (matrix instructions, one thread), four that empty the accumulators while
+// the next tile is computed into the other half of tensor memory.  The accumulator's lanes are
+// consecutive columns of the output, so a warp's store is contiguous.  Persistent blocks; tiles of one group
+// that share its rows are neighbours.
+//
+// Split: where there are fewer tiles than half the SMs, the blocks of a cluster share a tile's contracted
+// range, send each other their part of the sums through distributed shared memory and add them up
+// in the order of their ranks.
 //
 // Every wait is bounded: a role that gives up sets the status word, the others see it, copies in
 // flight are drained, tensor memory is freed, the kernel returns.
@@ -38,13 +43,15 @@ namespace sg {
 
 namespace {
 
-constexpr int kThreads = 192;      // producer, issuer, four epilogue warps
+constexpr int kProducers = 4;      // producer warps; warp 4 issues, warps 5 to 8 are the epilogue
+constexpr int kThreads = 288;
 constexpr int kEpilogue = 128;
 constexpr int kDeep = 64;          // contracted elements of a slice: 128 bytes, one swizzle row
 constexpr int kMaxStages = 12;
 constexpr int kABytes = 128 * 128; // A's part of a stage: 128 rows of 128 bytes
 constexpr int kBox = 64 * 128;     // a 64 x 64 box
 constexpr int kTmemCols = 512;
+constexpr int kSplitTile = 64;     // widest tile that is split
 constexpr int kSmemMost = 227 * 1024;
 
 struct Control {
@@ -74,15 +81,17 @@ struct MmaMaps {
   CUtensorMap a, b, c, d;  // Forward, Dx: weights, rows; Dw: x, dy, then rows of dy and of x; Adapted: w, x, b[i], v rows
 };
 
-template <int MODE, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant__ MmaMaps maps,
+template <int MODE, bool PAIR, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __grid_constant__ MmaMaps maps,
                                                            const __grid_constant__ MmaArgs p) {
   using namespace tc;
   extern __shared__ char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   Control& c = *reinterpret_cast<Control*>(smem_raw + (base - smem_u32(smem_raw)) + p.stages * p.stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;          // block of the pair
+  const int part = SPLIT ? static_cast<int>(cluster_rank()) : 0, parts = SPLIT ? p.split : 1;  // of the contracted range
+  const uint32_t tmem_cols = SPLIT ? kSplitTile : kTmemCols;
   constexpr int kSide = PAIR ? 2 : 1;
   constexpr bool kDw = MODE == kMmaDw;
   volatile int* failed = &c.failed;
@@ -101,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
     c.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc<PAIR>(smem_u32(&c.tmem), kTmemCols);
+  if (warp == kProducers) tmem_alloc<PAIR>(smem_u32(&c.tmem), tmem_cols);
   pdl_wait();
   pdl_go();
   // offsets are used as a non-decreasing sequence inside [0, slots], whatever the array holds
@@ -134,7 +143,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
   const int mt = (p.m + m_per_tile - 1) / m_per_tile;
   const int nt = kDw ? (p.n + p.tile_n - 1) / p.tile_n : 0;
   const int64_t total = kDw ? static_cast<int64_t>(p.groups) * mt * nt : static_cast<int64_t>(c.tiles[p.groups]) * mt;
-  const int64_t worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, workers = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const int64_t worker = PAIR ? blockIdx.x >> 1 : SPLIT ? blockIdx.x / parts : blockIdx.x;
+  const int64_t workers = PAIR ? gridDim.x >> 1 : SPLIT ? gridDim.x / parts : gridDim.x;
 
   auto tile_at = [&](int64_t i) {
     Tile t;
@@ -167,8 +177,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
   // columns of the instruction: a multiple of 16 per block of the pair
   auto columns = [&](int n) { return (n + 16 * kSide - 1) / (16 * kSide) * (16 * kSide); };
 
-  if (warp == 0) {
-    // ---- producer ------------------------------------------------------------------------------
+  if (warp < kProducers) {
+    // ---- producers ---------------------------------------------------------------------------------
     int s = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -176,31 +186,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
       const Tile t = tile_at(i);
       const int cols = columns(t.n), half = cols / kSide;
       const int jr = t.j0 + static_cast<int>(rank) * half;  // first N index of this block
-      // rows that this lane gathers: quads `lane` and `lane + 32` of this block's N side
-      int4 quad[2];
-      if ((MODE == kMmaForward || MODE == kMmaGated) && p.gather) {
+      // four rows that this lane gathers: a quad of this block's N side
+      const int quad = lane * kProducers + warp;
+      const bool gather = (MODE == kMmaForward || MODE == kMmaGated) && p.gather;
+      int4 mine = make_int4(0, 0, 0, 0);
+      if (gather && quad * 4 < half) {
+        int r[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          int r[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = jr + (lane + 32 * h) * 4 + e;
-            const int slot = j < t.j0 + t.n ? p.order[j] : -1;
-            const int row = slot >= 0 ? slot / p.top_k : p.rows;
-            r[e] = min(row, p.rows);
-          }
-          quad[h] = make_int4(r[0], r[1], r[2], r[3]);
+        for (int e = 0; e < 4; ++e) {
+          const int j = jr + quad * 4 + e;
+          const int slot = j < t.j0 + t.n ? p.order[j] : -1;
+          r[e] = slot >= 0 ? min(slot / p.top_k, p.rows) : p.rows;
         }
+        mine = make_int4(r[0], r[1], r[2], r[3]);
       }
-      // one slice: waits for a free stage and announces its bytes; returns the stage's address
+      // one slice: waits for a free stage and announces its bytes; returns the stage's address.  A copy of
+      // another warp may be done before the bytes are announced: the announcement is the barrier's only arrival
       auto open = [&](uint32_t bytes, bool last) -> uint32_t {
         ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err);
         ok = __all_sync(0xffffffffu, ok);
-        if (ok && lane == 0) {
+        if (ok && warp == 0 && lane == 0) {
           c.last[s] = last ? 1 : 0;
           if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), bytes * kSide);
         }
-        __syncwarp();
         return base + s * p.stage_bytes;
       };
       auto bar = [&]() { return PAIR ? map_rank(smem_u32(&c.full[s]), 0) : smem_u32(&c.full[s]); };
@@ -210,30 +218,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
           phase ^= 1u;
         }
       };
+      const int slices = (t.k + kDeep - 1) / kDeep;
+      const int q0 = SPLIT ? slices * part / parts : 0, q1 = SPLIT ? slices * (part + 1) / parts : slices;
 
       if (kDw) {
-        const int slices = (t.k + kDeep - 1) / kDeep;
         const int nb = (half + 63) / 64;  // 64-column blocks of dy
         for (int q = 0; q < slices && ok; ++q) {
-          const uint32_t a = open(static_cast<uint32_t>((2 + nb) * kBox), q + 1 == slices), b = a + kABytes;
+          const uint32_t a = open(static_cast<uint32_t>((2 + nb) * kBox), q + 1 == slices);
           if (!ok) break;
           const uint32_t fb = bar();
           const int m0 = t.m0 + static_cast<int>(rank) * 128, k0 = q * kDeep;
-          if (k0 + kDeep <= t.k) {
-            if (lane < 2) load_2d<PAIR>(a + lane * kBox, &maps.a, m0 + lane * 64, t.k0 + k0, fb);
-            else if (lane - 2 < nb) load_2d<PAIR>(b + (lane - 2) * kBox, &maps.b, jr + (lane - 2) * 64, t.k0 + k0, fb);
-          } else {  // the group ends inside the slice: rows past it read as zeros, on both sides
-            int r[4];
+          // box u: columns of x (0, 1), then of dy
+          const bool whole = k0 + kDeep <= t.k;
+          const int u = whole ? quad : quad >> 4;
+          const uint32_t dst = a + (u < 2 ? u * kBox : kABytes + (u - 2) * kBox);
+          const int col = u < 2 ? m0 + u * 64 : jr + (u - 2) * 64;
+          if (u < 2 + nb) {
+            if (whole) {
+              load_2d<PAIR>(dst, u < 2 ? &maps.a : &maps.b, col, t.k0 + k0, fb);
+            } else {  // the group ends inside the slice: rows past it read as zeros, on both sides
+              int r[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int o = k0 + (lane & 15) * 4 + e;
-              r[e] = o < t.k ? t.k0 + o : p.slots;
+              for (int e = 0; e < 4; ++e) {
+                const int o = k0 + (quad & 15) * 4 + e;
+                r[e] = o < t.k ? t.k0 + o : p.slots;
+              }
+              load_rows4<PAIR>(dst + (quad & 15) * 512, u < 2 ? &maps.d : &maps.c, col,
+                               make_int4(r[0], r[1], r[2], r[3]), fb);
             }
-            const int4 rows = make_int4(r[0], r[1], r[2], r[3]);
-            const uint32_t in_box = (lane & 15) * 512;
-            load_rows4<PAIR>(a + (lane >> 4) * kBox + in_box, &maps.d, m0 + (lane >> 4) * 64, rows, fb);
-            for (int blk = lane >> 4; blk < nb; blk += 2)
-              load_rows4<PAIR>(b + blk * kBox + in_box, &maps.c, jr + blk * 64, rows, fb);
           }
           close();
         }
@@ -241,9 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
       }
 
       const int boxes = (half + p.box_rows - 1) / p.box_rows;
-      const bool gather = (MODE == kMmaForward || MODE == kMmaGated) && p.gather;
       const uint32_t bytes = kABytes + (gather ? half : boxes * p.box_rows) * 128;
-      const int slices = (t.k + kDeep - 1) / kDeep;
       // Adapted: the adapters of the tile's tokens (lane, lane + 32, ...), in ascending order
       int ids[8];
       auto id_of = [&](int j) {
@@ -257,55 +267,56 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
           if (ids[e] > before) least = min(least, static_cast<uint32_t>(ids[e]));
         return static_cast<int>(__reduce_min_sync(0xffffffffu, least));  // -1: none left
       };
+      // the next adapter of this block: all of them, or (Split) every parts-th
+      auto mine_after = [&](int before, int skip) {
+        int id = following(before);
+        for (int e = 0; e < skip && id >= 0; ++e) id = following(id);
+        return id;
+      };
       int adapter = -1;
       if (MODE == kMmaAdapted) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) ids[e] = lane + 32 * e < t.n ? id_of(t.j0 + lane + 32 * e) : -1;
-        adapter = following(-1);
+        adapter = mine_after(-1, part);
       }
-      for (int q = 0; q < slices && ok; ++q) {
-        const uint32_t a = open(bytes, q + 1 == slices && adapter < 0), b = a + kABytes;
+      // A's two boxes go to the last lanes of the first two warps
+      const int box = lane == 31 ? warp : 2;
+      for (int q = q0; q < q1 && ok; ++q) {
+        const uint32_t a = open(bytes, q + 1 == q1 && adapter < 0), b = a + kABytes;
         if (!ok) break;
         const uint32_t fb = bar();
         const int k0 = q * kDeep;
-        if (lane < 2) {
+        if (box < 2) {
           const int m0 = t.m0 + static_cast<int>(rank) * (MODE == kMmaGated ? 64 : 128);
-          if (MODE == kMmaDx) load_3d<PAIR>(a + lane * kBox, &maps.a, m0 + lane * 64, k0, t.g, fb);
-          else if (MODE == kMmaGated) load_3d<PAIR>(a + lane * kBox, &maps.a, k0, m0 + lane * p.m, t.g, fb);
-          else load_3d<PAIR>(a + lane * kBox, &maps.a, k0, m0 + lane * 64, t.g, fb);
+          if (MODE == kMmaDx) load_3d<PAIR>(a + box * kBox, &maps.a, m0 + box * 64, k0, t.g, fb);
+          else if (MODE == kMmaGated) load_3d<PAIR>(a + box * kBox, &maps.a, k0, m0 + box * p.m, t.g, fb);
+          else load_3d<PAIR>(a + box * kBox, &maps.a, k0, m0 + box * 64, t.g, fb);
         }
         if (gather) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if ((lane + 32 * h) * 4 < half) load_rows4<PAIR>(b + (lane + 32 * h) * 512, &maps.b, k0, quad[h], fb);
-        } else if (lane < boxes) {
-          load_2d<PAIR>(b + lane * p.box_rows * 128, &maps.b, k0, jr + lane * p.box_rows, fb);
+          if (quad * 4 < half) load_rows4<PAIR>(b + quad * 512, &maps.b, k0, mine, fb);
+        } else {
+          // B's boxes start at the third warp
+          const int u = lane * kProducers + ((warp + 2) & 3);
+          if (u < boxes) load_2d<PAIR>(b + u * p.box_rows * 128, &maps.b, k0, jr + u * p.box_rows, fb);
         }
         close();
       }
       // then, per adapter, its b against the v rows of its own tokens (the others' read as zeros)
       while (MODE == kMmaAdapted && ok && adapter >= 0) {
-        const int after = following(adapter);
-        int4 rows[2];
+        const int after = mine_after(adapter, parts - 1);
+        int r[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          int r[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = jr + (lane + 32 * h) * 4 + e;
-            r[e] = id_of(j) == adapter ? j : p.rows;
-          }
-          rows[h] = make_int4(r[0], r[1], r[2], r[3]);
+        for (int e = 0; e < 4; ++e) {
+          const int j = jr + quad * 4 + e;
+          r[e] = quad * 4 < half && id_of(j) == adapter ? j : p.rows;
         }
         for (int k0 = 0; k0 < p.rank && ok; k0 += kDeep) {
           const uint32_t a = open(kABytes + half * 128, k0 + kDeep >= p.rank && after < 0), b = a + kABytes;
           if (!ok) break;
           const uint32_t fb = bar();
-          if (lane < 2)
-            load_3d<PAIR>(a + lane * kBox, &maps.c, k0, t.m0 + static_cast<int>(rank) * 128 + lane * 64, adapter, fb);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if ((lane + 32 * h) * 4 < half) load_rows4<PAIR>(b + (lane + 32 * h) * 512, &maps.d, k0, rows[h], fb);
+          if (box < 2)
+            load_3d<PAIR>(a + box * kBox, &maps.c, k0, t.m0 + static_cast<int>(rank) * 128 + box * 64, adapter, fb);
+          if (quad * 4 < half) load_rows4<PAIR>(b + quad * 512, &maps.d, k0, make_int4(r[0], r[1], r[2], r[3]), fb);
           close();
         }
         adapter = after;
@@ -321,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
         }
       }
     }
-  } else if (warp == 1 && rank == 0) {
+  } else if (warp == kProducers && rank == 0) {
     // ---- issuer ----------------------------------------------------------------------------------
     int s = 0, it = 0;
     uint32_t phase = 0;
@@ -356,12 +367,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
         ++it;
       }
       if (*failed) {
-        commit<false>(smem_u32(&c.drain));
+        commit<PAIR>(smem_u32(&c.drain));
         mbar_drain(smem_u32(&c.drain), 0);
       }
     }
     __syncwarp();
-  } else if (warp >= 2) {
+  } else if (warp > kProducers) {
     // ---- epilogue ----------------------------------------------------------------------------------
     const int quarter = warp & 3;  // the lanes of tensor memory that this warp can read
     const int ml = quarter * 32 + lane;
@@ -374,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
         ok = mbar_wait(smem_u32(&c.acc_full[it & 1]), (it >> 1) & 1, failed, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (MODE == kMmaGated) {  // the warps meet below: they go on together or not at all
-          if (warp == 2 && lane == 0) c.go[it & 1] = ok;
+          if (warp == kProducers + 1 && lane == 0) c.go[it & 1] = ok;
           asm volatile("bar.sync 1, %0;" ::"n"(kEpilogue) : "memory");
           if (!c.go[it & 1]) break;
         } else if (!ok) {
@@ -382,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
         }
         fence_after();
       }
+      if (SPLIT) break;  // the sums of the cluster's blocks meet below
       const uint32_t acc = tmem + (it & 1) * p.tile_n + (static_cast<uint32_t>(quarter * 32) << 16);
       for (int j = 0; j < t.n; j += 32) {
         uint32_t r[32];
@@ -452,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
     // rows behind the last group
     if ((MODE == kMmaForward || MODE == kMmaGated) && !p.scatter) {
       for (int64_t r = c.first[p.groups] + blockIdx.x; r < p.slots; r += gridDim.x)
-        for (int m = static_cast<int>(threadIdx.x) - 64; m < p.m; m += kEpilogue) {
+        for (int m = static_cast<int>(threadIdx.x) - (kThreads - kEpilogue); m < p.m; m += kEpilogue) {
           const int64_t o = r * p.out_stride + m;
           if (p.out_type == SPGEMM_DTYPE_F32) static_cast<float*>(p.out)[o] = 0.0f;
           else static_cast<uint16_t*>(p.out)[o] = 0;
@@ -461,9 +473,55 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_mma(const __grid_constant
   }
   fence_before();
   __syncthreads();
+  if (SPLIT) {
+    // Every block has its part of the sums; the stages are idle in all of them.  Block q of the cluster adds
+    // up columns [q, q + 1) * width of the tile: buf[source][column][lane].
+    cluster_sync();
+    fence_after();
+    const int width = p.tile_n / parts;
+    const bool there = worker < total && !*failed;
+    const Tile t = there ? tile_at(worker) : Tile{};
+    const int ml = (warp & 3) * 32 + lane;
+    if (there && warp > kProducers) {
+      const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      for (int j = 0; j < t.n; j += 32) {
+        uint32_t r[32];
+        tmem_load32(acc + j, r);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (j + e < t.n) {
+            const int owner = (j + e) / width, col = (j + e) - owner * width;
+            store_cluster(map_rank(base + ((part * width + col) * 128 + ml) * 4, owner), r[e]);
+          }
+      }
+    }
+    cluster_sync();
+    if (there && warp > kProducers) {
+      const float* buf = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)));
+      const int m = t.m0 + ml;
+      for (int col = 0; col < width && part * width + col < t.n; ++col) {
+        float sum = 0.0f;
+        for (int q = 0; q < parts; ++q) sum += buf[(q * width + col) * 128 + ml];
+        const int64_t j = t.j0 + part * width + col;
+        int64_t row = j;
+        if (MODE == kMmaForward && p.scatter) {
+          row = max(p.order[j], 0) / p.top_k;
+          if (p.scale) sum *= p.scale[t.g];
+        }
+        if (m < p.m) {
+          const int64_t o = row * p.out_stride + m;
+          if (p.out_type == SPGEMM_DTYPE_F32) static_cast<float*>(p.out)[o] = sum;
+          else if (p.out_type == SPGEMM_DTYPE_BF16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(sum);
+          else static_cast<__half*>(p.out)[o] = __float2half_rn(sum);
+        }
+      }
+    }
+    fence_before();
+    __syncthreads();
+  }
   if (PAIR) cluster_sync();
   fence_after();
-  if (warp == 1) tmem_free<PAIR>(tmem, kTmemCols);
+  if (warp == kProducers) tmem_free<PAIR>(tmem, tmem_cols);
 }
 
 namespace {
@@ -519,16 +577,20 @@ int sm_count() {
   return sms;
 }
 
-template <int MODE, bool PAIR>
-bool launch(const MmaMaps& maps, MmaArgs a, cudaStream_t s) {
+template <int MODE, bool PAIR, bool SPLIT>
+bool launch(const MmaMaps& maps, MmaArgs a, int64_t grid, cudaStream_t s) {
   a.stage_bytes = kABytes + std::max(a.tile_n / (PAIR ? 2 : 1), MODE == kMmaDw ? 64 : 16) * 128;
   const int control = static_cast<int>(sizeof(Control));
-  a.stages = std::min<int>(kMaxStages, (kSmemMost - 1024 - control) / a.stage_bytes);
+  // split: two blocks per SM, and the stages hold the sums that meet there
+  const int most = SPLIT ? kSmemMost / 2 - 1024 : kSmemMost;
+  a.stages = std::min<int>(kMaxStages, (most - 1024 - control) / a.stage_bytes);
   const int smem = 1024 + a.stages * a.stage_bytes + control;
-  auto kern = k_group_mma<MODE, PAIR>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+  auto kern = k_group_mma<MODE, PAIR, SPLIT>;
+  static const cudaError_t raised =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+  if (raised != cudaSuccess) return false;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(sm_count() / 2 * 2));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
@@ -536,11 +598,32 @@ bool launch(const MmaMaps& maps, MmaArgs a, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {PAIR ? 2u : 1u, 1u, 1u};
+  attr[1].val.clusterDim = {SPLIT ? static_cast<unsigned>(a.split) : PAIR ? 2u : 1u, 1u, 1u};
   cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 2 : 1;
+  cfg.numAttrs = PAIR || SPLIT ? 2 : 1;
   note_launch();
   return cudaLaunchKernelEx(&cfg, kern, maps, a) == cudaSuccess;
+}
+
+template <int MODE>
+bool launch_whole(const MmaMaps& maps, const MmaArgs& a, cudaStream_t s) {
+  return launch<MODE, false, false>(maps, a, sm_count() / 2 * 2, s);
+}
+
+// Split when the tiles (at most `tiles`) leave more than half the SMs idle: as many blocks per tile as
+// fit the SMs, up to 8, with at least two slices each.
+template <int MODE>
+bool launch_split(const MmaMaps& maps, MmaArgs a, int64_t tiles, cudaStream_t s) {
+  const int slices = (a.depth + kDeep - 1) / kDeep;
+  a.split = 1;
+  while (a.split < 8 && tiles * a.split * 2 <= sm_count() && a.split * 4 <= slices) a.split *= 2;
+  if (a.split == 1 || a.tile_n > kSplitTile || a.tile_n < a.split) return launch_whole<MODE>(maps, a, s);
+  return launch<MODE, false, true>(maps, a, tiles * a.split, s);
+}
+
+// most tiles on the N side: every group may end in a part of one
+int64_t most_tiles(const spgemm_grouping& g, int tile_n) {
+  return g.slots / tile_n + std::min<int64_t>(g.groups, g.slots);
 }
 
 // N-side tile: a power of two of about twice the average group, so that most groups are one tile
@@ -566,7 +649,7 @@ bool aligned(const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>
 
 }  // namespace
 
-bool mma_gathers(const spgemm_grouping& g) { return pick_tile(g.slots, g.groups, 256) <= 32; }
+bool mma_gathers(const spgemm_grouping& g) { return pick_tile(g.slots, g.groups, 256) <= 128; }
 
 bool mma_takes(const spgemm_dense& m) { return m.dtype != SPGEMM_DTYPE_F32 && aligned(m.data, m.stride) && m.rows < (1LL << 31) && m.cols < (1LL << 31); }
 bool mma_takes(const spgemm_weights& w) {
@@ -590,7 +673,7 @@ bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool ga
   MmaMaps maps;
   if (!encode_weights(&maps.a, w) || !encode_rows(&maps.b, x, gather ? 1 : a.box_rows)) return false;
   maps.c = maps.d = maps.b;
-  return gated ? launch<kMmaGated, false>(maps, a, s) : launch<kMmaForward, false>(maps, a, s);
+  return gated ? launch_whole<kMmaGated>(maps, a, s) : launch_whole<kMmaForward>(maps, a, s);
 }
 
 bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_weights& w, float* dx,
@@ -608,7 +691,7 @@ bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
   MmaMaps maps;
   if (!encode_weights(&maps.a, w) || !encode_rows(&maps.b, dy, a.box_rows)) return false;
   maps.c = maps.d = maps.b;
-  return launch<kMmaDx, false>(maps, a, s);
+  return launch_whole<kMmaDx>(maps, a, s);
 }
 
 bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_dense& x, const spgemm_weights& dw,
@@ -625,7 +708,7 @@ bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
   if (!encode_rows(&maps.a, x, 64) || !encode_rows(&maps.b, dy, 64) || !encode_rows(&maps.c, dy, 1) ||
       !encode_rows(&maps.d, x, 1))
     return false;
-  return launch<kMmaDw, false>(maps, a, s);
+  return launch_whole<kMmaDw>(maps, a, s);
 }
 
 bool launch_mma_shrink(const spgemm_grouping& g, const spgemm_dense& x, const spgemm_weights& a_w, const float* scale,
@@ -644,7 +727,7 @@ bool launch_mma_shrink(const spgemm_grouping& g, const spgemm_dense& x, const sp
   MmaMaps maps;
   if (!encode_weights(&maps.a, a_w) || !encode_rows(&maps.b, x, 1)) return false;
   maps.c = maps.d = maps.b;
-  return launch<kMmaForward, false>(maps, a, s);
+  return launch_split<kMmaForward>(maps, a, most_tiles(g, a.tile_n) * ceil_div(a.m, 128), s);
 }
 
 bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spgemm_weights& b, const int32_t* ids,
@@ -666,7 +749,7 @@ bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spge
   if (!encode_weights(&maps.a, shared) || !encode_rows(&maps.b, x, a.box_rows) || !encode_weights(&maps.c, b) ||
       !encode_rows(&maps.d, v, 1))
     return false;
-  return launch<kMmaAdapted, false>(maps, a, s);
+  return launch_split<kMmaAdapted>(maps, a, ceil_div(x.rows, a.tile_n) * ceil_div(a.m, 128), s);
 }
 
 }  // namespace sg

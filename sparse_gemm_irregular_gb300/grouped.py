@@ -45,9 +45,18 @@ class Routing:
                 raise ValueError("routing: ids, weights, order and position want tokens * top_k entries each")
         if self.ids.dim() != 2:
             raise ValueError("ids: (tokens, top_k) is wanted")
-        object.__setattr__(self, "_grouping", spgemm_grouping(n, self.ids.shape[1], self.offsets.numel() - 1,
-                                                              self.offsets.data_ptr(), self.order.data_ptr(),
-                                                              self.position.data_ptr()))
+
+    @classmethod
+    def _made(cls, ids, weights, offsets, order, position, rule=None) -> "Routing":
+        """From arrays that this module allocated: nothing to check."""
+        r = cls.__new__(cls)
+        r.__dict__.update(ids=ids, weights=weights, offsets=offsets, order=order, position=position, rule=rule)
+        return r
+
+    @property
+    def _grouping(self) -> spgemm_grouping:
+        return spgemm_grouping(self.ids.numel(), self.ids.shape[1], self.offsets.numel() - 1, self.offsets.data_ptr(),
+                               self.order.data_ptr(), self.position.data_ptr())
 
     @property
     def tokens(self) -> int:
@@ -150,14 +159,14 @@ def route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int 
         if bias.numel() != logits.shape[1]:
             raise ValueError("bias: one value per expert is wanted")
     t, dev, k = logits.shape[0], logits.device, max(int(top_k), 1)
-    ids = torch.empty((t, k), dtype=torch.int32, device=dev)
+    n = t * k
     weights = torch.empty((t, k), dtype=torch.float32, device=dev)
-    offsets = torch.empty(logits.shape[1] + 1, dtype=torch.int32, device=dev)
-    order = torch.empty(t * k, dtype=torch.int32, device=dev)
-    position = torch.empty((t, k), dtype=torch.int32, device=dev)
+    whole = torch.empty(3 * n + logits.shape[1] + 1, dtype=torch.int32, device=dev)  # one allocation for four arrays
+    ids, position = whole.as_strided((t, k), (k, 1)), whole.as_strided((t, k), (k, 1), n)
+    order, offsets = whole.as_strided((n,), (1,), 2 * n), whole.as_strided((logits.shape[1] + 1,), (1,), 3 * n)
     _call("spgemm_route", dev, stream, _ref(d), _ref(rule), bias.data_ptr() if bias is not None else None,
           ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), position.data_ptr())
-    return Routing(ids, weights, offsets, order, position, rule)
+    return Routing._made(ids, weights, offsets, order, position, rule)
 
 
 def route_backward(logits, routing: Routing, grad_weights, *, stream=None):
@@ -189,7 +198,10 @@ def group_rows(ids, groups: int, *, weights=None, stream=None) -> Routing:
           order.data_ptr(), position.data_ptr())
     if weights is None:
         weights = torch.ones(ids.shape, dtype=torch.float32, device=dev)
-    return Routing(ids, weights, offsets, order, position)
+    _want(weights, "weights", torch.float32)
+    if weights.numel() != ids.numel():
+        raise ValueError("weights: one per id is wanted")
+    return Routing._made(ids, weights, offsets, order, position)
 
 
 def expert_product(x, w, routing: Routing, *, grouped: bool = False, out_dtype=None, stream=None):
