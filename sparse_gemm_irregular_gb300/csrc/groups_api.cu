@@ -356,7 +356,8 @@ int spgemm_grouped_status(void* stream) {
   if (!err) return SPGEMM_OK;
   SG_TRY(check_cuda(cudaMemsetAsync(p, 0, sizeof(err), st), "grouped status"));
   SG_TRY(check_cuda(cudaStreamSynchronize(st), "grouped status"));
-  set_last_error((err & kErrTimeout) ? "a wait for an asynchronous copy expired" : "an id is outside its range");
+  if (err & kErrTimeout) set_last_error("a wait expired (sites " + std::to_string(err >> 8) + ")");
+  else set_last_error("an id is outside its range");
   return SPGEMM_ERR_DEVICE;
 }
 

@@ -51,6 +51,7 @@ constexpr int kMaxStages = 12;
 constexpr int kABytes = 128 * 128; // A's part of a stage: 128 rows of 128 bytes
 constexpr int kBox = 64 * 128;     // a 64 x 64 box
 constexpr int kTmemCols = 512;
+constexpr int kPairTile = 256;     // narrowest tile that two blocks share
 constexpr int kSplitTile = 64;     // widest tile that is split
 constexpr int kSmemMost = 227 * 1024;
 
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
     c.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (PAIR) cluster_sync();  // both blocks run before one allocates in both
   if (warp == kProducers) tmem_alloc<PAIR>(smem_u32(&c.tmem), tmem_cols);
   pdl_wait();
   pdl_go();
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
       // one slice: waits for a free stage and announces its bytes; returns the stage's address.  A copy of
       // another warp may be done before the bytes are announced: the announcement is the barrier's only arrival
       auto open = [&](uint32_t bytes, bool last) -> uint32_t {
-        ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err);
+        ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
         ok = __all_sync(0xffffffffu, ok);
         if (ok && warp == 0 && lane == 0) {
           c.last[s] = last ? 1 : 0;
@@ -344,11 +346,11 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         if (t.k == 0) continue;  // an empty group's gradient: the epilogue writes zeros
         const uint32_t idesc = instruction(p.bf16, kARows, kBRows, 128 * kSide, columns(t.n));
         const uint32_t acc = tmem + (it & 1) * p.tile_n;
-        ok = mbar_wait(smem_u32(&c.acc_empty[it & 1]), ((it >> 1) & 1) ^ 1u, failed, p.err);
+        ok = mbar_wait(smem_u32(&c.acc_empty[it & 1]), ((it >> 1) & 1) ^ 1u, failed, p.err, 2u);
         fence_after();
         bool last = false;
         for (bool first = true; ok && !last; first = false) {
-          ok = mbar_wait(smem_u32(&c.full[s]), phase, failed, p.err);
+          ok = mbar_wait(smem_u32(&c.full[s]), phase, failed, p.err, 4u);
           if (!ok) break;
           fence_after();
           last = c.last[s] != 0;
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
       const Tile t = tile_at(i);
       const bool zero = t.k == 0;
       if (!zero) {
-        ok = mbar_wait(smem_u32(&c.acc_full[it & 1]), (it >> 1) & 1, failed, p.err);
+        ok = mbar_wait(smem_u32(&c.acc_full[it & 1]), (it >> 1) & 1, failed, p.err, 8u);
         ok = __all_sync(0xffffffffu, ok);
         if (MODE == kMmaGated) {  // the warps meet below: they go on together or not at all
           if (warp == kProducers + 1 && lane == 0) c.go[it & 1] = ok;
@@ -607,7 +609,9 @@ bool launch(const MmaMaps& maps, MmaArgs a, int64_t grid, cudaStream_t s) {
 
 template <int MODE>
 bool launch_whole(const MmaMaps& maps, const MmaArgs& a, cudaStream_t s) {
-  return launch<MODE, false, false>(maps, a, sm_count() / 2 * 2, s);
+  const int64_t grid = sm_count() / 2 * 2;
+  if (a.tile_n >= kPairTile) return launch<MODE, true, false>(maps, a, grid, s);
+  return launch<MODE, false, false>(maps, a, grid, s);
 }
 
 // Split when the tiles (at most `tiles`) leave more than half the SMs idle: as many blocks per tile as

@@ -27,32 +27,33 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// one poll: waits in hardware for about a microsecond at most
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(1000u)
       : "memory");
   return ok != 0;
 }
 
-constexpr uint32_t kMaxPolls = 1u << 20;  // each poll itself waits in hardware for a while
+constexpr uint32_t kMaxPolls = 1u << 20;  // about a second
 
 // Waits for the phase; gives up (false) after kMaxPolls polls or when another role of the block
-// gave up, so that no wait is endless and all roles leave together.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* failed, uint32_t* err) {
+// gave up, so that no wait is endless and all roles leave together.  The status word keeps `site`.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* failed, uint32_t* err, uint32_t site) {
   for (uint32_t i = 0; i < kMaxPolls; ++i) {
     if (mbar_try(bar, parity)) return true;
-    if ((i & 63u) == 63u && *failed) return false;
+    if ((i & 15u) == 15u && *failed) return false;
   }
   *failed = 1;
-  set_error(err, kErrTimeout);
+  set_error(err, kErrTimeout | (site << 8));
   return false;
 }
 // the same, for draining after a failure: bounded, reports nothing
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
-  for (uint32_t i = 0; i < (kMaxPolls >> 2); ++i)
+  for (uint32_t i = 0; i < (kMaxPolls >> 4); ++i)
     if (mbar_try(bar, parity)) return;
 }
 
