@@ -225,29 +225,38 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
 
       if (kDw) {
         const int nb = (half + 63) / 64;  // 64-column blocks of dy
-        for (int q = 0; q < slices && ok; ++q) {
-          const uint32_t a = open(static_cast<uint32_t>((2 + nb) * kBox), q + 1 == slices);
+        const int m0 = t.m0 + static_cast<int>(rank) * 128;
+        const uint32_t bytes = static_cast<uint32_t>((2 + nb) * kBox);
+        // box u: 64 columns of x (0, 1), then of dy
+        auto column = [&](int u) { return u < 2 ? m0 + u * 64 : jr + (u - 2) * 64; };
+        const int whole = t.k / kDeep;
+        for (int q = 0; q < whole; ++q) {  // one lane of each warp; the others only keep count
+          if (lane == 0 && ok) {
+            ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
+            if (ok) {
+              if (warp == 0 && rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), bytes * kSide);
+              const uint32_t a = base + s * p.stage_bytes, fb = bar();
+              for (int u = warp; u < 2 + nb; u += kProducers)
+                load_2d<PAIR>(a + u * kBox, u < 2 ? &maps.a : &maps.b, column(u), t.k0 + q * kDeep, fb);
+            }
+          }
+          close();
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (ok && whole < slices) {  // the group ends inside the slice: rows past it read as zeros, on both sides
+          const uint32_t a = open(bytes, true);
           if (!ok) break;
           const uint32_t fb = bar();
-          const int m0 = t.m0 + static_cast<int>(rank) * 128, k0 = q * kDeep;
-          // box u: columns of x (0, 1), then of dy
-          const bool whole = k0 + kDeep <= t.k;
-          const int u = whole ? quad : quad >> 4;
-          const uint32_t dst = a + (u < 2 ? u * kBox : kABytes + (u - 2) * kBox);
-          const int col = u < 2 ? m0 + u * 64 : jr + (u - 2) * 64;
+          const int u = quad >> 4;
           if (u < 2 + nb) {
-            if (whole) {
-              load_2d<PAIR>(dst, u < 2 ? &maps.a : &maps.b, col, t.k0 + k0, fb);
-            } else {  // the group ends inside the slice: rows past it read as zeros, on both sides
-              int r[4];
+            int r[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int o = k0 + (quad & 15) * 4 + e;
-                r[e] = o < t.k ? t.k0 + o : p.slots;
-              }
-              load_rows4<PAIR>(dst + (quad & 15) * 512, u < 2 ? &maps.d : &maps.c, col,
-                               make_int4(r[0], r[1], r[2], r[3]), fb);
+            for (int e = 0; e < 4; ++e) {
+              const int o = whole * kDeep + (quad & 15) * 4 + e;
+              r[e] = o < t.k ? t.k0 + o : p.slots;
             }
+            load_rows4<PAIR>(a + u * kBox + (quad & 15) * 512, u < 2 ? &maps.d : &maps.c, column(u),
+                             make_int4(r[0], r[1], r[2], r[3]), fb);
           }
           close();
         }
@@ -281,27 +290,42 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         for (int e = 0; e < 8; ++e) ids[e] = lane + 32 * e < t.n ? id_of(t.j0 + lane + 32 * e) : -1;
         adapter = mine_after(-1, part);
       }
-      // A's two boxes go to the last lanes of the first two warps
+      // copy u of a slice: A's two boxes, then B's; box 2 and up: none for this lane
+      auto copy_a = [&](uint32_t a, int box, int k0, uint32_t fb) {
+        const int m0 = t.m0 + static_cast<int>(rank) * (MODE == kMmaGated ? 64 : 128);
+        if (MODE == kMmaDx) load_3d<PAIR>(a + box * kBox, &maps.a, m0 + box * 64, k0, t.g, fb);
+        else if (MODE == kMmaGated) load_3d<PAIR>(a + box * kBox, &maps.a, k0, m0 + box * p.m, t.g, fb);
+        else load_3d<PAIR>(a + box * kBox, &maps.a, k0, m0 + box * 64, t.g, fb);
+      };
       const int box = lane == 31 ? warp : 2;
-      for (int q = q0; q < q1 && ok; ++q) {
-        const uint32_t a = open(bytes, q + 1 == q1 && adapter < 0), b = a + kABytes;
-        if (!ok) break;
-        const uint32_t fb = bar();
-        const int k0 = q * kDeep;
-        if (box < 2) {
-          const int m0 = t.m0 + static_cast<int>(rank) * (MODE == kMmaGated ? 64 : 128);
-          if (MODE == kMmaDx) load_3d<PAIR>(a + box * kBox, &maps.a, m0 + box * 64, k0, t.g, fb);
-          else if (MODE == kMmaGated) load_3d<PAIR>(a + box * kBox, &maps.a, k0, m0 + box * p.m, t.g, fb);
-          else load_3d<PAIR>(a + box * kBox, &maps.a, k0, m0 + box * 64, t.g, fb);
+      if (gather) {
+        for (int q = q0; q < q1 && ok; ++q) {
+          const uint32_t a = open(bytes, q + 1 == q1);
+          if (!ok) break;
+          const uint32_t fb = bar();
+          if (box < 2) copy_a(a, box, q * kDeep, fb);
+          if (quad * 4 < half) load_rows4<PAIR>(a + kABytes + quad * 512, &maps.b, q * kDeep, mine, fb);
+          close();
         }
-        if (gather) {
-          if (quad * 4 < half) load_rows4<PAIR>(b + quad * 512, &maps.b, k0, mine, fb);
-        } else {
-          // B's boxes start at the third warp
-          const int u = lane * kProducers + ((warp + 2) & 3);
-          if (u < boxes) load_2d<PAIR>(b + u * p.box_rows * 128, &maps.b, k0, jr + u * p.box_rows, fb);
+      } else {
+        for (int q = q0; q < q1; ++q) {  // one lane of each warp; the others only keep count
+          if (lane == 0 && ok) {
+            ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
+            if (ok) {
+              if (warp == 0) {
+                if (MODE == kMmaAdapted) c.last[s] = q + 1 == q1 && adapter < 0 ? 1 : 0;
+                if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), bytes * kSide);
+              }
+              const uint32_t a = base + s * p.stage_bytes, fb = bar();
+              for (int u = warp; u < 2 + boxes; u += kProducers) {
+                if (u < 2) copy_a(a, u, q * kDeep, fb);
+                else load_2d<PAIR>(a + kABytes + (u - 2) * p.box_rows * 128, &maps.b, q * kDeep, jr + (u - 2) * p.box_rows, fb);
+              }
+            }
+          }
+          close();
         }
-        close();
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
       // then, per adapter, its b against the v rows of its own tokens (the others' read as zeros)
       while (MODE == kMmaAdapted && ok && adapter >= 0) {
@@ -348,17 +372,16 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         const uint32_t acc = tmem + (it & 1) * p.tile_n;
         ok = mbar_wait(smem_u32(&c.acc_empty[it & 1]), ((it >> 1) & 1) ^ 1u, failed, p.err, 2u);
         fence_after();
+        const int slices = (t.k + kDeep - 1) / kDeep;
+        const int n = SPLIT ? slices * (part + 1) / parts - slices * part / parts : slices;
         bool last = false;
-        for (bool first = true; ok && !last; first = false) {
+        for (int q = 0; ok && !last; ++q) {
           ok = mbar_wait(smem_u32(&c.full[s]), phase, failed, p.err, 4u);
           if (!ok) break;
           fence_after();
-          last = c.last[s] != 0;
-          const uint32_t a = base + s * p.stage_bytes, b = a + kABytes;
-#pragma unroll
-          for (int q = 0; q < kDeep / 16; ++q)
-            mma<PAIR>(acc, operand(a + (kARows ? q * 2048 : q * 32), kBox), operand(b + (kBRows ? q * 2048 : q * 32), kBox),
-                      idesc, !(first && q == 0));
+          last = MODE == kMmaAdapted ? q + 1 >= n && c.last[s] != 0 : q + 1 == n;
+          const uint32_t a = base + s * p.stage_bytes;
+          mma_slice<PAIR, kARows ? 128 : 2, kBRows ? 128 : 2>(acc, operand(a, kBox), operand(a + kABytes, kBox), idesc, q > 0);
           commit<PAIR>(smem_u32(&c.empty[s]));
           if (last) commit<PAIR>(smem_u32(&c.acc_full[it & 1]));
           if (++s == p.stages) {

@@ -27,18 +27,18 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// one poll: waits in hardware for about a microsecond at most
+// one poll: waits in hardware for a while
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(1000u)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
 
-constexpr uint32_t kMaxPolls = 1u << 20;  // about a second
+constexpr uint32_t kMaxPolls = 1u << 18;
 
 // Waits for the phase; gives up (false) after kMaxPolls polls or when another role of the block
 // gave up, so that no wait is endless and all roles leave together.  The status word keeps `site`.
@@ -169,18 +169,36 @@ __device__ __forceinline__ uint32_t instruction(bool bf16, bool a_rows, bool b_r
   return (1u << 4) | (type << 7) | (type << 10) | ((a_rows ? 1u : 0u) << 15) | ((b_rows ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
-template <bool PAIR>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// d (+)= the four 16-deep steps of a slice; STEP: how far a step moves an operand, in 16 bytes.  One
+// statement, so that the descriptors are ready before the first instruction.
+template <bool PAIR, int STEP_A, int STEP_B>
+__device__ __forceinline__ void mma_slice(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   const uint32_t acc = add ? 1u : 0u;
   if (PAIR)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b),
-        "r"(idesc), "r"(acc)
+        "{\n .reg .pred p, t;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n setp.ne.u32 p, %4, 0;\n setp.eq.u32 t, 0, 0;\n"
+        " add.s64 a1, %1, %5;\n add.s64 b1, %2, %8;\n"
+        " add.s64 a2, %1, %6;\n add.s64 b2, %2, %9;\n"
+        " add.s64 a3, %1, %7;\n add.s64 b3, %2, %10;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, t;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, t;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, t;\n"
+        "}"::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(STEP_A), "n"(2 * STEP_A), "n"(3 * STEP_A), "n"(STEP_B),
+        "n"(2 * STEP_B), "n"(3 * STEP_B)
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b),
-        "r"(idesc), "r"(acc)
+        "{\n .reg .pred p, t;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n setp.ne.u32 p, %4, 0;\n setp.eq.u32 t, 0, 0;\n"
+        " add.s64 a1, %1, %5;\n add.s64 b1, %2, %8;\n"
+        " add.s64 a2, %1, %6;\n add.s64 b2, %2, %9;\n"
+        " add.s64 a3, %1, %7;\n add.s64 b3, %2, %10;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n"
+        "}"::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(STEP_A), "n"(2 * STEP_A), "n"(3 * STEP_A), "n"(STEP_B),
+        "n"(2 * STEP_B), "n"(3 * STEP_B)
         : "memory");
 }
 // the barrier (of both blocks of a pair) gets one arrival when all earlier matrix instructions are done
