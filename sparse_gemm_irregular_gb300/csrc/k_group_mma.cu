@@ -64,7 +64,8 @@ struct Control {
   int last[kMaxStages];            // 1: the stage holds the last slice of its tile
   int scan[33];
   int first[kMaxGroups + 1];       // first position of each group (clamped to [0, slots])
-  int tiles[kMaxGroups + 1];       // N-side tiles before each group
+  int tiles[kMaxGroups + 1];       // full N-side tiles of the groups before each
+  int rest[kMaxGroups + 1];        // part tiles (at most one per group) of the groups before each
   float swap[4 * 16 * 32];         // Gated: halves that the gate and up warps exchange
 };
 
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
   pdl_go();
   // offsets are used as a non-decreasing sequence inside [0, slots], whatever the array holds
   {
-    int run = 0, top = 0;
+    int run = 0, parted = 0;
     for (int g0 = 0; g0 < p.groups; g0 += kThreads) {
       const int g = g0 + static_cast<int>(threadIdx.x);
       int lo = 0, hi = 0;
@@ -126,15 +127,21 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         hi = p.offsets ? min(max(p.offsets[g + 1], lo), p.slots) : p.slots;
         c.first[g] = lo;
       }
-      const int n = kDw ? 0 : (hi - lo + p.tile_n - 1) / p.tile_n;
-      const int incl = block_incl_scan(n, c.scan, &top);
+      const int n = kDw ? 0 : (hi - lo) / p.tile_n, part_tile = !kDw && hi - lo > n * p.tile_n ? 1 : 0;
+      int top = 0, top_part = 0;
+      const int incl = block_incl_scan(n, c.scan, &top), incl_part = block_incl_scan(part_tile, c.scan, &top_part);
       if (g < p.groups) {
         c.tiles[g] = run + incl - n;
+        c.rest[g] = parted + incl_part - part_tile;
         if (g == p.groups - 1) c.first[p.groups] = hi;
       }
       run += top;
+      parted += top_part;
     }
-    if (threadIdx.x == 0) c.tiles[p.groups] = run;
+    if (threadIdx.x == 0) {
+      c.tiles[p.groups] = run;
+      c.rest[p.groups] = parted;
+    }
   }
   fence_before();
   __syncthreads();
@@ -144,33 +151,45 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
   const int m_per_tile = (MODE == kMmaGated ? 64 : 128) * kSide;
   const int mt = (p.m + m_per_tile - 1) / m_per_tile;
   const int nt = kDw ? (p.n + p.tile_n - 1) / p.tile_n : 0;
-  const int64_t total = kDw ? static_cast<int64_t>(p.groups) * mt * nt : static_cast<int64_t>(c.tiles[p.groups]) * mt;
-  const int64_t worker = PAIR ? blockIdx.x >> 1 : SPLIT ? blockIdx.x / parts : blockIdx.x;
-  const int64_t workers = PAIR ? gridDim.x >> 1 : SPLIT ? gridDim.x / parts : gridDim.x;
+  const int worker = static_cast<int>(PAIR ? blockIdx.x >> 1 : SPLIT ? blockIdx.x / parts : blockIdx.x);
+  const int workers = static_cast<int>(PAIR ? gridDim.x >> 1 : SPLIT ? gridDim.x / parts : gridDim.x);
 
-  auto tile_at = [&](int64_t i) {
+  // Tiles in the order m fastest, then the N side: all full tiles of all groups, then the part tiles, so
+  // that blocks that take turns get equal work.  A walk keeps its place; no division per tile.
+  const int full_tiles = kDw ? p.groups * nt : c.tiles[p.groups], all_tiles = full_tiles + (kDw ? 0 : c.rest[p.groups]);
+  struct Walk {
+    int m, r, g;
+  };
+  const int step_m = workers % mt, step_r = workers / mt;
+  auto start = [&]() { return Walk{worker % mt, worker / mt, 0}; };
+  auto advance = [&](Walk& w) {
+    const bool was_full = w.r < full_tiles;
+    w.m += step_m;
+    w.r += step_r;
+    if (w.m >= mt) {
+      w.m -= mt;
+      ++w.r;
+    }
+    if (was_full && w.r >= full_tiles) w.g = 0;
+  };
+  auto tile_of = [&](Walk& w) {
     Tile t;
+    t.m0 = w.m * m_per_tile;
     if (kDw) {
-      t.g = static_cast<int>(i / (static_cast<int64_t>(mt) * nt));
-      const int r = static_cast<int>(i - static_cast<int64_t>(t.g) * mt * nt);
-      t.m0 = (r % mt) * m_per_tile;
-      t.j0 = (r / mt) * p.tile_n;
+      t.g = w.r / nt;
+      t.j0 = (w.r - t.g * nt) * p.tile_n;
       t.n = min(p.n - t.j0, p.tile_n);
       t.k0 = c.first[t.g];
       t.k = max(c.first[t.g + 1] - t.k0, 0);
     } else {
-      const int r = static_cast<int>(i / mt);
-      t.m0 = static_cast<int>(i - static_cast<int64_t>(r) * mt) * m_per_tile;
-      int lo = 0, hi = p.groups;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (c.tiles[mid] <= r) lo = mid;
-        else hi = mid;
-      }
-      t.g = lo;
-      const int lastp = p.offsets ? min(max(p.offsets[lo + 1], c.first[lo]), p.slots) : p.slots;
-      t.j0 = c.first[lo] + (r - c.tiles[lo]) * p.tile_n;
-      t.n = min(lastp - t.j0, p.tile_n);
+      const bool full = w.r < full_tiles;
+      const int* before = full ? c.tiles : c.rest;
+      const int r = full ? w.r : w.r - full_tiles;
+      while (w.g + 1 < p.groups && before[w.g + 1] <= r) ++w.g;
+      const int lo = c.first[w.g], hi = p.offsets ? min(max(p.offsets[w.g + 1], lo), p.slots) : p.slots;
+      t.g = w.g;
+      t.j0 = lo + (full ? (r - before[w.g]) * p.tile_n : (hi - lo) / p.tile_n * p.tile_n);
+      t.n = min(hi - t.j0, p.tile_n);
       t.k0 = 0;
       t.k = p.depth;
     }
@@ -184,8 +203,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
     int s = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int64_t i = worker; i < total && ok; i += workers) {
-      const Tile t = tile_at(i);
+    for (Walk w = start(); w.r < all_tiles && ok; advance(w)) {
+      const Tile t = tile_of(w);
       const int cols = columns(t.n), half = cols / kSide;
       const int jr = t.j0 + static_cast<int>(rank) * half;  // first N index of this block
       // four rows that this lane gathers: a quad of this block's N side
@@ -365,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
     bool ok = true;
     constexpr bool kARows = MODE == kMmaDx || MODE == kMmaDw, kBRows = MODE == kMmaDw;
     if (lane == 0) {
-      for (int64_t i = worker; i < total && ok; i += workers) {
-        const Tile t = tile_at(i);
+      for (Walk w = start(); w.r < all_tiles && ok; advance(w)) {
+        const Tile t = tile_of(w);
         if (t.k == 0) continue;  // an empty group's gradient: the epilogue writes zeros
         const uint32_t idesc = instruction(p.bf16, kARows, kBRows, 128 * kSide, columns(t.n));
         const uint32_t acc = tmem + (it & 1) * p.tile_n;
@@ -403,8 +422,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
     const int ml = quarter * 32 + lane;
     int it = 0;
     bool ok = true;
-    for (int64_t i = worker; i < total; i += workers) {
-      const Tile t = tile_at(i);
+    for (Walk w = start(); w.r < all_tiles; advance(w)) {
+      const Tile t = tile_of(w);
       const bool zero = t.k == 0;
       if (!zero) {
         ok = mbar_wait(smem_u32(&c.acc_full[it & 1]), (it >> 1) & 1, failed, p.err, 8u);
@@ -504,8 +523,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
     cluster_sync();
     fence_after();
     const int width = p.tile_n / parts;
-    const bool there = worker < total && !*failed;
-    const Tile t = there ? tile_at(worker) : Tile{};
+    Walk w = start();
+    const bool there = w.r < all_tiles && !*failed;
+    const Tile t = there ? tile_of(w) : Tile{};
     const int ml = (warp & 3) * 32 + lane;
     if (there && warp > kProducers) {
       const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
