@@ -16,7 +16,7 @@ struct MmaArgs {
   int bf16;
   int m, n, depth;         // M side, N side (Dw only), contracted length
   int tile_n, box_rows;
-  int stages, stage_bytes;
+  int stages, stage_bytes, sub_bytes;
   void* out;
   int64_t out_stride, out_group;
   int out_type;

@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
   const int part = SPLIT ? static_cast<int>(cluster_rank()) : 0, parts = SPLIT ? p.split : 1;  // of the contracted range
   const uint32_t tmem_cols = SPLIT ? kSplitTile : kTmemCols;
   constexpr int kSide = PAIR ? 2 : 1;
+  constexpr int kSub = PAIR ? 2 : 1;  // slices of a stage
   constexpr bool kDw = MODE == kMmaDw;
   volatile int* failed = &c.failed;
 
@@ -249,14 +250,17 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         // box u: 64 columns of x (0, 1), then of dy
         auto column = [&](int u) { return u < 2 ? m0 + u * 64 : jr + (u - 2) * 64; };
         const int whole = t.k / kDeep;
-        for (int q = 0; q < whole; ++q) {  // one lane of each warp; the others only keep count
+        for (int q = 0; q < whole; q += kSub) {  // one lane of each warp; the others only keep count
+          const int subs = min(kSub, whole - q);
           if (lane == 0 && ok) {
             ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
             if (ok) {
-              if (warp == 0 && rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), bytes * kSide);
-              const uint32_t a = base + s * p.stage_bytes, fb = bar();
-              for (int u = warp; u < 2 + nb; u += kProducers)
-                load_2d<PAIR>(a + u * kBox, u < 2 ? &maps.a : &maps.b, column(u), t.k0 + q * kDeep, fb);
+              if (warp == 0 && rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
+              const uint32_t fb = bar();
+              for (int h = 0; h < subs; ++h)
+                for (int u = warp; u < 2 + nb; u += kProducers)
+                  load_2d<PAIR>(base + s * p.stage_bytes + h * p.sub_bytes + u * kBox, u < 2 ? &maps.a : &maps.b, column(u),
+                                t.k0 + (q + h) * kDeep, fb);
             }
           }
           close();
@@ -327,18 +331,23 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           close();
         }
       } else {
-        for (int q = q0; q < q1; ++q) {  // one lane of each warp; the others only keep count
+        for (int q = q0; q < q1; q += kSub) {  // one lane of each warp; the others only keep count
+          const int subs = min(kSub, q1 - q);
           if (lane == 0 && ok) {
             ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
             if (ok) {
               if (warp == 0) {
-                if (MODE == kMmaAdapted) c.last[s] = q + 1 == q1 && adapter < 0 ? 1 : 0;
-                if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), bytes * kSide);
+                if (MODE == kMmaAdapted) c.last[s] = q + subs == q1 && adapter < 0 ? 1 : 0;
+                if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
               }
-              const uint32_t a = base + s * p.stage_bytes, fb = bar();
-              for (int u = warp; u < 2 + boxes; u += kProducers) {
-                if (u < 2) copy_a(a, u, q * kDeep, fb);
-                else load_2d<PAIR>(a + kABytes + (u - 2) * p.box_rows * 128, &maps.b, q * kDeep, jr + (u - 2) * p.box_rows, fb);
+              const uint32_t fb = bar();
+              for (int h = 0; h < subs; ++h) {
+                const uint32_t a = base + s * p.stage_bytes + h * p.sub_bytes;
+                const int k0 = (q + h) * kDeep;
+                for (int u = warp; u < 2 + boxes; u += kProducers) {
+                  if (u < 2) copy_a(a, u, k0, fb);
+                  else load_2d<PAIR>(a + kABytes + (u - 2) * p.box_rows * 128, &maps.b, k0, jr + (u - 2) * p.box_rows, fb);
+                }
               }
             }
           }
@@ -393,14 +402,22 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         fence_after();
         const int slices = (t.k + kDeep - 1) / kDeep;
         const int n = SPLIT ? slices * (part + 1) / parts - slices * part / parts : slices;
+        const int paired = kDw ? t.k / kDeep : n;  // slices that come kSub to a stage
         bool last = false;
-        for (int q = 0; ok && !last; ++q) {
+        for (int q = 0; ok && !last;) {
           ok = mbar_wait(smem_u32(&c.full[s]), phase, failed, p.err, 4u);
           if (!ok) break;
           fence_after();
-          last = MODE == kMmaAdapted ? q + 1 >= n && c.last[s] != 0 : q + 1 == n;
-          const uint32_t a = base + s * p.stage_bytes;
-          mma_slice<PAIR, kARows ? 128 : 2, kBRows ? 128 : 2>(acc, operand(a, kBox), operand(a + kABytes, kBox), idesc, q > 0);
+          // slices that come kSub to a stage; part slices and adapters' come alone.  (A rows gathered one to a
+          // stage only in kernels with kSub = 1.)
+          const int subs = q < paired ? min(kSub, paired - q) : 1;
+          for (int h = 0; h < subs; ++h) {
+            const uint32_t a = base + s * p.stage_bytes + h * p.sub_bytes;
+            mma_slice<PAIR, kARows ? 128 : 2, kBRows ? 128 : 2>(acc, operand(a, kBox), operand(a + kABytes, kBox), idesc,
+                                                                q + h > 0);
+          }
+          q += subs;
+          last = MODE == kMmaAdapted ? q >= n && c.last[s] != 0 : q == n;
           commit<PAIR>(smem_u32(&c.empty[s]));
           if (last) commit<PAIR>(smem_u32(&c.acc_full[it & 1]));
           if (++s == p.stages) {
@@ -472,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           asm volatile("bar.sync 1, %0;" ::"n"(kEpilogue) : "memory");
         } else {
           const int m = t.m0 + static_cast<int>(rank) * 128 + ml;
-          int64_t o = (kDw ? t.g * p.out_group : 0) + static_cast<int64_t>(t.j0 + j) * p.out_stride + m;
+          const int64_t o = (kDw ? t.g * p.out_group : 0) + static_cast<int64_t>(t.j0 + j) * p.out_stride + m;
           int token = 0;
           float f = 1.0f;
           if (MODE == kMmaForward && p.scatter) {  // rows leave in the tokens' order
@@ -482,15 +499,21 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           auto put = [&](auto type) {
             using T = decltype(type);
             T* out = static_cast<T*>(p.out);
+            if (MODE == kMmaForward && p.scatter) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (MODE == kMmaForward && p.scatter) {
+              for (int e = 0; e < 32; ++e) {
                 const int64_t row = __shfl_sync(0xffffffffu, token, e);
                 if (e < n && m < p.m) out[row * p.out_stride + m] = from_f32<T>(f * __uint_as_float(r[e]));
-              } else {
-                if (e < n && m < p.m) out[o] = from_f32<T>(__uint_as_float(r[e]));
-                o += p.out_stride;
               }
+            } else if (n == 32) {
+              if (m < p.m) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) out[o + e * p.out_stride] = from_f32<T>(__uint_as_float(r[e]));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e < n && m < p.m) out[o + e * p.out_stride] = from_f32<T>(__uint_as_float(r[e]));
             }
           };
           if (p.out_type == SPGEMM_DTYPE_F32) put(float());
@@ -624,7 +647,8 @@ int sm_count() {
 
 template <int MODE, bool PAIR, bool SPLIT>
 bool launch(const MmaMaps& maps, MmaArgs a, int64_t grid, cudaStream_t s) {
-  a.stage_bytes = kABytes + std::max(a.tile_n / (PAIR ? 2 : 1), MODE == kMmaDw ? 64 : 16) * 128;
+  a.sub_bytes = kABytes + std::max(a.tile_n / (PAIR ? 2 : 1), MODE == kMmaDw ? 64 : 16) * 128;
+  a.stage_bytes = a.sub_bytes * (PAIR ? 2 : 1);
   const int control = static_cast<int>(sizeof(Control));
   // split: two blocks per SM, and the stages hold the sums that meet there
   const int most = SPLIT ? kSmemMost / 2 - 1024 : kSmemMost;
