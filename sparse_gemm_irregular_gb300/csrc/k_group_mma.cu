@@ -66,7 +66,7 @@ struct Control {
   int first[kMaxGroups + 1];       // first position of each group (clamped to [0, slots])
   int tiles[kMaxGroups + 1];       // full N-side tiles of the groups before each
   int rest[kMaxGroups + 1];        // part tiles (at most one per group) of the groups before each
-  float swap[4 * 16 * 32];         // Gated: halves that the gate and up warps exchange
+  float swap[2][4 * 16 * 32];      // Gated: halves that the gate and up warps exchange, by turns
 };
 
 struct Tile {
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
     // ---- epilogue ----------------------------------------------------------------------------------
     const int quarter = warp & 3;  // the lanes of tensor memory that this warp can read
     const int ml = quarter * 32 + lane;
-    int it = 0;
+    int it = 0, turn = 0;
     bool ok = true;
     for (Walk w = start(); w.r < all_tiles; advance(w)) {
       const Tile t = tile_of(w);
@@ -468,25 +468,28 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         if (MODE == kMmaGated) {
           // gate warps (lanes 0..63) finish columns 0..15, up warps (64..127) columns 16..31
           const bool up = quarter >= 2;
-          float* mine = c.swap + quarter * 512;
-          const float* theirs = c.swap + (quarter ^ 2) * 512;
+          float* mine = c.swap[turn] + quarter * 512;
+          const float* theirs = c.swap[turn] + (quarter ^ 2) * 512;
+          turn ^= 1;  // one meeting per chunk: the next chunk writes the other half of the buffer
 #pragma unroll
           for (int e = 0; e < 16; ++e) mine[e * 32 + lane] = __uint_as_float(up ? r[e] : r[16 + e]);
           asm volatile("bar.sync 1, %0;" ::"n"(kEpilogue) : "memory");
           const int m = t.m0 + static_cast<int>(rank) * 64 + (quarter & 1) * 32 + lane;
+          const int j0 = j + (up ? 16 : 0), n16 = min(16, t.n - j0);
+          const int64_t o = static_cast<int64_t>(t.j0 + j0) * p.out_stride + m;
+          auto put = [&](auto type) {
+            using T = decltype(type);
+            T* out = static_cast<T*>(p.out);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int jj = j + (up ? 16 : 0) + e;
-            const float other = theirs[e * 32 + lane];
-            const float own = __uint_as_float(up ? r[16 + e] : r[e]);
-            const float h = up ? gated_silu(other, own) : gated_silu(own, other);
-            if (jj < t.n && m < p.m) {
-              const int64_t o = static_cast<int64_t>(t.j0 + jj) * p.out_stride + m;
-              if (p.out_type == SPGEMM_DTYPE_BF16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(h);
-              else static_cast<__half*>(p.out)[o] = __float2half_rn(h);
+            for (int e = 0; e < 16; ++e) {
+              const float other = theirs[e * 32 + lane], own = __uint_as_float(up ? r[16 + e] : r[e]);
+              // the result is rounded to 16 bits: the short exponential and division are exact enough
+              const float h = gated_silu_short(up ? other : own, up ? own : other);
+              if (e < n16 && m < p.m) out[o + e * p.out_stride] = from_f32<T>(h);
             }
-          }
-          asm volatile("bar.sync 1, %0;" ::"n"(kEpilogue) : "memory");
+          };
+          if (p.out_type == SPGEMM_DTYPE_BF16) put(__nv_bfloat16());
+          else put(__half());
         } else {
           const int m = t.m0 + static_cast<int>(rank) * 128 + ml;
           const int64_t o = (kDw ? t.g * p.out_group : 0) + static_cast<int64_t>(t.j0 + j) * p.out_stride + m;
