@@ -13,6 +13,7 @@ struct MmaArgs {
   int slots, groups, top_k;
   int rows;                // rows of the gathered matrix: the index that reads as zeros
   int gather, scatter;
+  int runs;                // gathered rows often follow one another
   int bf16;
   int m, n, depth;         // M side, N side (Dw only), contracted length
   int tile_n, box_rows;

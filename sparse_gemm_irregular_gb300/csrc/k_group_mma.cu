@@ -80,7 +80,7 @@ struct Tile {
 }  // namespace
 
 struct MmaMaps {
-  CUtensorMap a, b, c, d;  // Forward, Dx: weights, rows; Dw: x, dy, then rows of dy and of x; Adapted: w, x, b[i], v rows
+  CUtensorMap a, b, c, d;  // Forward, Dx: weights, rows (gathered: also in boxes); Dw: x, dy, then rows of dy and of x; Adapted: w, x, b[i], v rows
 };
 
 template <int MODE, bool PAIR, bool SPLIT>
@@ -286,8 +286,20 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         continue;
       }
 
+      // gathered rows that follow one another anyway (the tokens of one request) come in boxes
+      bool boxed = !gather;
+      if (MODE == kMmaForward && gather && p.runs) {
+        bool follow = true;
+        const int row0 = p.order[t.j0] / p.top_k;
+        for (int j = lane; j < t.n; j += 32) follow = follow && p.order[t.j0 + j] / p.top_k == row0 + j;
+        boxed = __all_sync(0xffffffffu, follow) != 0;
+      }
+      const int row_b = boxed && gather ? p.order[t.j0] / p.top_k : jr;
+      const CUtensorMap* map_b = gather ? &maps.c : &maps.b;
       const int boxes = (half + p.box_rows - 1) / p.box_rows;
-      const uint32_t bytes = kABytes + (gather ? half : boxes * p.box_rows) * 128;
+      // the second 64 rows of A may be none of the matrix's: the accumulator's lanes then hold nothing of use
+      const int boxes_a = MODE == kMmaForward && !PAIR && t.m0 + 64 >= p.m ? 1 : 2;
+      const uint32_t bytes = boxes_a * kBox + (boxed ? boxes * p.box_rows : half) * 128;
       // Adapted: the adapters of the tile's tokens (lane, lane + 32, ...), in ascending order
       int ids[8];
       auto id_of = [&](int j) {
@@ -321,12 +333,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         else load_3d<PAIR>(a + box * kBox, &maps.a, k0, m0 + box * 64, t.g, fb);
       };
       const int box = lane == 31 ? warp : 2;
-      if (gather) {
+      if (!boxed) {
         for (int q = q0; q < q1 && ok; ++q) {
           const uint32_t a = open(bytes, q + 1 == q1);
           if (!ok) break;
           const uint32_t fb = bar();
-          if (box < 2) copy_a(a, box, q * kDeep, fb);
+          if (box < boxes_a) copy_a(a, box, q * kDeep, fb);
           if (quad * 4 < half) load_rows4<PAIR>(a + kABytes + quad * 512, &maps.b, q * kDeep, mine, fb);
           close();
         }
@@ -344,9 +356,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
               for (int h = 0; h < subs; ++h) {
                 const uint32_t a = base + s * p.stage_bytes + h * p.sub_bytes;
                 const int k0 = (q + h) * kDeep;
-                for (int u = warp; u < 2 + boxes; u += kProducers) {
-                  if (u < 2) copy_a(a, u, k0, fb);
-                  else load_2d<PAIR>(a + kABytes + (u - 2) * p.box_rows * 128, &maps.b, k0, jr + (u - 2) * p.box_rows, fb);
+                for (int u = warp; u < boxes_a + boxes; u += kProducers) {
+                  const int v = u - boxes_a;
+                  if (v < 0) copy_a(a, u, k0, fb);
+                  else load_2d<PAIR>(a + kABytes + v * p.box_rows * 128, map_b, k0, row_b + v * p.box_rows, fb);
                 }
               }
             }
@@ -684,13 +697,13 @@ bool launch_whole(const MmaMaps& maps, const MmaArgs& a, cudaStream_t s) {
   return launch<MODE, false, false>(maps, a, grid, s);
 }
 
-// Split when the tiles (at most `tiles`) leave more than half the SMs idle: as many blocks per tile as
-// fit the SMs, up to 8, with at least two slices each.
+// Split when the tiles (at most `tiles`) leave most of the SMs idle: as many blocks per tile, up to 8, as
+// fit at two per SM, with at least two slices each.
 template <int MODE>
 bool launch_split(const MmaMaps& maps, MmaArgs a, int64_t tiles, cudaStream_t s) {
   const int slices = (a.depth + kDeep - 1) / kDeep;
   a.split = 1;
-  while (a.split < 8 && tiles * a.split * 2 <= sm_count() && a.split * 4 <= slices) a.split *= 2;
+  while (a.split < 8 && tiles * a.split <= sm_count() && a.split * 4 <= slices) a.split *= 2;
   if (a.split == 1 || a.tile_n > kSplitTile || a.tile_n < a.split) return launch_whole<MODE>(maps, a, s);
   return launch<MODE, false, true>(maps, a, tiles * a.split, s);
 }
@@ -792,15 +805,18 @@ bool launch_mma_shrink(const spgemm_grouping& g, const spgemm_dense& x, const sp
   a.gather = a.scatter = 1;
   a.m = static_cast<int>(v.cols);
   a.depth = static_cast<int>(x.cols);
+  // the widest tile that still gives every SM one: x is read once either way, a's rows once per tile
   a.tile_n = 32;
+  while (a.tile_n < 128 && g.slots > static_cast<int64_t>(a.tile_n) * sm_count()) a.tile_n *= 2;
   a.box_rows = 32;
   a.out = v.data;
   a.out_stride = v.stride;
   a.out_type = v.dtype;
   a.scale = scale;
   MmaMaps maps;
-  if (!encode_weights(&maps.a, a_w) || !encode_rows(&maps.b, x, 1)) return false;
-  maps.c = maps.d = maps.b;
+  a.runs = 1;
+  if (!encode_weights(&maps.a, a_w) || !encode_rows(&maps.b, x, 1) || !encode_rows(&maps.c, x, a.box_rows)) return false;
+  maps.d = maps.b;
   return launch_split<kMmaForward>(maps, a, most_tiles(g, a.tile_n) * ceil_div(a.m, 128), s);
 }
 
@@ -813,7 +829,12 @@ bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spge
   a.rank = static_cast<int>(b.cols);
   a.m = static_cast<int>(y.cols);
   a.depth = static_cast<int>(x.cols);
-  a.tile_n = pick_tile(x.rows, 2, 256);
+  // the widest tile that still gives every SM one; few rows: one tile, its depth split
+  a.tile_n = 256;
+  while (a.tile_n > 16 && (x.rows * 2 <= a.tile_n ||
+                           (x.rows > kSplitTile && a.tile_n > 32 &&
+                            ceil_div(x.rows, a.tile_n) * ceil_div(y.cols, 128) < sm_count())))
+    a.tile_n /= 2;
   a.box_rows = std::min(a.tile_n, 64);
   a.out = y.data;
   a.out_stride = y.stride;

@@ -30,7 +30,7 @@ namespace {
 constexpr int kWarps = 8;               // warps of a block
 constexpr int kWarpsOne = 32;           // of the block that does everything
 constexpr int kSteps = 4;               // most steps (32 / L tokens each) of a warp
-constexpr int kSlotsPerWarp = 256;      // consecutive slots of a warp (given ids)
+constexpr int kSlotsPerWarp = 64;       // consecutive slots of a warp (given ids)
 constexpr int kOneExperts = 256;        // most experts whose counts the single block keeps (32 KB)
 constexpr float kNegInf = -INFINITY;
 
@@ -567,9 +567,9 @@ Shape route_shape(int64_t tokens, int experts) {
   return {false, static_cast<int>(steps), ceil_div(tokens, kWarps * step * steps)};
 }
 
-// One block while its warps have at most four turns of 32 slots.
+// One block while its warps have at most sixteen turns of 32 slots: about 13 us, against 20 for three launches.
 Shape group_shape(int64_t slots, int groups) {
-  if (slots <= kWarpsOne * 128 && groups <= kOneExperts)
+  if (slots <= kWarpsOne * 512 && groups <= kOneExperts)
     return {true, static_cast<int>(std::max<int64_t>(32, ceil_div(slots, kWarpsOne * 32) * 32)), 1};
   return {false, kSlotsPerWarp, ceil_div(slots, kWarps * kSlotsPerWarp)};
 }

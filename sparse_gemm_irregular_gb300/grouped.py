@@ -91,15 +91,19 @@ class Routing:
                          self.weights.reshape(-1)[slot].double())
 
 
-def _dtype(t, name: str) -> int:
+_codes: dict = {}  # torch dtype -> SPGEMM_DTYPE_*, filled on first use (the package imports without torch)
+
+
+def _refuse(t, name: str, dims: int):
     import torch
-    d = t.dtype
-    code = 1 if d is torch.bfloat16 else 2 if d is torch.float16 else 0 if d is torch.float32 else None
-    if code is None:
-        raise TypeError("%s: float32, bfloat16 or float16 wanted, got %s" % (name, d))
+    if not _codes:
+        _codes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    if t.dtype not in _codes:
+        raise TypeError("%s: float32, bfloat16 or float16 wanted, got %s" % (name, t.dtype))
     if not t.is_cuda:
         raise ValueError("%s: a CUDA tensor is wanted" % name)
-    return code
+    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError("%s: %d dimensions with contiguous rows are wanted" % (name, dims))
 
 
 def _want(t, name: str, dtype):
@@ -108,19 +112,21 @@ def _want(t, name: str, dtype):
 
 
 def _dense(t, name: str) -> spgemm_dense:
-    code = _dtype(t, name)
-    shape, step = t.shape, t.stride()
-    if len(shape) != 2 or (shape[1] > 1 and step[1] != 1):
-        raise ValueError("%s: a matrix whose rows are contiguous is wanted" % name)
-    return spgemm_dense(t.data_ptr(), shape[0], shape[1], max(step[0], shape[1]), code, 0)
+    shape, step, code = t.shape, t.stride(), _codes.get(t.dtype)
+    if code is None or not t.is_cuda or len(shape) != 2 or (step[1] != 1 and shape[1] > 1):
+        _refuse(t, name, 2)
+        code = _codes[t.dtype]
+    rows, cols = shape
+    return spgemm_dense(t.data_ptr(), rows, cols, step[0] if step[0] > cols else cols, code, 0)
 
 
 def _weights(t, name: str) -> spgemm_weights:
-    code = _dtype(t, name)
-    shape, step = t.shape, t.stride()
-    if len(shape) != 3 or (shape[2] > 1 and step[2] != 1):
-        raise ValueError("%s: (groups, rows, columns) with contiguous rows is wanted" % name)
-    return spgemm_weights(t.data_ptr(), shape[0], shape[1], shape[2], step[0], max(step[1], shape[2]), code, 0)
+    shape, step, code = t.shape, t.stride(), _codes.get(t.dtype)
+    if code is None or not t.is_cuda or len(shape) != 3 or (step[2] != 1 and shape[2] > 1):
+        _refuse(t, name, 3)
+        code = _codes[t.dtype]
+    groups, rows, cols = shape
+    return spgemm_weights(t.data_ptr(), groups, rows, cols, step[0], step[1] if step[1] > cols else cols, code, 0)
 
 
 _ref = ctypes.byref
@@ -132,7 +138,7 @@ def _call(name: str, device, stream, *args):
     index = device.index
     raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
     fn = getattr(load(), name)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(index):
