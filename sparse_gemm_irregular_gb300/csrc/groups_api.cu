@@ -1,6 +1,7 @@
 // C entry points of the grouped-product operators: argument checks, scratch from the library's
 // stream-ordered pool, and the choice between the tensor-core and the CUDA-core kernels.
 #include <algorithm>
+#include <atomic>
 
 #include "group_mma.h"
 
@@ -11,9 +12,17 @@ cudaMemPool_t device_pool(int dev);
 static __device__ uint32_t g_grouped_err;
 
 uint32_t* grouped_err() {
-  void* p = nullptr;
-  if (cudaGetSymbolAddress(&p, g_grouped_err) != cudaSuccess) cudaGetLastError();
-  return static_cast<uint32_t*>(p);
+  static std::atomic<uint32_t*> at[64];  // per device: the symbol's address does not change
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  uint32_t* p = at[dev].load(std::memory_order_relaxed);
+  if (!p) {
+    void* v = nullptr;
+    if (cudaGetSymbolAddress(&v, g_grouped_err) != cudaSuccess) cudaGetLastError();
+    p = static_cast<uint32_t*>(v);
+    at[dev].store(p, std::memory_order_relaxed);
+  }
+  return p;
 }
 
 namespace {

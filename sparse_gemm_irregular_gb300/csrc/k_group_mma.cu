@@ -64,10 +64,9 @@ struct Control {
   int failed;
   int go[kSets][2];                // Gated: whether the four warps of a set take the next tile
   int last[kMaxStages];            // 1: the stage holds the last slice of its tile
-  int64_t scan[33];
+  int scan[33];
   int first[kMaxGroups + 1];       // first position of each group (clamped to [0, slots])
-  int tiles[kMaxGroups + 1];       // full N-side tiles of the groups before each
-  int rest[kMaxGroups + 1];        // part tiles (at most one per group) of the groups before each
+  int tiles[kMaxGroups + 1];       // N-side tiles of the groups before each
 };
 
 // Gated: columns that the gate and up warps of a set exchange, by turns
@@ -130,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
   pdl_go();
   // offsets are used as a non-decreasing sequence inside [0, slots], whatever the array holds
   {
-    int64_t run = 0;  // full tiles in the low half, part tiles in the high half
+    int run = 0;
     for (int g0 = 0; g0 < p.groups; g0 += kThreads) {
       const int g = g0 + static_cast<int>(threadIdx.x);
       int lo = 0, hi = 0;
@@ -141,20 +140,13 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         if (g == p.groups - 1) c.first[p.groups] = hi;
       }
       if (kDw) continue;
-      const int n = (hi - lo) / p.tile_n;
-      const int64_t both = (hi - lo > n * p.tile_n ? int64_t(1) << 32 : 0) + n;
-      int64_t top = 0;
-      const int64_t before = run + block_incl_scan(both, c.scan, &top) - both;
-      if (g < p.groups) {
-        c.tiles[g] = static_cast<int>(before);
-        c.rest[g] = static_cast<int>(before >> 32);
-      }
+      const int n = (hi - lo + p.tile_n - 1) / p.tile_n;
+      int top = 0;
+      const int before = run + block_incl_scan(n, c.scan, &top) - n;
+      if (g < p.groups) c.tiles[g] = before;
       run += top;
     }
-    if (threadIdx.x == 0) {
-      c.tiles[p.groups] = static_cast<int>(run);
-      c.rest[p.groups] = static_cast<int>(run >> 32);
-    }
+    if (threadIdx.x == 0) c.tiles[p.groups] = run;
   }
   fence_before();
   __syncthreads();
@@ -167,23 +159,22 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
   const int worker = static_cast<int>(PAIR ? blockIdx.x >> 1 : SPLIT ? blockIdx.x / parts : blockIdx.x);
   const int workers = static_cast<int>(PAIR ? gridDim.x >> 1 : SPLIT ? gridDim.x / parts : gridDim.x);
 
-  // Tiles in the order m fastest, then the N side: all full tiles of all groups, then the part tiles, so
-  // that blocks that take turns get equal work.  A walk keeps its place; no division per tile.
-  const int full_tiles = kDw ? p.groups * nt : c.tiles[p.groups], all_tiles = full_tiles + (kDw ? 0 : c.rest[p.groups]);
+  // Tiles in the order m fastest, then the N side, group by group: blocks that run at the same time share a
+  // group's weights and rows in L2.  (All full tiles first, then the groups' part tiles, balances the blocks
+  // better but reads the weights twice.)  A walk keeps its place; no division per tile.
+  const int all_tiles = kDw ? p.groups * nt : c.tiles[p.groups];
   struct Walk {
     int m, r, g;
   };
   const int step_m = workers % mt, step_r = workers / mt;
   auto start = [&]() { return Walk{worker % mt, worker / mt, 0}; };
   auto advance = [&](Walk& w) {
-    const bool was_full = w.r < full_tiles;
     w.m += step_m;
     w.r += step_r;
     if (w.m >= mt) {
       w.m -= mt;
       ++w.r;
     }
-    if (was_full && w.r >= full_tiles) w.g = 0;
   };
   auto tile_of = [&](Walk& w) {
     Tile t;
@@ -195,13 +186,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
       t.k0 = c.first[t.g];
       t.k = max(c.first[t.g + 1] - t.k0, 0);
     } else {
-      const bool full = w.r < full_tiles;
-      const int* before = full ? c.tiles : c.rest;
-      const int r = full ? w.r : w.r - full_tiles;
-      while (w.g + 1 < p.groups && before[w.g + 1] <= r) ++w.g;
+      while (w.g + 1 < p.groups && c.tiles[w.g + 1] <= w.r) ++w.g;
       const int lo = c.first[w.g], hi = p.offsets ? min(max(p.offsets[w.g + 1], lo), p.slots) : p.slots;
       t.g = w.g;
-      t.j0 = lo + (full ? (r - before[w.g]) * p.tile_n : (hi - lo) / p.tile_n * p.tile_n);
+      t.j0 = lo + (w.r - c.tiles[w.g]) * p.tile_n;
       t.n = min(hi - t.j0, p.tile_n);
       t.k0 = 0;
       t.k = p.depth;
@@ -677,9 +665,12 @@ bool encode_weights(CUtensorMap* map, const spgemm_weights& w) {
 }
 
 int sm_count() {
-  int dev = 0, sms = 1;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  static const int sms = [] {  // the library runs on one kind of device
+    int dev = 0, n = 1;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+  }();
   return sms;
 }
 
