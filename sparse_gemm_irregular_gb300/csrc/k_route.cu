@@ -29,7 +29,8 @@ namespace {
 
 constexpr int kWarps = 8;               // warps of a block
 constexpr int kWarpsOne = 32;           // of the block that does everything
-constexpr int kSteps = 4;               // most steps (32 / L tokens each) of a warp
+constexpr int kSteps = 2;               // most steps (32 / L tokens each) of a warp of many blocks
+constexpr int kStepsOne = 4;            // of the block that does everything
 constexpr int kSlotsPerWarp = 64;       // consecutive slots of a warp (given ids)
 constexpr int kOneExperts = 256;        // most experts whose counts the single block keeps (32 KB)
 constexpr float kNegInf = -INFINITY;
@@ -211,7 +212,7 @@ __device__ __forceinline__ int group_offsets(int groups, int* s_off, int* s_tmp,
 // slot's rank among the block's slots of the same expert and counts[e * blocks + block] = the block's
 // slots of expert e.
 template <typename T, int L, int V, bool ONE>
-__global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32)
+__global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32, ONE || V > 8 ? 1 : 4)
     k_route(const T* __restrict__ logits, int64_t stride, int64_t tokens, int experts, int pieces, int steps,
             const __grid_constant__ spgemm_route_rule r, const float* __restrict__ bias, int32_t* __restrict__ ids,
             float* __restrict__ weights, int32_t* __restrict__ position, int32_t* __restrict__ counts,
@@ -230,6 +231,9 @@ __global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32)
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kW + warp) * (steps * kPer);
   const int64_t t1 = min(tokens, t0 + steps * kPer);
   const int per = experts / r.groups;
+  float mine_bias[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) mine_bias[v] = bias && e0 + v < experts ? bias[e0 + v] : 0.0f;
   for (int64_t tw = t0; tw < t1; tw += kPer) {
     const int64_t t = tw + sub;
     const bool there = t < t1;
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32)
     uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float c = bias && e0 + v < experts ? s[v] + bias[e0 + v] : l[v];
+      const float c = bias ? s[v] + mine_bias[v] : l[v];
       key[v] = l[v] > kNegInf && c > kNegInf ? order_key(c) : 0u;
     }
     if (r.groups_kept < r.groups)
@@ -562,7 +566,7 @@ struct Shape {
 Shape route_shape(int64_t tokens, int experts) {
   const int64_t step = tokens_per_step(experts);
   const int64_t one = ceil_div(tokens, kWarpsOne * step);
-  if (one <= kSteps && experts <= kOneExperts) return {true, static_cast<int>(std::max<int64_t>(one, 1)), 1};
+  if (one <= kStepsOne && experts <= kOneExperts) return {true, static_cast<int>(std::max<int64_t>(one, 1)), 1};
   const int64_t steps = std::min<int64_t>(kSteps, std::max<int64_t>(1, tokens / (kWarps * step * 304)));
   return {false, static_cast<int>(steps), ceil_div(tokens, kWarps * step * steps)};
 }

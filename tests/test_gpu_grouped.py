@@ -84,6 +84,11 @@ ROUTES = [
     (66, 257, 32, dict(score="sigmoid", renormalise=False)),
     (40, 1000, 8, dict(score="softmax", groups=10, groups_kept=1)),
     (1500, 64, 6, dict(score="softmax")),
+    # rows enough for few lanes per token
+    (16413, 64, 6, dict(score="softmax", renormalise=False)),
+    (9001, 120, 5, dict(score="sigmoid", groups=3, groups_kept=2)),
+    (4199, 250, 8, dict(score="softmax", groups=5, groups_kept=3)),
+    (2111, 512, 9, dict(score="softmax", groups=16, groups_kept=4)),
 ]
 
 
