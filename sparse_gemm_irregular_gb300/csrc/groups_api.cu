@@ -2,6 +2,7 @@
 // stream-ordered pool, and the choice between the tensor-core and the CUDA-core kernels.
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 
 #include "group_mma.h"
 
@@ -29,38 +30,44 @@ namespace {
 
 constexpr int64_t kMaxSlots = (int64_t(1) << 31) - (1 << 20);  // positions and tile ends stay 32-bit
 
-// Scratch of one call, returned to the pool in stream order when the call ends.
+// Scratch of one call: one allocation of all its parts, returned to the pool in stream order when the
+// call ends.  Parts of no bytes are null.
 class Scratch {
  public:
-  explicit Scratch(cudaStream_t s) : s_(s) {
+  Scratch(cudaStream_t s, std::initializer_list<int64_t> parts) : s_(s) {
+    int64_t all = 0;
+    for (const int64_t b : parts) {
+      at_[n_] = b ? all : -1;
+      all += (b + 255) / 256 * 256;
+      ++n_;
+    }
+    if (!all) return;
     int dev = 0;
     cudaGetDevice(&dev);
-    pool_ = device_pool(dev);
+    void* p = nullptr;
+    if (cudaMallocFromPoolAsync(&p, static_cast<size_t>(all), device_pool(dev), s_) != cudaSuccess) {
+      cudaGetLastError();
+      set_last_error("scratch allocation failed");
+      ok_ = false;
+      return;
+    }
+    base_ = static_cast<char*>(p);
   }
   ~Scratch() {
-    for (int i = 0; i < n_; ++i) cudaFreeAsync(p_[i], s_);
+    if (base_) cudaFreeAsync(base_, s_);
   }
-  void* get(int64_t bytes) {
-    void* p = nullptr;
-    if (bytes == 0) return p;
-    if (n_ == kMost || cudaMallocFromPoolAsync(&p, static_cast<size_t>(bytes), pool_, s_) !=
-                           cudaSuccess) {
-      cudaGetLastError();
-      ok_ = false;
-      return nullptr;
-    }
-    return p_[n_++] = p;
+  Scratch(const Scratch&) = delete;
+  Scratch& operator=(const Scratch&) = delete;
+  template <typename T = void>
+  T* part(int i) const {
+    return base_ && at_[i] >= 0 ? reinterpret_cast<T*>(base_ + at_[i]) : nullptr;
   }
-  bool ok() const {
-    if (!ok_) set_last_error("scratch allocation failed");
-    return ok_;
-  }
+  bool ok() const { return ok_; }
 
  private:
-  static constexpr int kMost = 16;
   cudaStream_t s_;
-  cudaMemPool_t pool_ = nullptr;
-  void* p_[kMost];
+  char* base_ = nullptr;
+  int64_t at_[8];
   int n_ = 0;
   bool ok_ = true;
 };
@@ -118,20 +125,22 @@ spgemm_dense dense(void* data, int64_t rows, int64_t cols, int32_t dtype) {
   return spgemm_dense{data, rows, cols, cols, dtype, 0};
 }
 
-// x laid out in group order (scratch), its rows padded to 16 bytes
-spgemm_dense spread(const spgemm_grouping& g, const spgemm_dense& x, Scratch* scratch, cudaStream_t s) {
-  const int64_t stride = ceil_div(x.cols, 8) * 8;
-  const spgemm_dense rows{scratch->get(2 * g.slots * stride), g.slots, x.cols, stride, x.dtype, 0};
-  if (rows.data) launch_spread_rows(g, x, rows, s);
+// x laid out in group order takes this many bytes; none where its rows are gathered or in order already
+int64_t spread_bytes(const spgemm_grouping& g, const spgemm_dense& x) { return 2 * g.slots * (ceil_div(x.cols, 8) * 8); }
+int64_t forward_bytes(const spgemm_grouping& g, const spgemm_dense& x, bool by_token) {
+  return by_token && !mma_gathers(g) ? spread_bytes(g, x) : 0;
+}
+// lays x out in group order at `to`, its rows padded to 16 bytes
+spgemm_dense spread(const spgemm_grouping& g, const spgemm_dense& x, void* to, cudaStream_t s) {
+  const spgemm_dense rows{to, g.slots, x.cols, ceil_div(x.cols, 8) * 8, x.dtype, 0};
+  launch_spread_rows(g, x, rows, s);
   return rows;
 }
-
-// y = rows * w[g]^T on the tensor cores with x by token or by position
+// y = rows * w[g]^T on the tensor cores with x by token or by position; `to`: forward_bytes
 bool mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool by_token, const spgemm_weights& w, bool gated,
-                 const spgemm_dense& y, Scratch* scratch, cudaStream_t s) {
+                 const spgemm_dense& y, void* to, cudaStream_t s) {
   if (!by_token || mma_gathers(g)) return launch_mma_forward(g, x, by_token, w, gated, y, s);
-  const spgemm_dense rows = spread(g, x, scratch, s);
-  return rows.data && launch_mma_forward(g, rows, false, w, gated, y, s);
+  return launch_mma_forward(g, spread(g, x, to, s), false, w, gated, y, s);
 }
 
 }  // namespace
@@ -154,10 +163,9 @@ int spgemm_route(const spgemm_dense* logits, const spgemm_route_rule* rule, cons
   if (!offsets || (logits->rows > 0 && (!ids || !weights || !order || !position)))
     return bad("route: null output");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  Scratch scratch(st);
-  void* ws = scratch.get(route_scratch_bytes(logits->rows, static_cast<int32_t>(logits->cols)));
+  Scratch scratch(st, {route_scratch_bytes(logits->rows, static_cast<int32_t>(logits->cols))});
   if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
-  launch_route(*logits, *rule, bias, RouteOut{ids, weights, offsets, order, position}, ws, st);
+  launch_route(*logits, *rule, bias, RouteOut{ids, weights, offsets, order, position}, scratch.part(0), st);
   return check_cuda(cudaGetLastError(), "route");
 }
 
@@ -183,10 +191,9 @@ int spgemm_group_rows(const int32_t* ids, int64_t slots, int32_t groups, int32_t
     return SPGEMM_ERR_OVERFLOW;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  Scratch scratch(st);
-  void* ws = scratch.get(group_scratch_bytes(slots, groups));
+  Scratch scratch(st, {group_scratch_bytes(slots, groups)});
   if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
-  launch_group_rows(ids, slots, groups, offsets, order, position, ws, st);
+  launch_group_rows(ids, slots, groups, offsets, order, position, scratch.part(0), st);
   return check_cuda(cudaGetLastError(), "group rows");
 }
 
@@ -202,9 +209,9 @@ int spgemm_grouped_product(const spgemm_grouping* g, const spgemm_dense* x, int3
     return bad("grouped product: types differ");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (mma_takes(*x) && mma_takes(*w)) {
-    Scratch scratch(st);
-    if (!mma_forward(*g, *x, !x_grouped, *w, false, *y, &scratch, st))
-      return scratch.ok() ? launch_failed("grouped product") : SPGEMM_ERR_OUT_OF_MEMORY;
+    Scratch scratch(st, {forward_bytes(*g, *x, !x_grouped)});
+    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
+    if (!mma_forward(*g, *x, !x_grouped, *w, false, *y, scratch.part(0), st)) return launch_failed("grouped product");
   } else {
     launch_plain_forward(*g, *x, !x_grouped, *w, *y, st);
   }
@@ -226,24 +233,20 @@ int spgemm_grouped_product_backward(const spgemm_grouping* g, const spgemm_dense
   if (w->dtype != x->dtype || dy->dtype != x->dtype || (dx && dx->dtype != x->dtype) || (dw && dw->dtype != x->dtype))
     return bad("grouped product backward: types differ");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  Scratch scratch(st);
   const bool mma = g->slots > 0 && mma_takes(*x) && mma_takes(*dy) && mma_takes(*w);
-  if (dx && dx->rows > 0) {
+  const bool need_dx = dx && dx->rows > 0;
+  Scratch scratch(st, {need_dx ? 4 * g->slots * w->cols : 0, dw && mma ? spread_bytes(*g, *x) : 0});
+  if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
+  if (need_dx) {
     // one 32-bit row per position, summed per token afterwards: the sum is rounded once
-    spgemm_dense rows = dense(scratch.get(4 * g->slots * w->cols), g->slots, w->cols, SPGEMM_DTYPE_F32);
-    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
-    float* r = static_cast<float*>(rows.data);
+    float* r = scratch.part<float>(0);
     if (!mma) launch_plain_dx(*g, *dy, *w, r, st);
     else if (!launch_mma_dx(*g, *dy, *w, r, st)) return launch_failed("grouped product backward");
-    launch_combine(*g, nullptr, rows, *dx, st);
+    launch_combine(*g, nullptr, dense(r, g->slots, w->cols, SPGEMM_DTYPE_F32), *dx, st);
   }
-  if (dw && !mma) {
-    launch_plain_dw(*g, *dy, *x, *dw, st);
-  } else if (dw) {
-    const spgemm_dense rows = spread(*g, *x, &scratch, st);
-    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
-    if (!launch_mma_dw(*g, *dy, rows, *dw, st)) return launch_failed("grouped product backward");
-  }
+  if (dw && !mma) launch_plain_dw(*g, *dy, *x, *dw, st);
+  else if (dw && !launch_mma_dw(*g, *dy, spread(*g, *x, scratch.part(1), st), *dw, st))
+    return launch_failed("grouped product backward");
   return check_cuda(cudaGetLastError(), "grouped product backward");
 }
 
@@ -285,18 +288,20 @@ int spgemm_experts(const spgemm_grouping* g, const float* weights, const spgemm_
     return bad("experts: types differ");
   if (x->rows == 0) return SPGEMM_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  Scratch scratch(st);
-  const spgemm_dense h = dense(scratch.get(g->slots * hidden * dtype_size(x->dtype)), g->slots, hidden, x->dtype);
+  spgemm_dense h = dense(nullptr, g->slots, hidden, x->dtype);
+  const bool mma = mma_takes(*x) && mma_takes(*w_up) && mma_takes(h) && mma_takes(*w_down);
   // the down product's rows stay in 32 bits: the weighted sum is rounded once
-  const spgemm_dense y = dense(scratch.get(4 * g->slots * out->cols), g->slots, out->cols, SPGEMM_DTYPE_F32);
-  if (mma_takes(*x) && mma_takes(*w_up) && mma_takes(h) && mma_takes(*w_down)) {
-    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
-    if (!mma_forward(*g, *x, true, *w_up, true, h, &scratch, st) ||
-        !mma_forward(*g, h, false, *w_down, false, y, &scratch, st))
-      return scratch.ok() ? launch_failed("experts") : SPGEMM_ERR_OUT_OF_MEMORY;
+  Scratch scratch(st, {g->slots * hidden * dtype_size(x->dtype), 4 * g->slots * out->cols,
+                       mma ? forward_bytes(*g, *x, true) : 8 * g->slots * hidden});
+  if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
+  h.data = scratch.part(0);
+  const spgemm_dense y = dense(scratch.part(1), g->slots, out->cols, SPGEMM_DTYPE_F32);
+  if (mma) {
+    if (!mma_forward(*g, *x, true, *w_up, true, h, scratch.part(2), st) ||
+        !launch_mma_forward(*g, h, false, *w_down, false, y, st))
+      return launch_failed("experts");
   } else {
-    const spgemm_dense pre = dense(scratch.get(8 * g->slots * hidden), g->slots, 2 * hidden, SPGEMM_DTYPE_F32);
-    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
+    const spgemm_dense pre = dense(scratch.part(2), g->slots, 2 * hidden, SPGEMM_DTYPE_F32);
     launch_plain_forward(*g, *x, true, *w_up, pre, st);
     launch_gated(static_cast<float*>(pre.data), g->slots, hidden, h, st);
     launch_plain_forward(*g, h, false, *w_down, y, st);
@@ -326,30 +331,26 @@ int spgemm_adapted_product(const spgemm_dense* x, const spgemm_dense* w, const s
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t t = x->rows, rank = a->rows;
   const int32_t adapters = static_cast<int32_t>(a->groups);
-  Scratch scratch(st);
-  int32_t* offsets = static_cast<int32_t*>(scratch.get(4 * (adapters + 1)));
-  int32_t* order = static_cast<int32_t*>(scratch.get(4 * t));
-  int32_t* position = static_cast<int32_t*>(scratch.get(4 * t));
-  void* ws = scratch.get(group_scratch_bytes(t, adapters));
+  // v is rounded to x's type between the two small products on the tensor cores, 32-bit otherwise
+  spgemm_dense v{nullptr, t, rank, ceil_div(rank, 8) * 8, x->dtype, 0};
+  const bool mma = mma_takes(*x) && mma_takes(*w) && mma_takes(*a) && mma_takes(*b) && mma_takes(v);
+  if (!mma) v = dense(nullptr, t, rank, SPGEMM_DTYPE_F32);
+  Scratch scratch(st, {4 * (adapters + 1), 4 * t, 4 * t, group_scratch_bytes(t, adapters), t * v.stride * dtype_size(v.dtype),
+                       mma ? 0 : 4 * t * y->cols});
+  if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
+  int32_t *offsets = scratch.part<int32_t>(0), *order = scratch.part<int32_t>(1), *position = scratch.part<int32_t>(2);
+  v.data = scratch.part(4);
+  launch_group_rows(ids, t, adapters, offsets, order, position, scratch.part(3), st);
   const spgemm_grouping g{t, 1, adapters, offsets, order, position};
-  const spgemm_dense v16{nullptr, t, rank, ceil_div(rank, 8) * 8, x->dtype, 0};
-  if (mma_takes(*x) && mma_takes(*w) && mma_takes(*a) && mma_takes(*b) && mma_takes(v16)) {
-    spgemm_dense v = v16;
-    v.data = scratch.get(2 * t * v.stride);
-    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
-    launch_group_rows(ids, t, adapters, offsets, order, position, ws, st);
+  if (mma) {
     if (!launch_mma_shrink(g, *x, *a, scale, v, st) || !launch_mma_adapted(*x, *w, *b, ids, v, *y, st))
       return launch_failed("adapted product");
   } else {
-    const spgemm_dense v = dense(scratch.get(4 * t * rank), t, rank, SPGEMM_DTYPE_F32);
-    const spgemm_dense base = dense(scratch.get(4 * t * y->cols), t, y->cols, SPGEMM_DTYPE_F32);
-    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
-    launch_group_rows(ids, t, adapters, offsets, order, position, ws, st);
+    const spgemm_dense base = dense(scratch.part(5), t, y->cols, SPGEMM_DTYPE_F32);
     launch_plain_forward(g, *x, true, *a, v, st);
     const spgemm_weights shared{w->data, 1, w->rows, w->cols, 0, w->stride, w->dtype, 0};
     launch_plain_forward(spgemm_grouping{t, 1, 1, nullptr, nullptr, nullptr}, *x, false, shared, base, st);
-    launch_plain_adapter_add(g, ids, scale, static_cast<float*>(base.data), static_cast<float*>(v.data), rank, *b, *y,
-                             st);
+    launch_plain_adapter_add(g, ids, scale, static_cast<float*>(base.data), static_cast<float*>(v.data), rank, *b, *y, st);
   }
   return check_cuda(cudaGetLastError(), "adapted product");
 }

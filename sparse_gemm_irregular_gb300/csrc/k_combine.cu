@@ -43,14 +43,24 @@ __global__ void __launch_bounds__(kThreads) k_combine(const int32_t* __restrict_
     float acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-#pragma unroll 4
-    for (int j = 0; j < top_k; ++j) {
-      const int64_t p = position[t * top_k + j];
-      if (p < 0 || p >= slots) continue;
-      const float w = weights ? weights[t * top_k + j] : 1.0f;
-      const Pack<TY, V> r = *reinterpret_cast<const Pack<TY, V>*>(y + p * y_stride + c);
+    // four rows at a time: their loads are all under way before the first is added
+    for (int j0 = 0; j0 < top_k; j0 += 4) {
+      Pack<TY, V> row[4];
+      float w[4];
+      bool there[4];
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += w * to_f32(r.v[v]);
+      for (int j = 0; j < 4; ++j) {
+        const int64_t p = j0 + j < top_k ? position[t * top_k + j0 + j] : -1;
+        there[j] = p >= 0 && p < slots;
+        w[j] = there[j] && weights ? weights[t * top_k + j0 + j] : 1.0f;
+        if (there[j]) row[j] = *reinterpret_cast<const Pack<TY, V>*>(y + p * y_stride + c);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (there[j]) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] += w[j] * to_f32(row[j].v[v]);
+        }
     }
     Pack<TO, V> o;
 #pragma unroll
