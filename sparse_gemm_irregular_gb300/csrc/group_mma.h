@@ -13,6 +13,7 @@ struct MmaArgs {
   int slots, groups, top_k;
   int rows;                // rows of the gathered matrix: the index that reads as zeros
   int gather, scatter;
+  int early;               // the kernel before makes only the rows of B (or v): start without waiting for it
   int runs;                // gathered rows often follow one another
   int bf16;
   int m, n, depth;         // M side, N side (Dw only), contracted length
@@ -37,8 +38,10 @@ bool mma_gathers(const spgemm_grouping& g);
 
 // The same contracts as the launch_plain_* functions; false: the launch failed (cudaGetLastError
 // or the encoding of a copy descriptor).
+// early: x is made by the kernel launched just before on the stream, which was itself launched by launch_next or
+// by these functions and makes nothing else that is read here.
 bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool gather, const spgemm_weights& w,
-                        bool gated, const spgemm_dense& y, cudaStream_t s);
+                        bool gated, const spgemm_dense& y, bool early, cudaStream_t s);
 bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_weights& w, float* dx,
                    cudaStream_t s);
 // x with one row per position here
@@ -47,7 +50,7 @@ bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
 // v[t, :] = scale[i] * x[t] * a[i]^T, rounded to x's type, for the rows of every adapter i
 bool launch_mma_shrink(const spgemm_grouping& g, const spgemm_dense& x, const spgemm_weights& a, const float* scale,
                        const spgemm_dense& v, cudaStream_t s);
-// y[t, :] = x[t] * w^T + v[t] * b[ids[t]]^T
+// y[t, :] = x[t] * w^T + v[t] * b[ids[t]]^T; v is made by the launch_mma_shrink just before
 bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spgemm_weights& b, const int32_t* ids,
                         const spgemm_dense& v, const spgemm_dense& y, cudaStream_t s);
 

@@ -139,8 +139,8 @@ spgemm_dense spread(const spgemm_grouping& g, const spgemm_dense& x, void* to, c
 // y = rows * w[g]^T on the tensor cores with x by token or by position; `to`: forward_bytes
 bool mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool by_token, const spgemm_weights& w, bool gated,
                  const spgemm_dense& y, void* to, cudaStream_t s) {
-  if (!by_token || mma_gathers(g)) return launch_mma_forward(g, x, by_token, w, gated, y, s);
-  return launch_mma_forward(g, spread(g, x, to, s), false, w, gated, y, s);
+  if (!by_token || mma_gathers(g)) return launch_mma_forward(g, x, by_token, w, gated, y, false, s);
+  return launch_mma_forward(g, spread(g, x, to, s), false, w, gated, y, true, s);
 }
 
 }  // namespace
@@ -298,7 +298,7 @@ int spgemm_experts(const spgemm_grouping* g, const float* weights, const spgemm_
   const spgemm_dense y = dense(scratch.part(1), g->slots, out->cols, SPGEMM_DTYPE_F32);
   if (mma) {
     if (!mma_forward(*g, *x, true, *w_up, true, h, scratch.part(2), st) ||
-        !launch_mma_forward(*g, h, false, *w_down, false, y, st))
+        !launch_mma_forward(*g, h, false, *w_down, false, y, true, st))
       return launch_failed("experts");
   } else {
     const spgemm_dense pre = dense(scratch.part(2), g->slots, 2 * hidden, SPGEMM_DTYPE_F32);

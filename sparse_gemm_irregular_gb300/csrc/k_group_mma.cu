@@ -125,8 +125,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
   }
   if (PAIR) cluster_sync();  // both blocks run before one allocates in both
   if (warp == kProducers) tmem_alloc<PAIR>(smem_u32(&c.tmem), tmem_cols);
-  pdl_wait();
-  pdl_go();
+  // `early`: the kernel before this one (of the same call, itself started after everything before it was
+  // complete) makes only the rows of B, or v.  Weights, offsets and ids are read while it ends.
+  if (!p.early) {
+    pdl_wait();
+    pdl_go();
+  }
   // offsets are used as a non-decreasing sequence inside [0, slots], whatever the array holds
   {
     int run = 0;
@@ -203,7 +207,13 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
     // ---- producers ---------------------------------------------------------------------------------
     int s = 0;
     uint32_t phase = 0;
-    bool ok = true;
+    bool ok = true, waited = !p.early;
+    auto wait_before = [&]() {
+      if (waited) return;
+      pdl_wait();
+      pdl_go();
+      waited = true;
+    };
     for (Walk w = start(); w.r < all_tiles && ok; advance(w)) {
       const Tile t = tile_of(w);
       const int cols = columns(t.n), half = cols / kSide;
@@ -336,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
       };
       const int box = lane == 31 ? warp : 2;
       if (!boxed) {
+        wait_before();
         for (int q = q0; q < q1 && ok; ++q) {
           const uint32_t a = open(bytes, q + 1 == q1);
           if (!ok) break;
@@ -345,25 +356,41 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           close();
         }
       } else {
+        // fills the stage's next slice h: A's boxes, B's boxes, or both, dealt over the warps
+        auto fill = [&](int q, int h, bool with_a, bool with_b, uint32_t fb) {
+          const uint32_t a = base + s * p.stage_bytes + h * p.sub_bytes;
+          const int k0 = (q + h) * kDeep;
+          for (int u = warp; u < boxes_a + boxes; u += kProducers) {
+            const int v = u - boxes_a;
+            if (v < 0 && with_a) copy_a(a, u, k0, fb);
+            if (v >= 0 && with_b) load_2d<PAIR>(a + kABytes + v * p.box_rows * 128, map_b, k0, row_b + v * p.box_rows, fb);
+          }
+        };
+        int ahead = 0;  // stages whose A is on its way
+        if (MODE != kMmaAdapted && !waited) {
+          for (int q = q0; q < q1 && ahead < p.stages; q += kSub, ++ahead) {
+            const int subs = min(kSub, q1 - q);
+            if (lane == 0) {
+              if (warp == 0 && rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
+              for (int h = 0; h < subs; ++h) fill(q, h, true, false, bar());
+            }
+            close();
+          }
+          s = 0;
+          phase = 0;
+          wait_before();
+        }
         for (int q = q0; q < q1; q += kSub) {  // one lane of each warp; the others only keep count
           const int subs = min(kSub, q1 - q);
+          const bool fresh = ahead-- <= 0;
           if (lane == 0 && ok) {
-            ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
+            if (fresh) ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
             if (ok) {
-              if (warp == 0) {
+              if (warp == 0 && fresh) {
                 if (MODE == kMmaAdapted) c.last[s] = q + subs == q1 && adapter < 0 ? 1 : 0;
                 if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
               }
-              const uint32_t fb = bar();
-              for (int h = 0; h < subs; ++h) {
-                const uint32_t a = base + s * p.stage_bytes + h * p.sub_bytes;
-                const int k0 = (q + h) * kDeep;
-                for (int u = warp; u < boxes_a + boxes; u += kProducers) {
-                  const int v = u - boxes_a;
-                  if (v < 0) copy_a(a, u, k0, fb);
-                  else load_2d<PAIR>(a + kABytes + v * p.box_rows * 128, map_b, k0, row_b + v * p.box_rows, fb);
-                }
-              }
+              for (int h = 0; h < subs; ++h) fill(q, h, fresh, true, bar());
             }
           }
           close();
@@ -371,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
       // then, per adapter, its b against the v rows of its own tokens (the others' read as zeros)
+      if (MODE == kMmaAdapted && adapter >= 0) wait_before();
       while (MODE == kMmaAdapted && ok && adapter >= 0) {
         const int after = mine_after(adapter, parts - 1);
         int r[4];
@@ -556,6 +584,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           else static_cast<uint16_t*>(p.out)[o] = 0;
         }
     }
+  }
+  if (p.early) {  // blocks without a tile, and tiles without an adapter, have not waited yet
+    pdl_wait();
+    pdl_go();
   }
   fence_before();
   __syncthreads();
@@ -760,9 +792,10 @@ bool mma_takes(const spgemm_weights& w) {
 }
 
 bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool gather, const spgemm_weights& w,
-                        bool gated, const spgemm_dense& y, cudaStream_t s) {
+                        bool gated, const spgemm_dense& y, bool early, cudaStream_t s) {
   if (g.slots == 0) return true;
   MmaArgs a = base_args(g, x.dtype);
+  a.early = early;
   a.rows = static_cast<int>(x.rows);
   a.gather = gather;
   a.m = static_cast<int>(y.cols);
@@ -842,6 +875,7 @@ bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spge
   a.ids = ids;
   a.adapters = static_cast<int>(b.groups);
   a.rank = static_cast<int>(b.cols);
+  a.early = 1;
   a.m = static_cast<int>(y.cols);
   a.depth = static_cast<int>(x.cols);
   // the widest tile that still gives every SM one; few rows: one tile, its depth split
