@@ -7,12 +7,19 @@ current stream and do not synchronise.  ``Routing`` is the choice together with 
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 from dataclasses import dataclass
 from typing import Any
 
 from . import binding
-from .binding import _check, load, spgemm_dense, spgemm_grouping, spgemm_route_rule, spgemm_weights
+from .binding import _check, load
+
+# The structures of include/spgemm.h as bytes (a call borrows them): packed in one step, these calls are
+# short enough for the difference to ctypes' field-by-field structures to count.
+_pack_dense = struct.Struct("@Pqqqii").pack        # spgemm_dense
+_pack_weights = struct.Struct("@Pqqqqqii").pack    # spgemm_weights
+_pack_grouping = struct.Struct("@qiiPPP").pack     # spgemm_grouping
+_pack_rule = struct.Struct("@6ifi").pack           # spgemm_route_rule
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _GROUP_SCORES = {"max": 0, "top2": 1}
@@ -35,16 +42,16 @@ class Routing:
 
     def __post_init__(self):
         import torch
-        i32 = torch.int32
-        n = self.ids.numel()
-        for t, name, dtype, size in ((self.ids, "ids", i32, n), (self.weights, "weights", torch.float32, n),
-                                     (self.offsets, "offsets", i32, -1), (self.order, "order", i32, n),
-                                     (self.position, "position", i32, n)):
-            _want(t, name, dtype)
-            if size >= 0 and t.numel() != size:
+        i32, n = torch.int32, self.ids.numel()
+        for name in ("ids", "offsets", "order", "position", "weights"):
+            t = getattr(self, name)
+            if t.dtype is not (torch.float32 if name == "weights" else i32) or not t.is_cuda or not t.is_contiguous():
+                raise ValueError("%s: a contiguous CUDA tensor of %s is wanted"
+                                 % (name, "float32" if name == "weights" else "int32"))
+            if t.numel() != n and name != "offsets":
                 raise ValueError("routing: ids, weights, order and position want tokens * top_k entries each")
-        if self.ids.dim() != 2:
-            raise ValueError("ids: (tokens, top_k) is wanted")
+        if self.ids.dim() != 2 or self.offsets.dim() != 1:
+            raise ValueError("ids: (tokens, top_k) and offsets: (groups + 1) are wanted")
 
     @classmethod
     def _made(cls, ids, weights, offsets, order, position, rule=None) -> "Routing":
@@ -54,9 +61,10 @@ class Routing:
         return r
 
     @property
-    def _grouping(self) -> spgemm_grouping:
-        return spgemm_grouping(self.ids.numel(), self.ids.shape[1], self.offsets.numel() - 1, self.offsets.data_ptr(),
-                               self.order.data_ptr(), self.position.data_ptr())
+    def _grouping(self) -> bytes:
+        tokens, k = self.ids.shape
+        return _pack_grouping(tokens * k, k, self.offsets.shape[0] - 1, self.offsets.data_ptr(), self.order.data_ptr(),
+                              self.position.data_ptr())
 
     @property
     def tokens(self) -> int:
@@ -111,33 +119,35 @@ def _want(t, name: str, dtype):
         raise ValueError("%s: a contiguous CUDA tensor of %s is wanted" % (name, dtype))
 
 
-def _dense(t, name: str) -> spgemm_dense:
+def _dense(t, name: str) -> bytes:
     shape, step, code = t.shape, t.stride(), _codes.get(t.dtype)
     if code is None or not t.is_cuda or len(shape) != 2 or (step[1] != 1 and shape[1] > 1):
         _refuse(t, name, 2)
         code = _codes[t.dtype]
     rows, cols = shape
-    return spgemm_dense(t.data_ptr(), rows, cols, step[0] if step[0] > cols else cols, code, 0)
+    return _pack_dense(t.data_ptr(), rows, cols, step[0] if step[0] > cols else cols, code, 0)
 
 
-def _weights(t, name: str) -> spgemm_weights:
+def _weights(t, name: str) -> bytes:
     shape, step, code = t.shape, t.stride(), _codes.get(t.dtype)
     if code is None or not t.is_cuda or len(shape) != 3 or (step[2] != 1 and shape[2] > 1):
         _refuse(t, name, 3)
         code = _codes[t.dtype]
     groups, rows, cols = shape
-    return spgemm_weights(t.data_ptr(), groups, rows, cols, step[0], step[1] if step[1] > cols else cols, code, 0)
+    return _pack_weights(t.data_ptr(), groups, rows, cols, step[0], step[1] if step[1] > cols else cols, code, 0)
 
 
-_ref = ctypes.byref
+_entry: dict = {}  # entry points by name
 
 
 def _call(name: str, device, stream, *args):
     """Call an entry point with `device` current and the given or the current stream as last argument."""
     import torch
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(load(), name)
     index = device.index
-    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
-    fn = getattr(load(), name)
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == index:
         rc = fn(*args, raw)
     else:
@@ -158,19 +168,19 @@ def route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int 
     d = _dense(logits, "logits")
     if score not in _SCORES or group_score not in _GROUP_SCORES:
         raise ValueError("score: softmax or sigmoid; group_score: max or top2")
-    rule = spgemm_route_rule(top_k, _SCORES[score], groups, groups_kept, _GROUP_SCORES[group_score], bool(renormalise),
-                             scale, 0)
+    rule = _pack_rule(top_k, _SCORES[score], groups, groups_kept, _GROUP_SCORES[group_score], bool(renormalise), scale,
+                      0)
     if bias is not None:
         _want(bias, "bias", torch.float32)
         if bias.numel() != logits.shape[1]:
             raise ValueError("bias: one value per expert is wanted")
-    t, dev, k = logits.shape[0], logits.device, max(int(top_k), 1)
+    t, dev, k = logits.shape[0], logits.device, min(max(int(top_k), 1), 32)  # other values are refused below
     n = t * k
     weights = torch.empty((t, k), dtype=torch.float32, device=dev)
     whole = torch.empty(3 * n + logits.shape[1] + 1, dtype=torch.int32, device=dev)  # one allocation for four arrays
     ids, position = whole.as_strided((t, k), (k, 1)), whole.as_strided((t, k), (k, 1), n)
     order, offsets = whole.as_strided((n,), (1,), 2 * n), whole.as_strided((logits.shape[1] + 1,), (1,), 3 * n)
-    _call("spgemm_route", dev, stream, _ref(d), _ref(rule), bias.data_ptr() if bias is not None else None,
+    _call("spgemm_route", dev, stream, d, rule, bias.data_ptr() if bias is not None else None,
           ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), position.data_ptr())
     return Routing._made(ids, weights, offsets, order, position, rule)
 
@@ -185,8 +195,8 @@ def route_backward(logits, routing: Routing, grad_weights, *, stream=None):
     if grad_weights.shape != routing.ids.shape or logits.shape[0] != routing.tokens:
         raise ValueError("grad_weights: (tokens, top_k) is wanted")
     out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    _call("spgemm_route_backward", logits.device, stream, _ref(d), _ref(routing.rule), routing.ids.data_ptr(),
-          grad_weights.data_ptr(), _ref(_dense(out, "grad_logits")))
+    _call("spgemm_route_backward", logits.device, stream, d, routing.rule, routing.ids.data_ptr(),
+          grad_weights.data_ptr(), _dense(out, "grad_logits"))
     return out
 
 
@@ -218,8 +228,8 @@ def expert_product(x, w, routing: Routing, *, grouped: bool = False, out_dtype=N
     import torch
     g = routing._grouping
     dx, dw = _dense(x, "x"), _weights(w, "w")
-    y = torch.empty((g.slots, w.shape[1]), dtype=out_dtype or x.dtype, device=x.device)
-    _call("spgemm_grouped_product", x.device, stream, _ref(g), _ref(dx), int(grouped), _ref(dw), _ref(_dense(y, "y")))
+    y = torch.empty((routing.ids.numel(), w.shape[1]), dtype=out_dtype or x.dtype, device=x.device)
+    _call("spgemm_grouped_product", x.device, stream, g, dx, int(grouped), dw, _dense(y, "y"))
     return y
 
 
@@ -229,9 +239,9 @@ def expert_product_backward(dy, x, w, routing: Routing, *, need_dx: bool = True,
     g = routing._grouping
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
     dw = torch.empty(w.shape, dtype=w.dtype, device=x.device) if need_dw else None
-    _call("spgemm_grouped_product_backward", x.device, stream, _ref(g), _ref(_dense(dy, "dy")), _ref(_dense(x, "x")),
-          _ref(_weights(w, "w")), _ref(_dense(dx, "dx")) if need_dx else None,
-          _ref(_weights(dw, "dw")) if need_dw else None)
+    _call("spgemm_grouped_product_backward", x.device, stream, g, _dense(dy, "dy"), _dense(x, "x"),
+          _weights(w, "w"), _dense(dx, "dx") if need_dx else None,
+          _weights(dw, "dw") if need_dw else None)
     return dx, dw
 
 
@@ -240,8 +250,8 @@ def combine(y, routing: Routing, *, out_dtype=None, stream=None):
     import torch
     g = routing._grouping
     out = torch.empty((routing.tokens, y.shape[1]), dtype=out_dtype or y.dtype, device=y.device)
-    _call("spgemm_combine", y.device, stream, _ref(g), routing.weights.data_ptr(), _ref(_dense(y, "y")),
-          _ref(_dense(out, "out")))
+    _call("spgemm_combine", y.device, stream, g, routing.weights.data_ptr(), _dense(y, "y"),
+          _dense(out, "out"))
     return out
 
 
@@ -251,8 +261,8 @@ def combine_backward(dout, y, routing: Routing, *, stream=None):
     g = routing._grouping
     dy = torch.empty(y.shape, dtype=y.dtype, device=y.device)
     dweights = torch.empty(routing.ids.shape, dtype=torch.float32, device=y.device)
-    _call("spgemm_combine_backward", y.device, stream, _ref(g), routing.weights.data_ptr(),
-          _ref(_dense(dout, "dout")), _ref(_dense(y, "y")), _ref(_dense(dy, "dy")), dweights.data_ptr())
+    _call("spgemm_combine_backward", y.device, stream, g, routing.weights.data_ptr(),
+          _dense(dout, "dout"), _dense(y, "y"), _dense(dy, "dy"), dweights.data_ptr())
     return dy, dweights
 
 
@@ -262,8 +272,8 @@ def experts(x, w_up, w_down, routing: Routing, *, stream=None):
     import torch
     g = routing._grouping
     out = torch.empty((x.shape[0], w_down.shape[1]), dtype=x.dtype, device=x.device)
-    _call("spgemm_experts", x.device, stream, _ref(g), routing.weights.data_ptr(), _ref(_dense(x, "x")),
-          _ref(_weights(w_up, "w_up")), _ref(_weights(w_down, "w_down")), _ref(_dense(out, "out")))
+    _call("spgemm_experts", x.device, stream, g, routing.weights.data_ptr(), _dense(x, "x"),
+          _weights(w_up, "w_up"), _weights(w_down, "w_down"), _dense(out, "out"))
     return out
 
 
@@ -281,9 +291,9 @@ def adapted_product(x, w, a, b, ids, scale=None, *, stream=None):
         if scale.numel() != a.shape[0]:
             raise ValueError("scale: one value per adapter is wanted")
     y = torch.empty((x.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
-    _call("spgemm_adapted_product", x.device, stream, _ref(_dense(x, "x")), _ref(_dense(w, "w")),
-          _ref(_weights(a, "a")), _ref(_weights(b, "b")), ids.data_ptr(),
-          scale.data_ptr() if scale is not None else None, _ref(_dense(y, "y")))
+    _call("spgemm_adapted_product", x.device, stream, _dense(x, "x"), _dense(w, "w"),
+          _weights(a, "a"), _weights(b, "b"), ids.data_ptr(),
+          scale.data_ptr() if scale is not None else None, _dense(y, "y"))
     return y
 
 

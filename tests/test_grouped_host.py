@@ -33,6 +33,21 @@ def test_struct_layouts_match_the_header(tmp_path):
     assert got == want
 
 
+def test_packed_structures_have_the_layouts():
+    from sparse_gemm_irregular_gb300 import grouped as G
+    d = b.spgemm_dense.from_buffer_copy(G._pack_dense(16, 2, 3, 4, 1, 0))
+    assert (d.data, d.rows, d.cols, d.stride, d.dtype) == (16, 2, 3, 4, 1)
+    w = b.spgemm_weights.from_buffer_copy(G._pack_weights(16, 2, 3, 4, 5, 6, 2, 0))
+    assert (w.data, w.groups, w.rows, w.cols, w.group_stride, w.row_stride, w.dtype) == (16, 2, 3, 4, 5, 6, 2)
+    g = b.spgemm_grouping.from_buffer_copy(G._pack_grouping(6, 2, 3, 16, 32, 48))
+    assert (g.slots, g.top_k, g.groups, g.offsets, g.order, g.position) == (6, 2, 3, 16, 32, 48)
+    r = b.spgemm_route_rule.from_buffer_copy(G._pack_rule(1, 0, 3, 2, 1, True, 2.5, 0))
+    assert (r.top_k, r.score, r.groups, r.groups_kept, r.group_score, r.renormalise, r.scale) == (1, 0, 3, 2, 1, 1, 2.5)
+    for pack, cls in ((G._pack_dense, b.spgemm_dense), (G._pack_weights, b.spgemm_weights),
+                      (G._pack_grouping, b.spgemm_grouping), (G._pack_rule, b.spgemm_route_rule)):
+        assert pack.__self__.size == ctypes.sizeof(cls)
+
+
 def dense(rows, cols, stride=None, dtype=1, data=16):
     return b.spgemm_dense(data, rows, cols, cols if stride is None else stride, dtype, 0)
 
