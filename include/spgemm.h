@@ -476,6 +476,12 @@ int spgemm_adapted_product(const spgemm_dense* x, const spgemm_dense* w, const s
  * SPGEMM_OK, or SPGEMM_ERR_DEVICE when a device-side check failed since the last call. */
 int spgemm_grouped_status(void* stream);
 
+/* For tests: polls > 0 limits every wait inside the tensor-core kernels of later calls of this process
+ * to that many polls (0: about a second's worth), and hold != 0 makes the first block of each such
+ * kernel withhold one announcement, so that a wait runs out and spgemm_grouped_status answers
+ * SPGEMM_ERR_DEVICE; that call's results are meaningless, the context and later calls are not affected. */
+int spgemm_grouped_debug(int32_t hold, int32_t polls);
+
 const char* spgemm_strerror(int code);
 /* Detail of the last failure on the calling host thread ("" if none). */
 const char* spgemm_last_error(void);

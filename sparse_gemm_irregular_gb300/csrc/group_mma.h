@@ -27,7 +27,12 @@ struct MmaArgs {
   int adapters, rank;
   int split;               // blocks that share a tile's contracted range
   uint32_t* err;
+  uint32_t polls;          // of every wait
+  int hold;                // tests: withhold an announcement
 };
+
+// see spgemm_grouped_debug
+void mma_debug(int32_t hold, int32_t polls);
 
 // whether the copy engine can fetch rows of this matrix: 16-bit, 16-byte aligned rows
 bool mma_takes(const spgemm_dense& m);

@@ -355,6 +355,12 @@ int spgemm_adapted_product(const spgemm_dense* x, const spgemm_dense* w, const s
   return check_cuda(cudaGetLastError(), "adapted product");
 }
 
+int spgemm_grouped_debug(int32_t hold, int32_t polls) {
+  if (polls < 0) return bad("grouped debug: negative polls");
+  mma_debug(hold, polls);
+  return SPGEMM_OK;
+}
+
 int spgemm_grouped_status(void* stream) {
   set_last_error("");
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -36,6 +36,7 @@
 // Every wait is bounded: a role that gives up sets the status word, the others see it, copies in
 // flight are drained, tensor memory is freed, the kernel returns.
 #include <algorithm>
+#include <atomic>
 
 #include "group_mma.h"
 #include "tc.cuh"
@@ -103,6 +104,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
   constexpr int kSub = PAIR ? 2 : 1;  // slices of a stage
   constexpr bool kDw = MODE == kMmaDw;
   volatile int* failed = &c.failed;
+  const uint32_t drain_polls = max(p.polls >> 4, 64u);
+  bool hold = p.hold && blockIdx.x == 0;  // tests: block 0 never announces its first slice
 
   // ---- set-up: barriers, tensor memory, the groups' first positions and tile counts -----------
   if (warp == 0) {
@@ -235,11 +238,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
       // one slice: waits for a free stage and announces its bytes; returns the stage's address.  A copy of
       // another warp may be done before the bytes are announced: the announcement is the barrier's only arrival
       auto open = [&](uint32_t bytes, bool last) -> uint32_t {
-        ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
+        ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u, p.polls);
         ok = __all_sync(0xffffffffu, ok);
         if (ok && warp == 0 && lane == 0) {
           c.last[s] = last ? 1 : 0;
-          if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), bytes * kSide);
+          if (rank == 0 && !hold) mbar_expect_tx(smem_u32(&c.full[s]), bytes * kSide);
+          hold = false;
         }
         return base + s * p.stage_bytes;
       };
@@ -263,9 +267,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         for (int q = 0; q < whole; q += kSub) {  // one lane of each warp; the others only keep count
           const int subs = min(kSub, whole - q);
           if (lane == 0 && ok) {
-            ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
+            ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u, p.polls);
             if (ok) {
-              if (warp == 0 && rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
+              if (warp == 0 && rank == 0 && !hold) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
+              hold = false;
               const uint32_t fb = bar();
               for (int h = 0; h < subs; ++h)
                 for (int u = warp; u < 2 + nb; u += kProducers)
@@ -371,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           for (int q = q0; q < q1 && ahead < p.stages; q += kSub, ++ahead) {
             const int subs = min(kSub, q1 - q);
             if (lane == 0) {
-              if (warp == 0 && rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
+              if (warp == 0 && rank == 0 && !hold) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
+              hold = false;
               for (int h = 0; h < subs; ++h) fill(q, h, true, false, bar());
             }
             close();
@@ -384,11 +390,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           const int subs = min(kSub, q1 - q);
           const bool fresh = ahead-- <= 0;
           if (lane == 0 && ok) {
-            if (fresh) ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
+            if (fresh) ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u, p.polls);
             if (ok) {
               if (warp == 0 && fresh) {
                 if (MODE == kMmaAdapted) c.last[s] = q + subs == q1 && adapter < 0 ? 1 : 0;
-                if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
+                if (rank == 0 && !hold) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
+                hold = false;
               }
               for (int h = 0; h < subs; ++h) fill(q, h, fresh, true, bar());
             }
@@ -419,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
     // after a failure nothing consumes the stages any more: wait for the copies in flight
     if (*failed) {
       for (int q = 0; q < p.stages; ++q) {
-        mbar_drain(smem_u32(&c.full[s]), phase ^ 1u);
+        mbar_drain(smem_u32(&c.full[s]), phase ^ 1u, drain_polls);
         if (++s == p.stages) {
           s = 0;
           phase ^= 1u;
@@ -438,14 +445,14 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         if (t.k == 0) continue;  // an empty group's gradient: the epilogue writes zeros
         const uint32_t idesc = instruction(p.bf16, kARows, kBRows, 128 * kSide, columns(t.n));
         const uint32_t acc = tmem + (it & 1) * p.tile_n;
-        ok = mbar_wait(smem_u32(&c.acc_empty[it & 1]), ((it >> 1) & 1) ^ 1u, failed, p.err, 2u);
+        ok = mbar_wait(smem_u32(&c.acc_empty[it & 1]), ((it >> 1) & 1) ^ 1u, failed, p.err, 2u, p.polls);
         fence_after();
         const int slices = (t.k + kDeep - 1) / kDeep;
         const int n = SPLIT ? slices * (part + 1) / parts - slices * part / parts : slices;
         const int paired = kDw ? t.k / kDeep : n;  // slices that come kSub to a stage
         bool last = false;
         for (int q = 0; ok && !last;) {
-          ok = mbar_wait(smem_u32(&c.full[s]), phase, failed, p.err, 4u);
+          ok = mbar_wait(smem_u32(&c.full[s]), phase, failed, p.err, 4u, p.polls);
           if (!ok) break;
           fence_after();
           // slices that come kSub to a stage; part slices and adapters' come alone.  (A rows gathered one to a
@@ -469,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
       }
       if (*failed) {
         commit<PAIR>(smem_u32(&c.drain));
-        mbar_drain(smem_u32(&c.drain), 0);
+        mbar_drain(smem_u32(&c.drain), 0, drain_polls);
       }
     }
     __syncwarp();
@@ -483,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
       const Tile t = tile_of(w);
       const bool zero = t.k == 0;
       if (!zero) {
-        ok = mbar_wait(smem_u32(&c.acc_full[it & 1]), (it >> 1) & 1, failed, p.err, 8u);
+        ok = mbar_wait(smem_u32(&c.acc_full[it & 1]), (it >> 1) & 1, failed, p.err, 8u, p.polls);
         ok = __all_sync(0xffffffffu, ok);
         if (MODE == kMmaGated) {  // the warps meet below: they go on together or not at all
           if ((warp - kProducers - 1) % 4 == 0 && lane == 0) c.go[set][it & 1] = ok;
@@ -767,8 +774,13 @@ int pick_tile(int64_t slots, int64_t groups, int most) {
   return n;
 }
 
+std::atomic<int32_t> g_hold{0}, g_polls{0};  // set by tests
+
 MmaArgs base_args(const spgemm_grouping& g, int32_t dtype) {
   MmaArgs a = {};
+  const int32_t polls = g_polls.load(std::memory_order_relaxed);
+  a.hold = g_hold.load(std::memory_order_relaxed);
+  a.polls = polls > 0 ? static_cast<uint32_t>(polls) : tc::kMaxPolls;
   a.offsets = g.offsets;
   a.order = g.order;
   a.slots = static_cast<int>(g.slots);
@@ -782,6 +794,11 @@ MmaArgs base_args(const spgemm_grouping& g, int32_t dtype) {
 bool aligned(const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0; }
 
 }  // namespace
+
+void mma_debug(int32_t hold, int32_t polls) {
+  g_hold.store(hold, std::memory_order_relaxed);
+  g_polls.store(polls, std::memory_order_relaxed);
+}
 
 bool mma_gathers(const spgemm_grouping& g) { return pick_tile(g.slots, g.groups, 256) <= 128; }
 

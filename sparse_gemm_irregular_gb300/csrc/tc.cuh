@@ -38,12 +38,13 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-constexpr uint32_t kMaxPolls = 1u << 18;
+constexpr uint32_t kMaxPolls = 1u << 18;  // a poll that fails takes 3 us: about a second
 
-// Waits for the phase; gives up (false) after kMaxPolls polls or when another role of the block
-// gave up, so that no wait is endless and all roles leave together.  The status word keeps `site`.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* failed, uint32_t* err, uint32_t site) {
-  for (uint32_t i = 0; i < kMaxPolls; ++i) {
+// Waits for the phase; gives up (false) after `polls` polls or when another role of the block gave
+// up, so that no wait is endless and all roles leave together.  The status word keeps `site`.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* failed, uint32_t* err, uint32_t site,
+                                          uint32_t polls) {
+  for (uint32_t i = 0; i < polls; ++i) {
     if (mbar_try(bar, parity)) return true;
     if ((i & 15u) == 15u && *failed) return false;
   }
@@ -52,8 +53,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   return false;
 }
 // the same, for draining after a failure: bounded, reports nothing
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
-  for (uint32_t i = 0; i < (kMaxPolls >> 4); ++i)
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint32_t polls) {
+  for (uint32_t i = 0; i < polls; ++i)
     if (mbar_try(bar, parity)) return;
 }
 

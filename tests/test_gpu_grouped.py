@@ -485,3 +485,37 @@ def test_refusals(gpu_lib):
         gpu_lib.expert_product(x.cpu(), w, r)
     with pytest.raises(ValueError):
         gpu_lib.route_backward(l, gpu_lib.group_rows(r.ids, 8), torch.zeros(4, 2, device="cuda"))
+
+
+def test_a_wait_that_runs_out_is_reported(gpu_lib):
+    """A withheld announcement makes a wait run out in every kind of tensor-core kernel: the status says
+    so, and the same calls are right afterwards."""
+    import torch
+    lib = gpu_lib.load()
+    ids = _random_ids(2, 600, 2, 2)
+    few = _random_ids(3, 6, 4, 2)
+    r, rf = _routing(gpu_lib, ids, 2), _routing(gpu_lib, few, 4)
+    x, w = _normal(1, 600, 256).cuda(), _normal(2, 2, 256, 256, std=1 / 16).cuda()
+    xf, wf = _normal(3, 6, 256).cuda(), _normal(4, 4, 128, 256).cuda()
+    dy = _normal(5, 1200, 256).cuda()
+    a, b = _normal(6, 3, 16, 256, std=1 / 16).cuda(), _normal(7, 3, 256, 16).cuda()
+    which = torch.randint(0, 3, (600,), generator=_gen(8)).int().cuda()
+    calls = [lambda: gpu_lib.expert_product(x, w, r), lambda: gpu_lib.expert_product(xf, wf, rf),
+             lambda: gpu_lib.experts(x, w, w[:, :, :128].contiguous(), r),
+             lambda: gpu_lib.expert_product_backward(dy, x, w, r, need_dw=False)[0],
+             lambda: gpu_lib.expert_product_backward(dy, x, w, r, need_dx=False)[1],
+             lambda: gpu_lib.adapted_product(x, w[0], a, b, which),
+             lambda: gpu_lib.adapted_product(xf, w[0], a, b, which[:6].contiguous())]
+    for call in calls:
+        before = call().clone()
+        gpu_lib.grouped_status()
+        try:
+            assert lib.spgemm_grouped_debug(1, 500) == 0
+            call()
+            with pytest.raises(gpu_lib.SpgemmError) as e:
+                gpu_lib.grouped_status()
+            assert e.value.code == -6 and "wait" in str(e.value)
+        finally:
+            lib.spgemm_grouped_debug(0, 0)
+        assert torch.equal(call(), before)
+        gpu_lib.grouped_status()
