@@ -62,7 +62,7 @@ struct Control {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
-  int failed;
+  int failed[2];                   // a role gave up; polls allowed to a wait
   int go[kSets][2];                // Gated: whether the four warps of a set take the next tile
   int last[kMaxStages];            // 1: the stage holds the last slice of its tile
   int scan[33];
@@ -103,21 +103,21 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
   constexpr int kSide = PAIR ? 2 : 1;
   constexpr int kSub = PAIR ? 2 : 1;  // slices of a stage
   constexpr bool kDw = MODE == kMmaDw;
-  volatile int* failed = &c.failed;
-  const uint32_t drain_polls = max(p.polls >> 4, 64u);
-  bool hold = p.hold && blockIdx.x == 0;  // tests: block 0 never announces its first slice
+  volatile int* failed = c.failed;
 
   // ---- set-up: barriers, tensor memory, the groups' first positions and tile counts -----------
   if (warp == 0) {
     if (lane < p.stages) {
-      mbar_init(smem_u32(&c.full[lane]), 1);
+      // tests: an arrival that never comes, on the first stage of block 0
+      mbar_init(smem_u32(&c.full[lane]), p.hold && blockIdx.x == 0 && lane == 0 ? 2 : 1);
       mbar_init(smem_u32(&c.empty[lane]), 1);
     } else if (lane < p.stages + 2) {
       mbar_init(smem_u32(&c.acc_full[lane - p.stages]), 1);
       mbar_init(smem_u32(&c.acc_empty[lane - p.stages]), kEpilogue * kSide);
     } else if (lane == 31) {
       mbar_init(smem_u32(&c.drain), 1);
-      c.failed = 0;
+      c.failed[0] = 0;
+      c.failed[1] = static_cast<int>(p.polls);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   } else if (warp == 1 && lane == 0) {
@@ -238,12 +238,11 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
       // one slice: waits for a free stage and announces its bytes; returns the stage's address.  A copy of
       // another warp may be done before the bytes are announced: the announcement is the barrier's only arrival
       auto open = [&](uint32_t bytes, bool last) -> uint32_t {
-        ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u, p.polls);
+        ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
         ok = __all_sync(0xffffffffu, ok);
         if (ok && warp == 0 && lane == 0) {
           c.last[s] = last ? 1 : 0;
-          if (rank == 0 && !hold) mbar_expect_tx(smem_u32(&c.full[s]), bytes * kSide);
-          hold = false;
+          if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), bytes * kSide);
         }
         return base + s * p.stage_bytes;
       };
@@ -267,11 +266,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         for (int q = 0; q < whole; q += kSub) {  // one lane of each warp; the others only keep count
           const int subs = min(kSub, whole - q);
           if (lane == 0 && ok) {
-            ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u, p.polls);
+            ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
             if (ok) {
-              if (warp == 0 && rank == 0 && !hold) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
-              hold = false;
-              const uint32_t fb = bar();
+              if (warp == 0 && rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
+                  const uint32_t fb = bar();
               for (int h = 0; h < subs; ++h)
                 for (int u = warp; u < 2 + nb; u += kProducers)
                   load_2d<PAIR>(base + s * p.stage_bytes + h * p.sub_bytes + u * kBox, u < 2 ? &maps.a : &maps.b, column(u),
@@ -376,9 +374,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           for (int q = q0; q < q1 && ahead < p.stages; q += kSub, ++ahead) {
             const int subs = min(kSub, q1 - q);
             if (lane == 0) {
-              if (warp == 0 && rank == 0 && !hold) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
-              hold = false;
-              for (int h = 0; h < subs; ++h) fill(q, h, true, false, bar());
+              if (warp == 0 && rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
+                  for (int h = 0; h < subs; ++h) fill(q, h, true, false, bar());
             }
             close();
           }
@@ -390,13 +387,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           const int subs = min(kSub, q1 - q);
           const bool fresh = ahead-- <= 0;
           if (lane == 0 && ok) {
-            if (fresh) ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u, p.polls);
+            if (fresh) ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
             if (ok) {
               if (warp == 0 && fresh) {
                 if (MODE == kMmaAdapted) c.last[s] = q + subs == q1 && adapter < 0 ? 1 : 0;
-                if (rank == 0 && !hold) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
-                hold = false;
-              }
+                if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
+                    }
               for (int h = 0; h < subs; ++h) fill(q, h, fresh, true, bar());
             }
           }
@@ -426,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
     // after a failure nothing consumes the stages any more: wait for the copies in flight
     if (*failed) {
       for (int q = 0; q < p.stages; ++q) {
-        mbar_drain(smem_u32(&c.full[s]), phase ^ 1u, drain_polls);
+        mbar_drain(smem_u32(&c.full[s]), phase ^ 1u, max(p.polls >> 4, 64u));
         if (++s == p.stages) {
           s = 0;
           phase ^= 1u;
@@ -445,14 +441,14 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         if (t.k == 0) continue;  // an empty group's gradient: the epilogue writes zeros
         const uint32_t idesc = instruction(p.bf16, kARows, kBRows, 128 * kSide, columns(t.n));
         const uint32_t acc = tmem + (it & 1) * p.tile_n;
-        ok = mbar_wait(smem_u32(&c.acc_empty[it & 1]), ((it >> 1) & 1) ^ 1u, failed, p.err, 2u, p.polls);
+        ok = mbar_wait(smem_u32(&c.acc_empty[it & 1]), ((it >> 1) & 1) ^ 1u, failed, p.err, 2u);
         fence_after();
         const int slices = (t.k + kDeep - 1) / kDeep;
         const int n = SPLIT ? slices * (part + 1) / parts - slices * part / parts : slices;
         const int paired = kDw ? t.k / kDeep : n;  // slices that come kSub to a stage
         bool last = false;
         for (int q = 0; ok && !last;) {
-          ok = mbar_wait(smem_u32(&c.full[s]), phase, failed, p.err, 4u, p.polls);
+          ok = mbar_wait(smem_u32(&c.full[s]), phase, failed, p.err, 4u);
           if (!ok) break;
           fence_after();
           // slices that come kSub to a stage; part slices and adapters' come alone.  (A rows gathered one to a
@@ -476,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
       }
       if (*failed) {
         commit<PAIR>(smem_u32(&c.drain));
-        mbar_drain(smem_u32(&c.drain), 0, drain_polls);
+        mbar_drain(smem_u32(&c.drain), 0, max(p.polls >> 4, 64u));
       }
     }
     __syncwarp();
@@ -490,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
       const Tile t = tile_of(w);
       const bool zero = t.k == 0;
       if (!zero) {
-        ok = mbar_wait(smem_u32(&c.acc_full[it & 1]), (it >> 1) & 1, failed, p.err, 8u, p.polls);
+        ok = mbar_wait(smem_u32(&c.acc_full[it & 1]), (it >> 1) & 1, failed, p.err, 8u);
         ok = __all_sync(0xffffffffu, ok);
         if (MODE == kMmaGated) {  // the warps meet below: they go on together or not at all
           if ((warp - kProducers - 1) % 4 == 0 && lane == 0) c.go[set][it & 1] = ok;

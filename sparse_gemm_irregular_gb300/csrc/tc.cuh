@@ -40,15 +40,18 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 
 constexpr uint32_t kMaxPolls = 1u << 18;  // a poll that fails takes 3 us: about a second
 
-// Waits for the phase; gives up (false) after `polls` polls or when another role of the block gave
-// up, so that no wait is endless and all roles leave together.  The status word keeps `site`.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* failed, uint32_t* err, uint32_t site,
-                                          uint32_t polls) {
-  for (uint32_t i = 0; i < polls; ++i) {
+// Waits for the phase; gives up (false) after failed[1] polls (kMaxPolls at most) or when another
+// role of the block gave up (failed[0]), so that no wait is endless and all roles leave together.  Both
+// are looked at every sixteen polls only.  The status word keeps `site`.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* failed, uint32_t* err, uint32_t site) {
+  for (uint32_t i = 0; i < kMaxPolls; ++i) {
     if (mbar_try(bar, parity)) return true;
-    if ((i & 15u) == 15u && *failed) return false;
+    if ((i & 15u) == 15u) {
+      if (failed[0]) return false;
+      if (static_cast<int>(i) >= failed[1]) break;
+    }
   }
-  *failed = 1;
+  failed[0] = 1;
   set_error(err, kErrTimeout | (site << 8));
   return false;
 }
