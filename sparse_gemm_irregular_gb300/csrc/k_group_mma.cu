@@ -12,12 +12,11 @@
 //   Dw        x^T (columns of x, in order)    dy^T (columns of dy)             the group's positions
 //   Adapted   w rows, then b[i] rows          x rows, then v rows of adapter i columns of x, then rank
 //
-// Operands go to shared memory in 64-deep slices by bulk copies: 128-byte swizzled boxes.  Rows in
-// any order come by gathering copies, four rows each.  These take about 40 cycles per four rows of a
-// slice where the matrix instruction takes 8, so they serve what is bound by the weights (up to
-// mma_gathers() rows per group, straight from the routing's order) and the ends of groups; for more rows x is
-// laid out in group order first (k_spread_rows).  Measured at 65536 rows, 2048 x 2048: 2.13 ms gathering
-// throughout, 0.41 ms from ordered rows, 0.06 ms to order them.
+// Operands go to shared memory in 64-deep slices by bulk copies: 128-byte swizzled boxes.  Rows in any
+// order come by gathering copies, four rows each, about 40 cycles from one warp where the matrix instruction
+// takes 8 for them.  They serve tiles of at most 128 rows (mma_gathers(): the weights bound these, and they
+// save the launch that lays x out: product chain of 509 rows 97 -> 87 us) and the ends of groups; for more
+// rows x is laid out in group order first (65536 rows, 2048 x 2048: 1.95 ms a chain gathering throughout, 1.61 ms so).
 // A gathered row index past the matrix reads as zeros: that masks the positions behind a group's
 // end (Dw, where they are contracted, on both operands, so that a NaN there cannot leak) and, in Adapted,
 // the tokens of other adapters.
@@ -25,13 +24,24 @@
 // Thirteen warps: four producers (a warp issues its lanes' copies one after the other, so a slice's copies
 // are dealt over four), an issuer (matrix instructions, one thread), two sets of four that empty the
 // accumulators while the next tile is computed into the other half of tensor memory (the last tile's
-// emptying is not hidden: two sets halve it).  The accumulator's lanes are
-// consecutive columns of the output, so a warp's store is contiguous.  Persistent blocks; tiles of one group
-// that share its rows are neighbours.
+// emptying is not hidden: two sets halve it).  The accumulator's lanes are consecutive columns of the
+// output, so a warp's store is contiguous.  Persistent blocks.
+//
+// Pairs: tiles of 256 rows are shared by two blocks (cta_group::2): each holds half of A and half of B, so
+// an SM fetches 32 KB per slice of 512 cycles instead of 48.  Their stages hold two slices: with one, the
+// issuer's barrier round per slice took as long as the slice's instructions (368 -> 315 us below).
 //
 // Split: where there are fewer tiles than half the SMs, the blocks of a cluster share a tile's contracted
 // range, send each other their part of the sums through distributed shared memory and add them up
 // in the order of their ranks.
+//
+// Measured on GB300 (of the measured 1935 TFLOP/s and 6.69 TB/s): 65536 rows, 32 unequal groups, 2048 x 2048:
+// forward 329 us (1671 TFLOP/s, 86%; equal groups 303 us, 94%; the library's dense batched product 280 us), dx
+// 357 us (80%, 32-bit rows out), dw 333 us (85%); tensor pipe 73% busy, the rest is barrier rounds and the
+// epilogue's stores (20 us of 303).  Gated, 49152 rows, 64 groups, 2048 x 2048: 268 us (1540 TFLOP/s, 80%).
+// Adapted, 8192 rows, 4096 x 4096, rank 64: 174 us (1650 TFLOP/s, 85%).  Eight tokens, 64 experts: bound by the
+// weights, 82% of the copy rate over the whole layer; what is missing is the last wave of tiles and 4 us of set-up
+// per kernel.
 //
 // Every wait is bounded: a role that gives up sets the status word, the others see it, copies in
 // flight are drained, tensor memory is freed, the kernel returns.

@@ -19,6 +19,11 @@
 // warps up and writes its counts; k_block_offsets scans them over the blocks, k_group_scatter
 // over the experts.  Few tokens (one block's worth) finish in the first kernel.
 // Ranks and scans are integers: the result does not depend on the order of the blocks.
+//
+// Measured on GB300: 16 x 64 (32-bit logits) 7 us in one launch, latency; 16384 x 256 (32-bit, sigmoid, bias,
+// 8 groups) 27 us + 10 us for the transpose, 17 MB read at 0.6 TB/s; 65536 x 64 (bf16) 31 us + 12 us.  Both
+// are bound by instructions: 70% of the issue slots, about 1050 warp instructions per 256-expert row and
+// 1400 per four 64-expert rows.  (One warp per token: 115 and 43 us.)
 #include <algorithm>
 
 #include "groups.h"
@@ -346,7 +351,8 @@ __global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32, ONE || V > 8 
   }
 }
 
-// The same for given ids: equal ids among 32 consecutive slots are ranked by a warp match.
+// The same for given ids: equal ids among 32 consecutive slots are ranked by a warp match.  Bound by the latency of
+// its turns: 4 us for 777 ids, 10 us for 8192, one block.
 template <bool ONE>
 __global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32)
     k_count_ids(const int32_t* __restrict__ ids, int64_t slots, int per_warp, int groups, int32_t* __restrict__ position,
@@ -400,7 +406,8 @@ __global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32)
 }
 
 // counts[e * blocks + b] -> the slots of group e in the blocks before b; total[e] = all of them.
-// One block per group.
+// One block per group, consecutive threads on consecutive blocks' counts: 4 us for 512 blocks x 64 groups
+// (a warp per group over counts laid out by block: 25 us at 1024 blocks).
 __global__ void __launch_bounds__(256) k_block_offsets(int32_t* __restrict__ counts, int64_t blocks,
                                                        int32_t* __restrict__ total) {
   __shared__ int s_tmp[33];
@@ -420,7 +427,8 @@ __global__ void __launch_bounds__(256) k_block_offsets(int32_t* __restrict__ cou
 }
 
 // position: rank in the block -> position; order: its inverse; offsets.  per_block consecutive
-// slots belong to one block of the counting kernel, and to one block here.
+// slots belong to one block of the counting kernel, and to one block here.  8 us for 393216 slots: scattered
+// 4-byte stores.
 __global__ void __launch_bounds__(kWarps * 32) k_group_scatter(const int32_t* __restrict__ ids, int64_t slots,
                                                                int64_t per_block, int groups,
                                                                const int32_t* __restrict__ counts,
@@ -451,7 +459,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_group_scatter(const int32_t* __
 }
 
 // Gradient of the logits; the row's scores are computed again.  A token's chosen gradients meet its row
-// through shared memory.  Bound by instructions per row, like the choice.
+// through shared memory.  Bound by instructions per row, like the choice: 14 us for 65536 x 64 in bf16, 17 MB
+// at 1.2 TB/s, half the issue slots.
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(kWarps * 32) k_route_backward(const T* __restrict__ logits, int64_t stride,
                                                                 int64_t tokens, int experts, int pieces,
