@@ -47,6 +47,7 @@
 // flight are drained, tensor memory is freed, the kernel returns.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "group_mma.h"
 #include "tc.cuh"
@@ -64,7 +65,6 @@ constexpr int kMaxStages = 12;
 constexpr int kABytes = 128 * 128; // A's part of a stage: 128 rows of 128 bytes
 constexpr int kBox = 64 * 128;     // a 64 x 64 box
 constexpr int kTmemCols = 512;
-constexpr int kPairTile = 256;     // narrowest tile that two blocks share
 constexpr int kSplitTile = 64;     // widest tile that is split
 constexpr int kSmemMost = 227 * 1024;
 
@@ -749,35 +749,62 @@ bool launch(const MmaMaps& maps, MmaArgs a, int64_t grid, cudaStream_t s) {
 }
 
 template <int MODE>
-bool launch_whole(const MmaMaps& maps, const MmaArgs& a, cudaStream_t s) {
+bool launch_whole(const MmaMaps& maps, const MmaArgs& a, bool pair, cudaStream_t s) {
   const int64_t grid = sm_count() / 2 * 2;
-  if (a.tile_n >= kPairTile) return launch<MODE, true, false>(maps, a, grid, s);
-  return launch<MODE, false, false>(maps, a, grid, s);
+  return pair ? launch<MODE, true, false>(maps, a, grid, s) : launch<MODE, false, false>(maps, a, grid, s);
+}
+
+// Width of the N-side tile, and whether two blocks share it.
+struct Width {
+  int n;
+  bool pair;
+};
+
+// The width with the least waves x cycles of a tile.  A slice takes the longer of its instructions (two
+// cycles per column) and its bytes at 60 per cycle and SM, a tile the longer of its slices and of the
+// epilogue (12 cycles per column) plus 1000 to change over; `tiles(n)` of them on the N side.  Measured against
+// "twice the average group, pairs at 256": product chains of 12131 rows in 4 groups, 1064 x 456, 174 -> 171 us, 801 rows x 4 of 40 groups, 3864 x 384, 181 -> 163 us;
+// where there are many tiles both pick the same.
+template <typename F>
+Width pick_width(int64_t m, int m_per_block, int64_t slices, int least, F tiles) {
+  Width best{256, true};
+  double least_time = -1.0;
+  for (int n = 256; n >= least; n /= 2)
+    for (int side = n == 256 ? 2 : 1; side >= 1; --side) {
+      const double bytes = 16384.0 + n / side * 128.0;
+      const double tile = std::max(slices * std::max(2.0 * n, bytes / 60.0), 12.0 * n) + 1000.0;
+      const double all = static_cast<double>(tiles(n)) * static_cast<double>(ceil_div(m, m_per_block * side));
+      const double time = std::ceil(all / (sm_count() / side)) * tile + 12.0 * n;
+      if (least_time < 0.0 || time < least_time) {
+        least_time = time;
+        best = Width{n, side == 2};
+      }
+    }
+  return best;
+}
+
+// N-side tiles of a grouping whose groups are not known here: each group that has rows ends in a part tile
+int64_t likely_tiles(const spgemm_grouping& g, int n) {
+  const int64_t used = std::min<int64_t>(g.groups, g.slots);
+  return std::max(used, g.slots / n + used / 2);
 }
 
 // Split when the tiles (at most `tiles`) leave half the SMs idle: as many blocks per tile, up to 8, as fit at
 // two per SM, with at least two slices each.  Measured at 64 rows, 4096 x 4096, 48 adapters: 4 blocks per tile
 // 19 us, 8 blocks 13 us; with three quarters of the SMs busy (125 tiles, 16 slices) 13 us whole, 18 us split.
 template <int MODE>
-bool launch_split(const MmaMaps& maps, MmaArgs a, int64_t tiles, cudaStream_t s) {
+bool launch_split(const MmaMaps& maps, MmaArgs a, int64_t tiles, bool pair, cudaStream_t s) {
   const int slices = (a.depth + kDeep - 1) / kDeep;
   a.split = 1;
   if (tiles * 2 <= sm_count())
     while (a.split < 8 && tiles * a.split <= sm_count() && a.split * 4 <= slices && a.split * 8 <= a.tile_n) a.split *= 2;
-  if (a.split == 1 || a.tile_n > kSplitTile) return launch_whole<MODE>(maps, a, s);
+  if (a.split == 1 || a.tile_n > kSplitTile) return launch_whole<MODE>(maps, a, pair, s);
   return launch<MODE, false, true>(maps, a, tiles * a.split, s);
 }
 
 // most tiles on the N side: every group may end in a part of one
 int64_t most_tiles(const spgemm_grouping& g, int tile_n) {
   return g.slots / tile_n + std::min<int64_t>(g.groups, g.slots);
-}
-
-// N-side tile: a power of two of about twice the average group, so that most groups are one tile
-int pick_tile(int64_t slots, int64_t groups, int most) {
-  int n = 16;
-  while (n < most && n < 2 * slots / groups) n *= 2;
-  return n;
 }
 
 std::atomic<int32_t> g_hold{0}, g_polls{0};  // set by tests
@@ -806,7 +833,7 @@ void mma_debug(int32_t hold, int32_t polls) {
   g_polls.store(polls, std::memory_order_relaxed);
 }
 
-bool mma_gathers(const spgemm_grouping& g) { return pick_tile(g.slots, g.groups, 256) <= 128; }
+bool mma_gathers(const spgemm_grouping& g) { return g.slots <= 64 * static_cast<int64_t>(g.groups); }
 
 bool mma_takes(const spgemm_dense& m) { return m.dtype != SPGEMM_DTYPE_F32 && aligned(m.data, m.stride) && m.rows < (1LL << 31) && m.cols < (1LL << 31); }
 bool mma_takes(const spgemm_weights& w) {
@@ -823,7 +850,10 @@ bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool ga
   a.gather = gather;
   a.m = static_cast<int>(y.cols);
   a.depth = static_cast<int>(x.cols);
-  a.tile_n = pick_tile(g.slots, g.groups, 256);
+  // gathered rows come to blocks on their own, 128 at most
+  Width width = pick_width(a.m, gated ? 64 : 128, ceil_div(a.depth, kDeep), 16, [&](int n) { return likely_tiles(g, n); });
+  if (gather && width.n > 128) width = Width{128, false};
+  a.tile_n = width.n;
   a.box_rows = std::min(a.tile_n, 64);
   a.out = y.data;
   a.out_stride = y.stride;
@@ -831,7 +861,7 @@ bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool ga
   MmaMaps maps;
   if (!encode_weights(&maps.a, w) || !encode_rows(&maps.b, x, gather ? 1 : a.box_rows)) return false;
   maps.c = maps.d = maps.b;
-  return gated ? launch_whole<kMmaGated>(maps, a, s) : launch_whole<kMmaForward>(maps, a, s);
+  return gated ? launch_whole<kMmaGated>(maps, a, width.pair, s) : launch_whole<kMmaForward>(maps, a, width.pair, s);
 }
 
 bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_weights& w, float* dx,
@@ -841,7 +871,8 @@ bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
   a.rows = static_cast<int>(dy.rows);
   a.m = static_cast<int>(w.cols);
   a.depth = static_cast<int>(w.rows);
-  a.tile_n = pick_tile(g.slots, g.groups, 256);
+  const Width width = pick_width(a.m, 128, ceil_div(a.depth, kDeep), 16, [&](int n) { return likely_tiles(g, n); });
+  a.tile_n = width.n;
   a.box_rows = std::min(a.tile_n, 64);
   a.out = dx;
   a.out_stride = w.cols;
@@ -849,7 +880,7 @@ bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
   MmaMaps maps;
   if (!encode_weights(&maps.a, w) || !encode_rows(&maps.b, dy, a.box_rows)) return false;
   maps.c = maps.d = maps.b;
-  return launch_whole<kMmaDx>(maps, a, s);
+  return launch_whole<kMmaDx>(maps, a, width.pair, s);
 }
 
 bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_dense& x, const spgemm_weights& dw,
@@ -857,7 +888,9 @@ bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
   MmaArgs a = base_args(g, x.dtype);
   a.m = static_cast<int>(dw.cols);
   a.n = static_cast<int>(dw.rows);
-  a.tile_n = dw.rows > 128 ? 256 : dw.rows > 64 ? 128 : 64;
+  const Width width = pick_width(a.m, 128, ceil_div(ceil_div(g.slots, g.groups), kDeep), 64,
+                                 [&](int n) { return g.groups * ceil_div(dw.rows, n); });
+  a.tile_n = width.n;
   a.out = dw.data;
   a.out_stride = dw.row_stride;
   a.out_group = dw.group_stride;
@@ -866,7 +899,7 @@ bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
   if (!encode_rows(&maps.a, x, 64) || !encode_rows(&maps.b, dy, 64) || !encode_rows(&maps.c, dy, 1) ||
       !encode_rows(&maps.d, x, 1))
     return false;
-  return launch_whole<kMmaDw>(maps, a, s);
+  return launch_whole<kMmaDw>(maps, a, width.pair, s);
 }
 
 bool launch_mma_shrink(const spgemm_grouping& g, const spgemm_dense& x, const spgemm_weights& a_w, const float* scale,
@@ -888,7 +921,7 @@ bool launch_mma_shrink(const spgemm_grouping& g, const spgemm_dense& x, const sp
   a.runs = 1;
   if (!encode_weights(&maps.a, a_w) || !encode_rows(&maps.b, x, 1) || !encode_rows(&maps.c, x, a.box_rows)) return false;
   maps.d = maps.b;
-  return launch_split<kMmaForward>(maps, a, most_tiles(g, a.tile_n) * ceil_div(a.m, 128), s);
+  return launch_split<kMmaForward>(maps, a, most_tiles(g, a.tile_n) * ceil_div(a.m, 128), false, s);
 }
 
 bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spgemm_weights& b, const int32_t* ids,
@@ -901,12 +934,12 @@ bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spge
   a.early = 1;
   a.m = static_cast<int>(y.cols);
   a.depth = static_cast<int>(x.cols);
-  // the widest tile that still gives every SM one; few rows: one tile, its depth split
-  a.tile_n = 256;
-  while (a.tile_n > 16 && (x.rows * 2 <= a.tile_n ||
-                           (x.rows > kSplitTile && a.tile_n > 32 &&
-                            ceil_div(x.rows, a.tile_n) * ceil_div(y.cols, 128) < sm_count())))
-    a.tile_n /= 2;
+  Width width = pick_width(a.m, 128, ceil_div(a.depth, kDeep), 32, [&](int n) { return ceil_div(x.rows, n); });
+  if (x.rows <= kSplitTile) {  // one tile; its depth is split
+    width = Width{16, false};
+    while (width.n < x.rows) width.n *= 2;
+  }
+  a.tile_n = width.n;
   a.box_rows = std::min(a.tile_n, 64);
   a.out = y.data;
   a.out_stride = y.stride;
@@ -916,7 +949,7 @@ bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spge
   if (!encode_weights(&maps.a, shared) || !encode_rows(&maps.b, x, a.box_rows) || !encode_weights(&maps.c, b) ||
       !encode_rows(&maps.d, v, 1))
     return false;
-  return launch_split<kMmaAdapted>(maps, a, ceil_div(x.rows, a.tile_n) * ceil_div(a.m, 128), s);
+  return launch_split<kMmaAdapted>(maps, a, ceil_div(x.rows, a.tile_n) * ceil_div(a.m, 128), width.pair, s);
 }
 
 }  // namespace sg
