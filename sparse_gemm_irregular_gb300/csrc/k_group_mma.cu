@@ -754,30 +754,46 @@ bool launch_whole(const MmaMaps& maps, const MmaArgs& a, bool pair, cudaStream_t
   return pair ? launch<MODE, true, false>(maps, a, grid, s) : launch<MODE, false, false>(maps, a, grid, s);
 }
 
-// Width of the N-side tile, and whether two blocks share it.
+// Width of the N-side tile, whether two blocks share it, and how many share its depth.
 struct Width {
   int n;
   bool pair;
+  int split;
 };
+
+// The most blocks (up to 8) that may share a tile's depth: only where the tiles (at most `tiles`) leave half
+// the SMs idle, as many as fit at two per SM, with at least two slices each.
+int most_split(int n, int64_t tiles, int64_t slices) {
+  int split = 1;
+  if (n <= kSplitTile && tiles * 2 <= sm_count())
+    while (split < 8 && tiles * split <= sm_count() && split * 4 <= slices && split * 8 <= n) split *= 2;
+  return split;
+}
 
 // The width with the least waves x cycles of a tile.  A slice takes the longer of its instructions (two
 // cycles per column) and its bytes at 60 per cycle and SM, a tile the longer of its slices and of the
-// epilogue (12 cycles per column) plus 1000 to change over; `tiles(n)` of them on the N side.  Measured against
-// "twice the average group, pairs at 256": product chains of 12131 rows in 4 groups, 1064 x 456, 174 -> 171 us, 801 rows x 4 of 40 groups, 3864 x 384, 181 -> 163 us;
-// where there are many tiles both pick the same.
+// epilogue (12 cycles per column) plus 1000 to change over, or 8000 for the meeting of a split tile's blocks;
+// `tiles(n)` of them on the N side.
+// Measured against "twice the average group, pairs at 256": product chain of 801 rows x 4 of 40 groups,
+// 3864 x 384, 181 -> 163 us; adapters of 387 rows, 2192 x 5592, 88 -> 55 us; where there are many tiles
+// both pick the same.
 template <typename F>
-Width pick_width(int64_t m, int m_per_block, int64_t slices, int least, F tiles) {
-  Width best{256, true};
+Width pick_width(int64_t m, int m_per_block, int64_t slices, int least, bool splits, F tiles) {
+  Width best{256, true, 1};
   double least_time = -1.0;
   for (int n = 256; n >= least; n /= 2)
     for (int side = n == 256 ? 2 : 1; side >= 1; --side) {
-      const double bytes = 16384.0 + n / side * 128.0;
-      const double tile = std::max(slices * std::max(2.0 * n, bytes / 60.0), 12.0 * n) + 1000.0;
-      const double all = static_cast<double>(tiles(n)) * static_cast<double>(ceil_div(m, m_per_block * side));
-      const double time = std::ceil(all / (sm_count() / side)) * tile + 12.0 * n;
+      const int64_t all = tiles(n) * ceil_div(m, m_per_block * side);
+      const int split = splits && side == 1 ? most_split(n, all, slices) : 1;
+      const double slice = std::max(2.0 * n, (16384.0 + n / side * 128.0) / 60.0);
+      const double crowd = all * split > sm_count() ? 1.5 : 1.0;  // two blocks of a split tile on one SM
+      const double tile = split > 1 ? ceil_div(slices, split) * slice * crowd + 8000.0
+                                    : std::max(slices * slice, 12.0 * n) + 1000.0;
+      const double waves = split > 1 ? 1.0 : std::ceil(static_cast<double>(all) / (sm_count() / side));
+      const double time = waves * tile + 12.0 * n;
       if (least_time < 0.0 || time < least_time) {
         least_time = time;
-        best = Width{n, side == 2};
+        best = Width{n, side == 2, split};
       }
     }
   return best;
@@ -789,16 +805,12 @@ int64_t likely_tiles(const spgemm_grouping& g, int n) {
   return std::max(used, g.slots / n + used / 2);
 }
 
-// Split when the tiles (at most `tiles`) leave half the SMs idle: as many blocks per tile, up to 8, as fit at
-// two per SM, with at least two slices each.  Measured at 64 rows, 4096 x 4096, 48 adapters: 4 blocks per tile
-// 19 us, 8 blocks 13 us; with three quarters of the SMs busy (125 tiles, 16 slices) 13 us whole, 18 us split.
+// Measured at 64 rows, 4096 x 4096, 48 adapters: 4 blocks per tile 19 us, 8 blocks 13 us; with three quarters of
+// the SMs busy (125 tiles, 16 slices) 13 us whole, 18 us split.
 template <int MODE>
-bool launch_split(const MmaMaps& maps, MmaArgs a, int64_t tiles, bool pair, cudaStream_t s) {
-  const int slices = (a.depth + kDeep - 1) / kDeep;
-  a.split = 1;
-  if (tiles * 2 <= sm_count())
-    while (a.split < 8 && tiles * a.split <= sm_count() && a.split * 4 <= slices && a.split * 8 <= a.tile_n) a.split *= 2;
-  if (a.split == 1 || a.tile_n > kSplitTile) return launch_whole<MODE>(maps, a, pair, s);
+bool launch_split(const MmaMaps& maps, MmaArgs a, const Width& width, int64_t tiles, cudaStream_t s) {
+  if (width.split == 1) return launch_whole<MODE>(maps, a, width.pair, s);
+  a.split = width.split;
   return launch<MODE, false, true>(maps, a, tiles * a.split, s);
 }
 
@@ -851,8 +863,8 @@ bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool ga
   a.m = static_cast<int>(y.cols);
   a.depth = static_cast<int>(x.cols);
   // gathered rows come to blocks on their own, 128 at most
-  Width width = pick_width(a.m, gated ? 64 : 128, ceil_div(a.depth, kDeep), 16, [&](int n) { return likely_tiles(g, n); });
-  if (gather && width.n > 128) width = Width{128, false};
+  Width width = pick_width(a.m, gated ? 64 : 128, ceil_div(a.depth, kDeep), 16, false, [&](int n) { return likely_tiles(g, n); });
+  if (gather && width.n > 128) width = Width{128, false, 1};
   a.tile_n = width.n;
   a.box_rows = std::min(a.tile_n, 64);
   a.out = y.data;
@@ -871,7 +883,7 @@ bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
   a.rows = static_cast<int>(dy.rows);
   a.m = static_cast<int>(w.cols);
   a.depth = static_cast<int>(w.rows);
-  const Width width = pick_width(a.m, 128, ceil_div(a.depth, kDeep), 16, [&](int n) { return likely_tiles(g, n); });
+  const Width width = pick_width(a.m, 128, ceil_div(a.depth, kDeep), 16, false, [&](int n) { return likely_tiles(g, n); });
   a.tile_n = width.n;
   a.box_rows = std::min(a.tile_n, 64);
   a.out = dx;
@@ -888,7 +900,7 @@ bool launch_mma_dw(const spgemm_grouping& g, const spgemm_dense& dy, const spgem
   MmaArgs a = base_args(g, x.dtype);
   a.m = static_cast<int>(dw.cols);
   a.n = static_cast<int>(dw.rows);
-  const Width width = pick_width(a.m, 128, ceil_div(ceil_div(g.slots, g.groups), kDeep), 64,
+  const Width width = pick_width(a.m, 128, ceil_div(ceil_div(g.slots, g.groups), kDeep), 64, false,
                                  [&](int n) { return g.groups * ceil_div(dw.rows, n); });
   a.tile_n = width.n;
   a.out = dw.data;
@@ -912,6 +924,8 @@ bool launch_mma_shrink(const spgemm_grouping& g, const spgemm_dense& x, const sp
   // the widest tile that still gives every SM one: x is read once either way, a's rows once per tile
   a.tile_n = 32;
   while (a.tile_n < 128 && g.slots > static_cast<int64_t>(a.tile_n) * sm_count()) a.tile_n *= 2;
+  const int64_t tiles = most_tiles(g, a.tile_n) * ceil_div(a.m, 128);
+  const Width width{a.tile_n, false, most_split(a.tile_n, tiles, ceil_div(a.depth, kDeep))};
   a.box_rows = 32;
   a.out = v.data;
   a.out_stride = v.stride;
@@ -921,7 +935,7 @@ bool launch_mma_shrink(const spgemm_grouping& g, const spgemm_dense& x, const sp
   a.runs = 1;
   if (!encode_weights(&maps.a, a_w) || !encode_rows(&maps.b, x, 1) || !encode_rows(&maps.c, x, a.box_rows)) return false;
   maps.d = maps.b;
-  return launch_split<kMmaForward>(maps, a, most_tiles(g, a.tile_n) * ceil_div(a.m, 128), false, s);
+  return launch_split<kMmaForward>(maps, a, width, tiles, s);
 }
 
 bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spgemm_weights& b, const int32_t* ids,
@@ -934,11 +948,8 @@ bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spge
   a.early = 1;
   a.m = static_cast<int>(y.cols);
   a.depth = static_cast<int>(x.cols);
-  Width width = pick_width(a.m, 128, ceil_div(a.depth, kDeep), 32, [&](int n) { return ceil_div(x.rows, n); });
-  if (x.rows <= kSplitTile) {  // one tile; its depth is split
-    width = Width{16, false};
-    while (width.n < x.rows) width.n *= 2;
-  }
+  const Width width =
+      pick_width(a.m, 128, ceil_div(a.depth, kDeep), 16, true, [&](int n) { return ceil_div(x.rows, n); });
   a.tile_n = width.n;
   a.box_rows = std::min(a.tile_n, 64);
   a.out = y.data;
@@ -949,7 +960,7 @@ bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spge
   if (!encode_weights(&maps.a, shared) || !encode_rows(&maps.b, x, a.box_rows) || !encode_weights(&maps.c, b) ||
       !encode_rows(&maps.d, v, 1))
     return false;
-  return launch_split<kMmaAdapted>(maps, a, ceil_div(x.rows, a.tile_n) * ceil_div(a.m, 128), width.pair, s);
+  return launch_split<kMmaAdapted>(maps, a, width, ceil_div(x.rows, a.tile_n) * ceil_div(a.m, 128), s);
 }
 
 }  // namespace sg
