@@ -28,8 +28,8 @@
 // output, so a warp's store is contiguous.  Persistent blocks.
 //
 // Pairs: tiles of 256 rows are shared by two blocks (cta_group::2): each holds half of A and half of B, so
-// an SM fetches 32 KB per slice of 512 cycles instead of 48.  Their stages hold two slices: with one, the
-// issuer's barrier round per slice took as long as the slice's instructions (368 -> 315 us below).
+// an SM fetches 32 KB per slice of 512 cycles instead of 48.  A stage holds two slices: with one, the issuer's
+// barrier round per slice (about 450 cycles) took as long as the slice's instructions (368 -> 315 us below).
 //
 // Split: where there are fewer tiles than half the SMs, the blocks of a cluster share a tile's contracted
 // range, send each other their part of the sums through distributed shared memory and add them up
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
   const int part = SPLIT ? static_cast<int>(cluster_rank()) : 0, parts = SPLIT ? p.split : 1;  // of the contracted range
   const uint32_t tmem_cols = SPLIT ? kSplitTile : kTmemCols;
   constexpr int kSide = PAIR ? 2 : 1;
-  constexpr int kSub = PAIR ? 2 : 1;  // slices of a stage
+  constexpr int kSub = SPLIT ? 1 : 2;  // slices of a stage
   constexpr bool kDw = MODE == kMmaDw;
   volatile int* failed = c.failed;
 
@@ -245,18 +245,26 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         }
         mine = make_int4(r[0], r[1], r[2], r[3]);
       }
-      // one slice: waits for a free stage and announces its bytes; returns the stage's address.  A copy of
-      // another warp may be done before the bytes are announced: the announcement is the barrier's only arrival
+      auto bar = [&]() { return PAIR ? map_rank(smem_u32(&c.full[s]), 0) : smem_u32(&c.full[s]); };
+      // The first warp announces a stage's bytes, the barrier's only arrival (a copy of another warp may be done
+      // before).  `units`: copies of the stage that are dealt over the warps.  A warp without one still takes
+      // part, by a few bytes that it takes off itself: otherwise it could fall two rounds behind the others, and
+      // a barrier's parity cannot tell two rounds from none.
+      auto announce = [&](uint32_t bytes, int units) {
+        const uint32_t idle = static_cast<uint32_t>(max(kProducers - units, 0)) * 16u;
+        if (warp == 0 && rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), (bytes + idle) * kSide);
+        if (warp >= units) mbar_complete_tx(bar(), 16u);
+      };
+      // one stage: waits until it is free and announces its bytes; returns its address
       auto open = [&](uint32_t bytes, bool last) -> uint32_t {
         ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
         ok = __all_sync(0xffffffffu, ok);
-        if (ok && warp == 0 && lane == 0) {
-          c.last[s] = last ? 1 : 0;
-          if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), bytes * kSide);
+        if (ok && lane == 0) {
+          if (warp == 0) c.last[s] = last ? 1 : 0;
+          announce(bytes, kProducers);
         }
         return base + s * p.stage_bytes;
       };
-      auto bar = [&]() { return PAIR ? map_rank(smem_u32(&c.full[s]), 0) : smem_u32(&c.full[s]); };
       auto close = [&]() {
         if (++s == p.stages) {
           s = 0;
@@ -278,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           if (lane == 0 && ok) {
             ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
             if (ok) {
-              if (warp == 0 && rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
-                  const uint32_t fb = bar();
+              announce(subs * bytes, 2 + nb);
+              const uint32_t fb = bar();
               for (int h = 0; h < subs; ++h)
                 for (int u = warp; u < 2 + nb; u += kProducers)
                   load_2d<PAIR>(base + s * p.stage_bytes + h * p.sub_bytes + u * kBox, u < 2 ? &maps.a : &maps.b, column(u),
@@ -360,12 +368,16 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
       const int box = lane == 31 ? warp : 2;
       if (!boxed) {
         wait_before();
-        for (int q = q0; q < q1 && ok; ++q) {
-          const uint32_t a = open(bytes, q + 1 == q1);
+        for (int q = q0; q < q1 && ok; q += kSub) {
+          const int subs = min(kSub, q1 - q);
+          const uint32_t stage = open(subs * bytes, q + subs == q1);
           if (!ok) break;
           const uint32_t fb = bar();
-          if (box < boxes_a) copy_a(a, box, q * kDeep, fb);
-          if (quad * 4 < half) load_rows4<PAIR>(a + kABytes + quad * 512, &maps.b, q * kDeep, mine, fb);
+          for (int h = 0; h < subs; ++h) {
+            const uint32_t a = stage + h * p.sub_bytes;
+            if (box < boxes_a) copy_a(a, box, (q + h) * kDeep, fb);
+            if (quad * 4 < half) load_rows4<PAIR>(a + kABytes + quad * 512, &maps.b, (q + h) * kDeep, mine, fb);
+          }
           close();
         }
       } else {
@@ -384,8 +396,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           for (int q = q0; q < q1 && ahead < p.stages; q += kSub, ++ahead) {
             const int subs = min(kSub, q1 - q);
             if (lane == 0) {
-              if (warp == 0 && rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
-                  for (int h = 0; h < subs; ++h) fill(q, h, true, false, bar());
+              announce(subs * bytes, boxes_a + boxes);
+              for (int h = 0; h < subs; ++h) fill(q, h, true, false, bar());
             }
             close();
           }
@@ -399,10 +411,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           if (lane == 0 && ok) {
             if (fresh) ok = mbar_wait(smem_u32(&c.empty[s]), phase ^ 1u, failed, p.err, 1u);
             if (ok) {
-              if (warp == 0 && fresh) {
-                if (MODE == kMmaAdapted) c.last[s] = q + subs == q1 && adapter < 0 ? 1 : 0;
-                if (rank == 0) mbar_expect_tx(smem_u32(&c.full[s]), subs * bytes * kSide);
-                    }
+              if (fresh) {
+                if (MODE == kMmaAdapted && warp == 0) c.last[s] = q + subs == q1 && adapter < 0 ? 1 : 0;
+                announce(subs * bytes, boxes_a + boxes);
+              }
               for (int h = 0; h < subs; ++h) fill(q, h, fresh, true, bar());
             }
           }
@@ -461,8 +473,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           ok = mbar_wait(smem_u32(&c.full[s]), phase, failed, p.err, 4u);
           if (!ok) break;
           fence_after();
-          // slices that come kSub to a stage; part slices and adapters' come alone.  (A rows gathered one to a
-          // stage only in kernels with kSub = 1.)
+          // part slices of a group and adapters' come alone
           const int subs = q < paired ? min(kSub, paired - q) : 1;
           for (int h = 0; h < subs; ++h) {
             const uint32_t a = base + s * p.stage_bytes + h * p.sub_bytes;
@@ -722,7 +733,7 @@ int sm_count() {
 template <int MODE, bool PAIR, bool SPLIT>
 bool launch(const MmaMaps& maps, MmaArgs a, int64_t grid, cudaStream_t s) {
   a.sub_bytes = kABytes + std::max(a.tile_n / (PAIR ? 2 : 1), MODE == kMmaDw ? 64 : 16) * 128;
-  a.stage_bytes = a.sub_bytes * (PAIR ? 2 : 1);
+  a.stage_bytes = a.sub_bytes * (SPLIT ? 1 : 2);
   const int control = static_cast<int>(sizeof(Control) + (MODE == kMmaGated ? sizeof(Swap) : 0));
   // split: two blocks per SM, and the stages hold the sums that meet there
   const int most = SPLIT ? kSmemMost / 2 - 1024 : kSmemMost;

@@ -375,6 +375,28 @@ def test_experts(gpu_lib, tokens, groups, top_k, d, hidden, n, dtype):
     gpu_lib.grouped_status()
 
 
+@pytest.mark.parametrize("tokens,groups,top_k,d,hidden", [(1594, 65, 4, 448, 504), (700, 30, 3, 192, 72), (2500, 9, 2, 1000, 136)])
+def test_no_wait_runs_out_over_many_calls(gpu_lib, tokens, groups, top_k, d, hidden):
+    """Groups of very different sizes, so that a slice is dealt over fewer copies than there are warps to
+    issue them, call after call without a pause: every call gives the first one's bits and no wait expires."""
+    import torch
+    ids = _random_ids(tokens, tokens, groups, top_k)
+    weights = np.random.default_rng(1).random(ids.shape).astype(np.float32)
+    r = _routing(gpu_lib, ids, groups, weights)
+    x = _normal(1, tokens, d).cuda()
+    up, down = _normal(2, groups, 2 * hidden, d, std=d ** -0.5).cuda(), _normal(3, groups, d, hidden, std=hidden ** -0.5).cuda()
+    dy = _normal(4, ids.size, 2 * hidden).cuda()
+    first = gpu_lib.experts(x, up, down, r)
+    dx, dw = gpu_lib.expert_product_backward(dy, x, up, r)
+    for _ in range(40):
+        out = gpu_lib.experts(x, up, down, r)
+        again = gpu_lib.expert_product_backward(dy, x, up, r)
+        assert torch.equal(out, first) and torch.equal(again[0], dx) and torch.equal(again[1], dw)
+    outs = [gpu_lib.experts(x, up, down, r) for _ in range(20)]
+    assert all(torch.equal(o, first) for o in outs)
+    gpu_lib.grouped_status()
+
+
 # ---- adapters ------------------------------------------------------------------------------------
 @pytest.mark.parametrize("tokens,adapters,rank,d,n", [
     (1, 1, 8, 64, 64), (1, 3, 16, 128, 72), (5, 2, 8, 40, 136), (64, 48, 16, 256, 264), (300, 3, 64, 512, 128),
