@@ -284,13 +284,15 @@ __global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32, ONE || V > 8 
         }
       }
     }
+    float over = 1.0f;  // a division per chosen expert: a single one has the weight 1 exactly
     if (r.renormalise) {
       float sum = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if ((chosen >> v) & 1u) sum += s[v];
       sum = lanes_sum<L>(sum);
-      f = sum > 0.0f ? 1.0f / sum : 0.0f;  // the row's own factor cancels
+      f = sum > 0.0f ? 1.0f : 0.0f;  // the row's own factor cancels
+      over = sum > 0.0f ? sum : 1.0f;
     }
     f *= r.scale;
     int before = __popc(chosen);  // chosen experts of the lower lanes
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__((ONE ? kWarpsOne : kWarps) * 32, ONE || V > 8 
           for (int i = 0; i < V; ++i) w = i == v ? s[i] : w;
           const int rank = cnt[e0 + v]++;
           ids[o] = e0 + v;
-          weights[o] = w * f;
+          weights[o] = w / over * f;
           position[o] = rank;
         }
       if (kPer > 1) __syncwarp();
@@ -497,22 +499,22 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_backward(const T* __restr
 #pragma unroll
     for (int v = 0; v < V; ++v) d[v] = full[e0 + v];
     if (r.renormalise) {  // w = s / sum: ds = (dw - sum of dw * w) / sum, over the chosen ones
-      float sum = 0.0f, dot = 0.0f;
+      float sum = 0.0f, mean = 0.0f;
       for (int j = 0; j < r.top_k; ++j) {
         const int e = there ? ids[t * r.top_k + j] : -1;
         if (e >= e0 && e < e0 + V && e < experts) chosen |= 1u << (e - e0);
       }
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if ((chosen >> v) & 1u) {
-          sum += s[v];
-          dot += d[v] * s[v];
-        }
+        if ((chosen >> v) & 1u) sum += s[v];
       sum = lanes_sum<L>(sum);
-      dot = lanes_sum<L>(dot);
-      const float mean = sum > 0.0f ? dot / sum : 0.0f;
+      // each weight by division, so that a single choice (weight exactly 1) has the gradient 0 exactly
 #pragma unroll
-      for (int v = 0; v < V; ++v) d[v] = (chosen >> v) & 1u && sum > 0.0f ? (d[v] - mean) / sum : 0.0f;
+      for (int v = 0; v < V; ++v)
+        if (((chosen >> v) & 1u) && sum > 0.0f) mean += d[v] * (s[v] / sum);
+      mean = lanes_sum<L>(mean);
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] = ((chosen >> v) & 1u) && sum > 0.0f ? (d[v] - mean) / sum : 0.0f;
     }
     float dot = 0.0f;
     if (r.score == SPGEMM_SCORE_SOFTMAX) {

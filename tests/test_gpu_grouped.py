@@ -170,6 +170,17 @@ def test_route_gradient_against_differences(gpu_lib):
                 assert np.allclose(d[:, e], (vals[0] - vals[1]) / (2 * h), atol=2e-5, rtol=0)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_a_single_renormalised_choice_has_no_gradient(gpu_lib, score, dtype):
+    """Its weight is 1 whatever the logits: the gradient is 0, not a rounding error."""
+    import torch
+    l = _normal(4, 777, 53, dtype=dtype).cuda()
+    r = gpu_lib.route(l, 1, score=score, scale=2.5)
+    assert torch.all(r.weights == 2.5)
+    assert torch.all(gpu_lib.route_backward(l, r, torch.randn(777, 1, device="cuda")) == 0)
+
+
 def test_route_empty_batch(gpu_lib):
     import torch
     r = gpu_lib.route(torch.empty(0, 16, device="cuda"), 2)
