@@ -15,7 +15,7 @@
 // Operands go to shared memory in 64-deep slices by bulk copies: 128-byte swizzled boxes.  Rows in any
 // order come by gathering copies, four rows each, about 40 cycles from one warp where the matrix instruction
 // takes 8 for them.  They serve tiles of at most 128 rows (mma_gathers(): the weights bound these, and they
-// save the launch that lays x out: product chain of 509 rows 97 -> 87 us) and the ends of groups; for more
+// save the launch that lays x out: product chain of 509 rows 97 -> 81 us) and the ends of groups; for more
 // rows x is laid out in group order first (65536 rows, 2048 x 2048: 1.95 ms a chain gathering throughout, 1.61 ms so).
 // A gathered row index past the matrix reads as zeros: that masks the positions behind a group's
 // end (Dw, where they are contracted, on both operands, so that a NaN there cannot leak) and, in Adapted,
@@ -36,12 +36,11 @@
 // in the order of their ranks.
 //
 // Measured on GB300 (of the measured 1935 TFLOP/s and 6.69 TB/s): 65536 rows, 32 unequal groups, 2048 x 2048:
-// forward 329 us (1671 TFLOP/s, 86%; equal groups 303 us, 94%; the library's dense batched product 280 us), dx
-// 357 us (80%, 32-bit rows out), dw 333 us (85%); tensor pipe 73% busy, the rest is barrier rounds and the
-// epilogue's stores (20 us of 303).  Gated, 49152 rows, 64 groups, 2048 x 2048: 268 us (1540 TFLOP/s, 80%).
-// Adapted, 8192 rows, 4096 x 4096, rank 64: 174 us (1650 TFLOP/s, 85%).  Eight tokens, 64 experts: bound by the
-// weights, 82% of the copy rate over the whole layer; what is missing is the last wave of tiles and 4 us of set-up
-// per kernel.
+// forward 315 us (1745 TFLOP/s, 90%; equal groups 303 us, the library's dense batched product 280 us), dx 344 us
+// (83%, 32-bit rows out), dw 336 us (85%); tensor pipe 73% busy, the rest is barrier rounds and the epilogue's
+// stores (20 us of 303).  Gated, 49152 rows, 64 groups, 2048 x 2048: 267 us (1540 TFLOP/s, 80%).  Adapted, 8192
+// rows, 4096 x 4096, rank 64: 165 us (1760 TFLOP/s, 91%).  A layer of eight tokens and 64 experts reads its
+// weights at 90% of the copy rate: 67 us; what is missing is the last wave of tiles and the first one's set-up.
 //
 // Every wait is bounded: a role that gives up sets the status word, the others see it, copies in
 // flight are drained, tensor memory is freed, the kernel returns.
