@@ -739,9 +739,14 @@ bool launch(const MmaMaps& maps, MmaArgs a, int64_t grid, cudaStream_t s) {
   a.stages = std::min<int>(kMaxStages, (most - 1024 - control) / a.stage_bytes);
   const int smem = 1024 + a.stages * a.stage_bytes + control;
   auto kern = k_group_mma<MODE, PAIR, SPLIT>;
-  static const cudaError_t raised =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
-  if (raised != cudaSuccess) return false;
+  static std::atomic<uint64_t> raised{0};  // devices on which the kernel may use this much shared memory
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(raised.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess) return false;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);

@@ -21,7 +21,7 @@
 // Ranks and scans are integers: the result does not depend on the order of the blocks.
 //
 // Measured on GB300: 16 x 64 (32-bit logits) 7 us in one launch, latency; 16384 x 256 (32-bit, sigmoid, bias,
-// 8 groups) 27 us + 10 us for the transpose, 17 MB read at 0.6 TB/s; 65536 x 64 (bf16) 31 us + 12 us.  Both
+// 8 groups) 34 us + 12 us for the transpose, 17 MB read at 0.5 TB/s; 65536 x 64 (bf16) 29 us + 13 us.  Both
 // are bound by instructions: 70% of the issue slots, about 1050 warp instructions per 256-expert row and
 // 1400 per four 64-expert rows.  (One warp per token: 115 and 43 us.)
 #include <algorithm>

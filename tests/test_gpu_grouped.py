@@ -300,6 +300,30 @@ def test_product_strides_and_streams(gpu_lib):
         assert np.all(np.abs(_np(y) - want) <= rounding("bf16", want) + SUM * 128 * mag)
 
 
+def test_outputs_past_32_bit_offsets(gpu_lib):
+    """More than 2^31 elements in y: rows at the start, around the boundary and at the end."""
+    import torch
+    tokens, k, d, n, groups = 270_000, 4, 64, 2048, 9
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.rand(tokens, groups, device="cuda", generator=g).topk(k, 1).indices.sort(1).values.int()
+    r = gpu_lib.group_rows(ids, groups)
+    x = torch.randn(tokens, d, device="cuda", generator=g).bfloat16()
+    w = torch.randn(groups, n, d, device="cuda", generator=g).bfloat16()
+    y = gpu_lib.expert_product(x, w, r)
+    assert y.numel() > 1 << 31
+    edge = (1 << 31) // n
+    at = torch.tensor([0, 1, edge - 1, edge, edge + 1, tokens * k - 2, tokens * k - 1], device="cuda")
+    slot = r.order[at].long()
+    xr, wr = x[slot // k].double(), w[ids.reshape(-1)[slot].long()].double()
+    want = torch.einsum("pd,pnd->pn", xr, wr)
+    mag = torch.einsum("pd,pnd->pn", xr.abs(), wr.abs())
+    assert ((y[at].double() - want).abs() <= U["bf16"] * want.abs() + SUM * d * mag).all()
+    out = gpu_lib.combine(y, r)
+    last = y[r.position[tokens - 1].long()].double()
+    assert ((out[tokens - 1].double() - last.sum(0)).abs() <= U["bf16"] * last.sum(0).abs() + SUM * k * last.abs().sum(0)).all()
+    gpu_lib.grouped_status()
+
+
 def test_masked_values_stay_in_their_rows(gpu_lib):
     """A NaN or infinite row of x reaches only its own slots, in every product."""
     import torch

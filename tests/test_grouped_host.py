@@ -101,6 +101,12 @@ def test_group_rows_refuses():
     assert lib.spgemm_group_rows(16, 1 << 31, 4, 16, 16, 16, None) == -5
 
 
+def test_debug_refuses_negative_polls():
+    lib = sg.load()
+    assert lib.spgemm_grouped_debug(0, -1) == -1
+    assert lib.spgemm_grouped_debug(0, 0) == 0
+
+
 def test_products_refuse():
     lib = sg.load()
     g, x, w, y = grouping(8, 2, 3), dense(4, 16), weights(3, 24, 16), dense(8, 24)
