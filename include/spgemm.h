@@ -438,7 +438,10 @@ int spgemm_group_rows(const int32_t* ids, int64_t slots, int32_t groups, int32_t
  * (row(p) = x[order[p] / top_k]) or, when x_grouped, one row per position (row(p) = x[p]); w[g] is
  * y.cols x x.cols.  Rows of y from offsets[groups] on are set to zero.  y may be 32-bit (sums are
  * held in 32 bits in any case).  All types equal otherwise; 16-bit types whose rows start on 16-byte
- * boundaries run on the tensor cores, anything else on the CUDA cores. */
+ * boundaries run on the tensor cores, anything else on the CUDA cores.  16-bit rows of y are the same on both:
+ * the 32-bit sum in the order of the columns, one fused multiply-add each, rounded once (sums so close to a rounding
+ * boundary that the tensor cores' order could round them another way are added up again).  32-bit rows of y are the
+ * sums as each path forms them. */
 int spgemm_grouped_product(const spgemm_grouping* g, const spgemm_dense* x, int32_t x_grouped,
                            const spgemm_weights* w, const spgemm_dense* y, void* stream);
 

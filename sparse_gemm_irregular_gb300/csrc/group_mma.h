@@ -26,6 +26,8 @@ struct MmaArgs {
   const int32_t* ids;      // Adapted: the adapter of each row
   int adapters, rank;
   int split;               // blocks that share a tile's contracted range
+  uint32_t* unsure;        // Forward, 16-bit rows out: where the marks go (k_group_settle.cu), or NULL
+  float near;              // sums closer than this times the largest beside them to a rounding boundary are marked
   uint32_t* err;
   uint32_t polls;          // of every wait
   int hold;                // tests: withhold an announcement
@@ -44,9 +46,18 @@ bool mma_gathers(const spgemm_grouping& g);
 // The same contracts as the launch_plain_* functions; false: the launch failed (cudaGetLastError
 // or the encoding of a copy descriptor).
 // early: x is made by the kernel launched just before on the stream, which was itself launched by launch_next or
-// by these functions and makes nothing else that is read here.
+// by these functions and makes nothing else that is read here.  unsure: mma_marks_bytes() of scratch for the marks
+// that launch_settle reads, or NULL.
 bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool gather, const spgemm_weights& w,
-                        bool gated, const spgemm_dense& y, bool early, cudaStream_t s);
+                        bool gated, const spgemm_dense& y, uint32_t* unsure, bool early, cudaStream_t s);
+
+// Rows of the N-side tiles that launch_mma_forward takes (not gated), and the bytes of its marks: a word per 32
+// rows of a tile and column of y.
+int mma_forward_tile(const spgemm_grouping& g, const spgemm_dense& x, bool gather, int64_t cols);
+int64_t mma_marks_bytes(const spgemm_grouping& g, int tile_n, int64_t cols);
+// Sums the marked elements of y again in index order (k_group_settle.cu); arguments as of launch_mma_forward.
+bool launch_settle(const spgemm_grouping& g, const spgemm_dense& x, bool gather, const spgemm_weights& w,
+                   const spgemm_dense& y, const uint32_t* unsure, int tile_n, cudaStream_t s);
 bool launch_mma_dx(const spgemm_grouping& g, const spgemm_dense& dy, const spgemm_weights& w, float* dx,
                    cudaStream_t s);
 // x with one row per position here

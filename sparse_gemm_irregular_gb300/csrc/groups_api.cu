@@ -127,22 +127,12 @@ spgemm_dense dense(void* data, int64_t rows, int64_t cols, int32_t dtype) {
 
 // x laid out in group order takes this many bytes; none where its rows are gathered or in order already
 int64_t spread_bytes(const spgemm_grouping& g, const spgemm_dense& x) { return 2 * g.slots * (ceil_div(x.cols, 8) * 8); }
-int64_t forward_bytes(const spgemm_grouping& g, const spgemm_dense& x, bool by_token) {
-  return by_token && !mma_gathers(g) ? spread_bytes(g, x) : 0;
-}
 // lays x out in group order at `to`, its rows padded to 16 bytes
 spgemm_dense spread(const spgemm_grouping& g, const spgemm_dense& x, void* to, cudaStream_t s) {
   const spgemm_dense rows{to, g.slots, x.cols, ceil_div(x.cols, 8) * 8, x.dtype, 0};
   launch_spread_rows(g, x, rows, s);
   return rows;
 }
-// y = rows * w[g]^T on the tensor cores with x by token or by position; `to`: forward_bytes
-bool mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool by_token, const spgemm_weights& w, bool gated,
-                 const spgemm_dense& y, void* to, cudaStream_t s) {
-  if (!by_token || mma_gathers(g)) return launch_mma_forward(g, x, by_token, w, gated, y, false, s);
-  return launch_mma_forward(g, spread(g, x, to, s), false, w, gated, y, true, s);
-}
-
 }  // namespace
 }  // namespace sg
 
@@ -209,9 +199,15 @@ int spgemm_grouped_product(const spgemm_grouping* g, const spgemm_dense* x, int3
     return bad("grouped product: types differ");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (mma_takes(*x) && mma_takes(*w)) {
-    Scratch scratch(st, {forward_bytes(*g, *x, !x_grouped)});
+    const bool lay = !x_grouped && !mma_gathers(*g), gather = !x_grouped && !lay, round = y->dtype != SPGEMM_DTYPE_F32;
+    const int tile_n = mma_forward_tile(*g, *x, gather, y->cols);
+    Scratch scratch(st, {lay ? spread_bytes(*g, *x) : 0, round ? mma_marks_bytes(*g, tile_n, y->cols) : 0});
     if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
-    if (!mma_forward(*g, *x, !x_grouped, *w, false, *y, scratch.part(0), st)) return launch_failed("grouped product");
+    const spgemm_dense rows = lay ? spread(*g, *x, scratch.part(0), st) : *x;
+    uint32_t* marks = scratch.part<uint32_t>(1);
+    if (!launch_mma_forward(*g, rows, gather, *w, false, *y, marks, lay, st) ||
+        (round && !launch_settle(*g, rows, gather, *w, *y, marks, tile_n, st)))
+      return launch_failed("grouped product");
   } else {
     launch_plain_forward(*g, *x, !x_grouped, *w, *y, st);
   }
@@ -290,15 +286,17 @@ int spgemm_experts(const spgemm_grouping* g, const float* weights, const spgemm_
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   spgemm_dense h = dense(nullptr, g->slots, hidden, x->dtype);
   const bool mma = mma_takes(*x) && mma_takes(*w_up) && mma_takes(h) && mma_takes(*w_down);
+  const bool lay = mma && !mma_gathers(*g);
   // the down product's rows stay in 32 bits: the weighted sum is rounded once
   Scratch scratch(st, {g->slots * hidden * dtype_size(x->dtype), 4 * g->slots * out->cols,
-                       mma ? forward_bytes(*g, *x, true) : 8 * g->slots * hidden});
+                       !mma ? 8 * g->slots * hidden : lay ? spread_bytes(*g, *x) : 0});
   if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
   h.data = scratch.part(0);
   const spgemm_dense y = dense(scratch.part(1), g->slots, out->cols, SPGEMM_DTYPE_F32);
   if (mma) {
-    if (!mma_forward(*g, *x, true, *w_up, true, h, scratch.part(2), st) ||
-        !launch_mma_forward(*g, h, false, *w_down, false, y, true, st))
+    const spgemm_dense rows = lay ? spread(*g, *x, scratch.part(2), st) : *x;
+    if (!launch_mma_forward(*g, rows, !lay, *w_up, true, h, nullptr, lay, st) ||
+        !launch_mma_forward(*g, h, false, *w_down, false, y, nullptr, true, st))
       return launch_failed("experts");
   } else {
     const spgemm_dense pre = dense(scratch.part(2), g->slots, 2 * hidden, SPGEMM_DTYPE_F32);

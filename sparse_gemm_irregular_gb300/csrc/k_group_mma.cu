@@ -84,6 +84,20 @@ struct Swap {
   float v[kSets][2][4][8][32];
 };
 
+// whether two 32-bit values round to different numbers of the type
+template <typename T>
+__device__ __forceinline__ bool rounds_apart(float a, float b);
+template <>
+__device__ __forceinline__ bool rounds_apart<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return __bfloat16_as_ushort(v.x) != __bfloat16_as_ushort(v.y);
+}
+template <>
+__device__ __forceinline__ bool rounds_apart<__half>(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return __half_as_ushort(__low2half(v)) != __half_as_ushort(__high2half(v));
+}
+
 struct Tile {
   int g;       // group
   int m0;      // first M index
@@ -560,6 +574,23 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
         } else {
           const int m = t.m0 + static_cast<int>(rank) * 128 + ml;
           const int64_t o = (kDw ? t.g * p.out_group : 0) + static_cast<int64_t>(t.j0 + j) * p.out_stride + m;
+          if (MODE == kMmaForward && p.unsure) {
+            auto mark = [&](auto type) {
+              using T = decltype(type);
+              uint32_t marks = 0;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float v = __uint_as_float(r[e]), size = fabsf(v);
+                // the largest finite sum of these 32 columns of the row
+                const uint32_t most = __reduce_max_sync(0xffffffffu, m < p.m && size < INFINITY ? __float_as_uint(size) : 0u);
+                const float near = __uint_as_float(most) * p.near;
+                if (rounds_apart<T>(v - near, v + near)) marks |= 1u << e;
+              }
+              if (m < p.m) p.unsure[(static_cast<int64_t>(w.r) * ((p.tile_n + 31) / 32) + j / 32) * p.m + m] = marks;
+            };
+            if (p.out_type == SPGEMM_DTYPE_BF16) mark(__nv_bfloat16());
+            else mark(__half());
+          }
           int token = 0;
           float f = 1.0f;
           if (MODE == kMmaForward && p.scatter) {  // rows leave in the tokens' order
@@ -868,8 +899,35 @@ bool mma_takes(const spgemm_weights& w) {
          w.rows < (1LL << 30) && w.cols < (1LL << 30);
 }
 
+namespace {
+
+// How far the tensor cores' sum of `depth` products may be from the 32-bit sum in index order, in units of the
+// largest sum of the row's 32 columns beside it: half a unit in the last place (2^-24) for each of its depth / 16
+// additions, and 16 more for the other order's own roundings.  Largest distance measured, in units of this:
+// 0.97 in 7e8 sums of normal, uniform and shifted values of 64 to 8192 terms, 1.22 where a hundredth of the features
+// is thirty times the rest; no element of these was rounded another way without being marked.  At half of this
+// 3e-8 of them were, at twice this twice as many sums are marked.
+float near_of(int64_t depth) { return static_cast<float>(depth + 256) * 0x1p-28f; }
+
+// gathered rows come to blocks on their own, 128 at most
+Width forward_width(const spgemm_grouping& g, const spgemm_dense& x, bool gather, bool gated, int64_t cols) {
+  const Width width =
+      pick_width(cols, gated ? 64 : 128, ceil_div(x.cols, kDeep), 16, false, [&](int n) { return likely_tiles(g, n); });
+  return gather && width.n > 128 ? Width{128, false, 1} : width;
+}
+
+}  // namespace
+
+int mma_forward_tile(const spgemm_grouping& g, const spgemm_dense& x, bool gather, int64_t cols) {
+  return forward_width(g, x, gather, false, cols).n;
+}
+
+int64_t mma_marks_bytes(const spgemm_grouping& g, int tile_n, int64_t cols) {
+  return 4 * most_tiles(g, tile_n) * ceil_div(tile_n, 32) * cols;
+}
+
 bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool gather, const spgemm_weights& w,
-                        bool gated, const spgemm_dense& y, bool early, cudaStream_t s) {
+                        bool gated, const spgemm_dense& y, uint32_t* unsure, bool early, cudaStream_t s) {
   if (g.slots == 0) return true;
   MmaArgs a = base_args(g, x.dtype);
   a.early = early;
@@ -877,14 +935,14 @@ bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool ga
   a.gather = gather;
   a.m = static_cast<int>(y.cols);
   a.depth = static_cast<int>(x.cols);
-  // gathered rows come to blocks on their own, 128 at most
-  Width width = pick_width(a.m, gated ? 64 : 128, ceil_div(a.depth, kDeep), 16, false, [&](int n) { return likely_tiles(g, n); });
-  if (gather && width.n > 128) width = Width{128, false, 1};
+  const Width width = forward_width(g, x, gather, gated, y.cols);
   a.tile_n = width.n;
   a.box_rows = std::min(a.tile_n, 64);
   a.out = y.data;
   a.out_stride = y.stride;
   a.out_type = y.dtype;
+  a.unsure = unsure;
+  a.near = near_of(x.cols);
   MmaMaps maps;
   if (!encode_weights(&maps.a, w) || !encode_rows(&maps.b, x, gather ? 1 : a.box_rows)) return false;
   maps.c = maps.d = maps.b;

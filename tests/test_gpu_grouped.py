@@ -264,6 +264,61 @@ def test_expert_product_and_gradients(gpu_lib, tokens, groups, top_k, d, n, dtyp
     gpu_lib.grouped_status()
 
 
+def _ordered_sums(x, w, ids, offsets, order):
+    """y in 32 bits, added in the order of the columns by fused multiply-adds (the products of 16-bit values are
+    exact in 64 bits, their sum with a 32-bit value is rounded to 64 bits 2^29 times finer than to 32)."""
+    y = np.zeros((ids.size, w.shape[1]), np.float32)
+    for g in range(w.shape[0]):
+        p = slice(offsets[g], offsets[g + 1])
+        rows = x[order[p] // ids.shape[1]]
+        for k in range(x.shape[1]):
+            y[p] = (y[p].astype(np.float64) + rows[:, k:k + 1] * w[g, None, :, k]).astype(np.float32)
+    return y
+
+
+# a few rows per group (rows gathered), many (laid out first), tiles of 256 rows shared by two blocks
+@pytest.mark.parametrize("tokens,groups,top_k,d,n", [
+    (1, 4, 2, 64, 128), (33, 64, 6, 256, 96), (300, 3, 2, 328, 72), (700, 5, 3, 500, 392), (2500, 2, 1, 264, 1200)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_16_bit_rows_are_the_ordered_sums_rounded_on_both_paths(gpu_lib, tokens, groups, top_k, d, n, dtype):
+    """The matrix instructions add in another order, but not one element may be rounded another way for it: the
+    gradient of the weights is formed from these rows in 32 bits."""
+    import torch
+    ids = _random_ids(tokens + d, tokens, groups, top_k)
+    r = _routing(gpu_lib, ids, groups)
+    offsets, order, _ = transpose(ids, groups)
+    x, w = _normal(1, tokens, d, dtype=dtype), _normal(2, groups, n, d, dtype=dtype, std=d ** -0.5)
+    want = torch.from_numpy(_ordered_sums(_np(x), _np(w), ids, offsets, order)).to(_t(dtype))
+    y = gpu_lib.expert_product(x.cuda(), w.cuda(), r)
+    assert torch.equal(y.cpu(), want)
+    off = torch.nn.functional.pad(x, (1, 0)).cuda()[:, 1:]  # rows that do not start on 16 bytes
+    assert torch.equal(gpu_lib.expert_product(off, w.cuda(), r), y)
+    rows = torch.zeros(ids.size, d, dtype=x.dtype)
+    rows[:offsets[-1]] = x[torch.tensor(order[:offsets[-1]] // ids.shape[1], dtype=torch.long)]
+    assert torch.equal(gpu_lib.expert_product(rows.cuda(), w.cuda(), r, grouped=True), y)
+    gpu_lib.grouped_status()
+
+
+@pytest.mark.parametrize("tokens,groups,top_k,d,n,dtype", [
+    (4096, 8, 4, 2048, 1024, "bf16"), (509, 16, 2, 1024, 776, "f16"), (900, 30, 3, 4000, 520, "bf16"), (2000, 6, 2, 1576, 792, "f16")])
+def test_gradient_of_the_weights_in_the_chain(gpu_lib, tokens, groups, top_k, d, n, dtype):
+    """dweights of product and weighted sum: as from 32-bit rows added in order and rounded once, to the rounding of
+    the 32-bit scalar product, and not to that of the rows' 16 bits."""
+    import torch
+    ids = _random_ids(tokens, tokens, groups, top_k)
+    r = _routing(gpu_lib, ids, groups)
+    x, w = _normal(1, tokens, d, dtype=dtype).cuda(), _normal(2, groups, n, d, dtype=dtype, std=d ** -0.5).cuda()
+    dout = _normal(3, tokens, n, dtype=dtype).cuda()
+    _, dweights = gpu_lib.combine_backward(dout, gpu_lib.expert_product(x, w, r), r)
+    rows = gpu_lib.expert_product(x.float(), w.float(), r).to(x.dtype).double()  # the CUDA cores add in order
+    at = r.position.long()
+    picked = torch.where(at[..., None] >= 0, rows[at.clamp(min=0)], 0.0)
+    want = (picked * dout.double()[:, None]).sum(2)
+    mag = (picked * dout.double()[:, None]).abs().sum(2)
+    assert ((dweights.double() - want).abs() <= SUM * n * mag).all()
+    assert float((dweights.double() - want).norm() / want.norm()) <= 2e-6
+
+
 def test_product_gradients_against_differences(gpu_lib):
     import torch
     ids = _random_ids(3, 12, 3, 2)
