@@ -119,13 +119,21 @@ def _want(t, name: str, dtype):
         raise ValueError("%s: a contiguous CUDA tensor of %s is wanted" % (name, dtype))
 
 
+def _one_row(rows: int, cols: int, step: int, name: str) -> int:
+    """The stride of a matrix whose own is shorter than a row: any will do for a single row, others are refused
+    (expanded tensors and sliding windows: the library's matrices have their rows one behind the other)."""
+    if rows > 1:
+        raise ValueError("%s: rows overlap (stride %d, %d columns); contiguous() makes a copy that does not" % (name, step, cols))
+    return cols
+
+
 def _dense(t, name: str) -> bytes:
     shape, step, code = t.shape, t.stride(), _codes.get(t.dtype)
     if code is None or not t.is_cuda or len(shape) != 2 or (step[1] != 1 and shape[1] > 1):
         _refuse(t, name, 2)
         code = _codes[t.dtype]
     rows, cols = shape
-    return _pack_dense(t.data_ptr(), rows, cols, step[0] if step[0] > cols else cols, code, 0)
+    return _pack_dense(t.data_ptr(), rows, cols, step[0] if step[0] >= cols else _one_row(rows, cols, step[0], name), code, 0)
 
 
 def _weights(t, name: str) -> bytes:
@@ -134,7 +142,8 @@ def _weights(t, name: str) -> bytes:
         _refuse(t, name, 3)
         code = _codes[t.dtype]
     groups, rows, cols = shape
-    return _pack_weights(t.data_ptr(), groups, rows, cols, step[0], step[1] if step[1] > cols else cols, code, 0)
+    return _pack_weights(t.data_ptr(), groups, rows, cols, step[0],
+                         step[1] if step[1] >= cols else _one_row(rows, cols, step[1], name), code, 0)
 
 
 _entry: dict = {}  # entry points by name

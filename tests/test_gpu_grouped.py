@@ -599,6 +599,37 @@ def test_refusals(gpu_lib):
         gpu_lib.route_backward(l, gpu_lib.group_rows(r.ids, 8), torch.zeros(4, 2, device="cuda"))
 
 
+def test_expanded_and_overlapping_inputs_are_refused(gpu_lib):
+    """Every matrix of every call: rows that share storage are refused before any device work, copies are taken."""
+    import torch
+    l = _normal(1, 6, 8, dtype="f32").cuda()
+    r = gpu_lib.route(l, 2)
+    x, w = _normal(2, 6, 16).cuda(), _normal(3, 8, 24, 16).cuda()
+    y, dout = _normal(4, 12, 24).cuda(), _normal(5, 6, 24).cuda()
+    up, down = _normal(6, 8, 48, 16).cuda(), _normal(7, 8, 24, 24).cuda()
+    a, b, which = _normal(8, 3, 4, 16).cuda(), _normal(9, 3, 24, 4).cuda(), torch.zeros(6, dtype=torch.int32, device="cuda")
+    wide = lambda t: t[..., :1, :].expand(t.shape)  # noqa: E731  one row for all
+    slide = lambda t: t.reshape(-1).as_strided(t.shape, t.stride()[:-2] + (t.shape[-1] - 1, 1))  # noqa: E731
+    for f in (wide, slide):
+        for call in (lambda: gpu_lib.route(f(l), 2), lambda: gpu_lib.route_backward(f(l), r, torch.zeros(6, 2, device="cuda")),
+                     lambda: gpu_lib.expert_product(f(x), w, r), lambda: gpu_lib.expert_product(x, f(w), r),
+                     lambda: gpu_lib.expert_product_backward(f(y), x, w, r), lambda: gpu_lib.expert_product_backward(y, f(x), w, r),
+                     lambda: gpu_lib.expert_product_backward(y, x, f(w), r), lambda: gpu_lib.combine(f(y), r),
+                     lambda: gpu_lib.combine_backward(f(dout), y, r), lambda: gpu_lib.combine_backward(dout, f(y), r),
+                     lambda: gpu_lib.experts(f(x), up, down, r), lambda: gpu_lib.experts(x, f(up), down, r),
+                     lambda: gpu_lib.experts(x, up, f(down), r), lambda: gpu_lib.adapted_product(f(x), w[0], a, b, which),
+                     lambda: gpu_lib.adapted_product(x, f(w[0]), a, b, which), lambda: gpu_lib.adapted_product(x, w[0], f(a), b, which),
+                     lambda: gpu_lib.adapted_product(x, w[0], a, f(b), which)):
+            with pytest.raises(ValueError, match="overlap"):
+                call()
+    # the gradient of a sum over tokens is such a tensor: copied, it is taken; one matrix for all groups is taken as it is
+    got = gpu_lib.combine_backward(wide(dout).contiguous(), y, r)
+    again = gpu_lib.combine_backward(dout[:1].repeat(6, 1), y, r)
+    assert all(torch.equal(p, q) for p, q in zip(got, again))
+    one = w[:1].expand(8, 24, 16)
+    assert torch.equal(gpu_lib.expert_product(x, one, r), gpu_lib.expert_product(x, one.contiguous(), r))
+
+
 def test_a_wait_that_runs_out_is_reported(gpu_lib):
     """A withheld announcement makes a wait run out in every kind of tensor-core kernel: the status says
     so, and the same calls are right afterwards."""

@@ -145,6 +145,41 @@ def test_layers_refuse():
     assert lib.spgemm_combine_backward(R(g), 16, R(out), R(dense(8, 40)), R(dense(8, 40)), None, None) == -1
 
 
+class Stand:
+    """What the packing looks at, of a tensor on a GPU."""
+    def __init__(self, shape, step):
+        import torch
+        self.shape, self.step, self.dtype, self.is_cuda = shape, step, torch.bfloat16, True
+
+    def stride(self, i=None):
+        return self.step if i is None else self.step[i]
+
+    def dim(self):
+        return len(self.shape)
+
+    def data_ptr(self):
+        return 64
+
+
+@pytest.mark.parametrize("shape,step", [((16, 8), (0, 1)), ((16, 8), (7, 1)), ((2, 8), (1, 1)), ((5, 1), (0, 1)), ((5, 1), (0, 0))])
+def test_rows_that_overlap_are_refused(shape, step):
+    """A stride shorter than a row is not replaced by a longer one: that would read past the storage."""
+    from sparse_gemm_irregular_gb300 import grouped as G
+    with pytest.raises(ValueError, match="overlap"):
+        G._dense(Stand(shape, step), "x")
+    with pytest.raises(ValueError, match="overlap"):
+        G._weights(Stand((3,) + shape, (64,) + step), "w")
+
+
+def test_strides_arrive_as_they_are():
+    from sparse_gemm_irregular_gb300 import grouped as G
+    for shape, step, want in (((16, 8), (8, 1), 8), ((16, 8), (24, 1), 24), ((1, 8), (0, 1), 8), ((1, 8), (3, 1), 8), ((0, 8), (8, 1), 8),
+                              ((5, 1), (1, 7), 1), ((5, 1), (9, 0), 9), ((5, 0), (1, 1), 1)):
+        assert b.spgemm_dense.from_buffer_copy(G._dense(Stand(shape, step), "x")).stride == want
+        w = b.spgemm_weights.from_buffer_copy(G._weights(Stand((3,) + shape, (0,) + step), "w"))  # one matrix for all groups
+        assert (w.row_stride, w.group_stride) == (want, 0)
+
+
 # ---- the reference of the GPU tests, pinned by closed forms -------------------------------------
 def test_reference_route_closed_forms():
     ids, w, _ = route(np.array([[0.0, np.log(2.0), np.log(4.0), -np.inf]]), 2)
