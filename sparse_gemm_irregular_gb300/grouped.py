@@ -4,9 +4,14 @@ matrix of the group that a sparse choice sends them to.
 The calls marshal PyTorch device tensors into the C entry points of include/spgemm.h
 (``spgemm_route`` and those after it) and allocate the outputs; they enqueue on the given or the
 current stream and do not synchronise.  ``Routing`` is the choice together with its transpose.
+
+A call with ``stream=`` is the call with that stream current: its outputs belong to that stream, its inputs'
+memory is not handed out again before the stream has passed it.  What the inputs still wait for on other
+streams, and who reads the outputs on others, is the caller's to order, as everywhere in PyTorch.
 """
 from __future__ import annotations
 
+import functools
 import struct
 from dataclasses import dataclass
 from typing import Any
@@ -149,14 +154,35 @@ def _weights(t, name: str) -> bytes:
 _entry: dict = {}  # entry points by name
 
 
-def _call(name: str, device, stream, *args):
-    """Call an entry point with `device` current and the given or the current stream as last argument."""
+def _on_stream(fn):
+    """Gives a call its ``stream`` argument: everything that it allocates, fills and launches belongs there."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+        used = [t for a in (*args, *kw.values()) for t in
+                ((a.ids, a.weights, a.offsets, a.order, a.position) if isinstance(a, Routing) else (a,))
+                if isinstance(t, torch.Tensor)]
+        for t in used:
+            if t.device != stream.device:
+                raise ValueError("stream: on %s, a tensor on %s" % (stream.device, t.device))
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kw)
+        for t in used:
+            t.record_stream(stream)
+        return out
+    return call
+
+
+def _call(name: str, device, *args):
+    """Call an entry point with `device` current and its current stream as last argument."""
     import torch
     fn = _entry.get(name)
     if fn is None:
         fn = _entry[name] = getattr(load(), name)
     index = device.index
-    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    raw = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() == index:
         rc = fn(*args, raw)
     else:
@@ -166,6 +192,7 @@ def _call(name: str, device, stream, *args):
         _check(rc, name)
 
 
+@_on_stream
 def route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int = 1, groups_kept: int = 1,
           group_score: str = "max", renormalise: bool = True, scale: float = 1.0, stream=None) -> Routing:
     """Choose ``top_k`` experts per token from router logits (tokens, experts).
@@ -189,11 +216,12 @@ def route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int 
     whole = torch.empty(3 * n + logits.shape[1] + 1, dtype=torch.int32, device=dev)  # one allocation for four arrays
     ids, position = whole.as_strided((t, k), (k, 1)), whole.as_strided((t, k), (k, 1), n)
     order, offsets = whole.as_strided((n,), (1,), 2 * n), whole.as_strided((logits.shape[1] + 1,), (1,), 3 * n)
-    _call("spgemm_route", dev, stream, d, rule, bias.data_ptr() if bias is not None else None,
+    _call("spgemm_route", dev, d, rule, bias.data_ptr() if bias is not None else None,
           ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), position.data_ptr())
     return Routing._made(ids, weights, offsets, order, position, rule)
 
 
+@_on_stream
 def route_backward(logits, routing: Routing, grad_weights, *, stream=None):
     """Gradient of the logits for a gradient of ``routing.weights`` (see spgemm_route_backward)."""
     import torch
@@ -204,11 +232,12 @@ def route_backward(logits, routing: Routing, grad_weights, *, stream=None):
     if grad_weights.shape != routing.ids.shape or logits.shape[0] != routing.tokens:
         raise ValueError("grad_weights: (tokens, top_k) is wanted")
     out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    _call("spgemm_route_backward", logits.device, stream, d, routing.rule, routing.ids.data_ptr(),
+    _call("spgemm_route_backward", logits.device, d, routing.rule, routing.ids.data_ptr(),
           grad_weights.data_ptr(), _dense(out, "grad_logits"))
     return out
 
 
+@_on_stream
 def group_rows(ids, groups: int, *, weights=None, stream=None) -> Routing:
     """The Routing of given ids (tokens, top_k) or (tokens,) int32, -1 for none; weights default to
     ones (see spgemm_group_rows)."""
@@ -219,7 +248,7 @@ def group_rows(ids, groups: int, *, weights=None, stream=None) -> Routing:
     offsets = torch.empty(groups + 1, dtype=torch.int32, device=dev)
     order = torch.empty(ids.numel(), dtype=torch.int32, device=dev)
     position = torch.empty_like(ids)
-    _call("spgemm_group_rows", dev, stream, ids.data_ptr(), ids.numel(), groups, offsets.data_ptr(),
+    _call("spgemm_group_rows", dev, ids.data_ptr(), ids.numel(), groups, offsets.data_ptr(),
           order.data_ptr(), position.data_ptr())
     if weights is None:
         weights = torch.ones(ids.shape, dtype=torch.float32, device=dev)
@@ -229,6 +258,7 @@ def group_rows(ids, groups: int, *, weights=None, stream=None) -> Routing:
     return Routing._made(ids, weights, offsets, order, position)
 
 
+@_on_stream
 def expert_product(x, w, routing: Routing, *, grouped: bool = False, out_dtype=None, stream=None):
     """Rows times the matrix of their group: (slots, w.shape[1]) in group order.
 
@@ -238,54 +268,59 @@ def expert_product(x, w, routing: Routing, *, grouped: bool = False, out_dtype=N
     g = routing._grouping
     dx, dw = _dense(x, "x"), _weights(w, "w")
     y = torch.empty((routing.ids.numel(), w.shape[1]), dtype=out_dtype or x.dtype, device=x.device)
-    _call("spgemm_grouped_product", x.device, stream, g, dx, int(grouped), dw, _dense(y, "y"))
+    _call("spgemm_grouped_product", x.device, g, dx, int(grouped), dw, _dense(y, "y"))
     return y
 
 
+@_on_stream
 def expert_product_backward(dy, x, w, routing: Routing, *, need_dx: bool = True, need_dw: bool = True, stream=None):
     """(dx, dw) of ``expert_product`` with one row of x per token (see spgemm_grouped_product_backward)."""
     import torch
     g = routing._grouping
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
     dw = torch.empty(w.shape, dtype=w.dtype, device=x.device) if need_dw else None
-    _call("spgemm_grouped_product_backward", x.device, stream, g, _dense(dy, "dy"), _dense(x, "x"),
+    _call("spgemm_grouped_product_backward", x.device, g, _dense(dy, "dy"), _dense(x, "x"),
           _weights(w, "w"), _dense(dx, "dx") if need_dx else None,
           _weights(dw, "dw") if need_dw else None)
     return dx, dw
 
 
+@_on_stream
 def combine(y, routing: Routing, *, out_dtype=None, stream=None):
     """Weighted sum of a token's rows: (tokens, y.shape[1]) (see spgemm_combine)."""
     import torch
     g = routing._grouping
     out = torch.empty((routing.tokens, y.shape[1]), dtype=out_dtype or y.dtype, device=y.device)
-    _call("spgemm_combine", y.device, stream, g, routing.weights.data_ptr(), _dense(y, "y"),
+    _call("spgemm_combine", y.device, g, routing.weights.data_ptr(), _dense(y, "y"),
           _dense(out, "out"))
     return out
 
 
+@_on_stream
 def combine_backward(dout, y, routing: Routing, *, stream=None):
     """(dy, dweights) of ``combine`` (see spgemm_combine_backward)."""
     import torch
     g = routing._grouping
     dy = torch.empty(y.shape, dtype=y.dtype, device=y.device)
     dweights = torch.empty(routing.ids.shape, dtype=torch.float32, device=y.device)
-    _call("spgemm_combine_backward", y.device, stream, g, routing.weights.data_ptr(),
+    _call("spgemm_combine_backward", y.device, g, routing.weights.data_ptr(),
           _dense(dout, "dout"), _dense(y, "y"), _dense(dy, "dy"), dweights.data_ptr())
     return dy, dweights
 
 
+@_on_stream
 def experts(x, w_up, w_down, routing: Routing, *, stream=None):
     """A gated expert layer, (tokens, d) -> (tokens, w_down.shape[1]): w_up (groups, 2 * hidden, d)
     holds the gate's rows, then up's; w_down (groups, n, hidden).  See spgemm_experts."""
     import torch
     g = routing._grouping
     out = torch.empty((x.shape[0], w_down.shape[1]), dtype=x.dtype, device=x.device)
-    _call("spgemm_experts", x.device, stream, g, routing.weights.data_ptr(), _dense(x, "x"),
+    _call("spgemm_experts", x.device, g, routing.weights.data_ptr(), _dense(x, "x"),
           _weights(w_up, "w_up"), _weights(w_down, "w_down"), _dense(out, "out"))
     return out
 
 
+@_on_stream
 def adapted_product(x, w, a, b, ids, scale=None, *, stream=None):
     """x w^T + scale[i] (x a[i]^T) b[i]^T with i = ids[token] (int32; -1: the projection alone).
 
@@ -300,7 +335,7 @@ def adapted_product(x, w, a, b, ids, scale=None, *, stream=None):
         if scale.numel() != a.shape[0]:
             raise ValueError("scale: one value per adapter is wanted")
     y = torch.empty((x.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
-    _call("spgemm_adapted_product", x.device, stream, _dense(x, "x"), _dense(w, "w"),
+    _call("spgemm_adapted_product", x.device, _dense(x, "x"), _dense(w, "w"),
           _weights(a, "a"), _weights(b, "b"), ids.data_ptr(),
           scale.data_ptr() if scale is not None else None, _dense(y, "y"))
     return y

@@ -355,6 +355,77 @@ def test_product_strides_and_streams(gpu_lib):
         assert np.all(np.abs(_np(y) - want) <= rounding("bf16", want) + SUM * 128 * mag)
 
 
+def _busy(torch):
+    """Some tens of milliseconds of ordinary work on the current stream."""
+    a = torch.ones(8192, 8192, device="cuda", dtype=torch.bfloat16)
+    for _ in range(30):
+        a @ a
+
+
+def test_calls_on_a_side_stream_wait_for_no_other(gpu_lib):
+    """Default weights are filled on the call's stream, not behind what the current one has under way."""
+    import torch
+    ids = _random_ids(8, 3000, 6, 2)
+    ids_c, y = torch.tensor(ids).cuda(), _normal(1, 6000, 64).cuda()
+    want = gpu_lib.combine(y, gpu_lib.group_rows(ids_c, 6))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):  # what a recycled block would hold
+        for size in ((3000, 2), (6000,)):
+            torch.full(size, 7.0, device="cuda")
+    torch.full((3000, 2), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    _busy(torch)
+    r = gpu_lib.group_rows(ids_c, 6, stream=side)
+    out = gpu_lib.combine(y, r, stream=side)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()  # the current stream is still busy: nothing waited for it
+    with torch.cuda.stream(side):
+        assert torch.equal(out.clone(), want)
+    torch.cuda.synchronize()
+
+
+def test_outputs_of_a_side_stream_are_its_own(gpu_lib):
+    """The current stream still writes to a tensor that is given up: its memory is not the side stream's output."""
+    import torch
+    ids = _random_ids(8, 2000, 6, 2)
+    r = _routing(gpu_lib, ids, 6)
+    x, w = _normal(1, 2000, 128).cuda(), _normal(2, 6, 512, 128).cuda()
+    want = gpu_lib.expert_product(x, w, r)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    _busy(torch)
+    given_up = torch.zeros(4000, 512, device="cuda", dtype=torch.bfloat16)
+    block = given_up.data_ptr()
+    del given_up
+    y = gpu_lib.expert_product(x, w, r, stream=side)
+    side.synchronize()
+    assert y.data_ptr() != block
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+
+def test_inputs_of_a_side_stream_are_kept(gpu_lib):
+    """An input that is given up after the call is not handed out while the side stream has yet to read it."""
+    import torch
+    ids = _random_ids(8, 2000, 6, 2)
+    r = _routing(gpu_lib, ids, 6)
+    x, w = _normal(1, 2000, 128).cuda(), _normal(2, 6, 512, 128).cuda()
+    want = gpu_lib.expert_product(x, w, r)
+    side = torch.cuda.Stream()
+    mine = x.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        _busy(torch)
+    y = gpu_lib.expert_product(mine, w, r, stream=side)
+    block = mine.data_ptr()
+    del mine
+    other = torch.full_like(x, float("nan"))
+    assert other.data_ptr() != block
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+
 def test_outputs_past_32_bit_offsets(gpu_lib):
     """More than 2^31 elements in y: rows at the start, around the boundary and at the end."""
     import torch
