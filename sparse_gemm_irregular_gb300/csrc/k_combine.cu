@@ -169,7 +169,11 @@ void launch_spread_rows(const spgemm_grouping& g, const spgemm_dense& x, const s
 void launch_combine_backward(const spgemm_grouping& g, const float* weights, const spgemm_dense& dout,
                              const spgemm_dense& y, const spgemm_dense& dy, float* dweights, cudaStream_t s) {
   const int64_t tokens = dout.rows;
-  if (tokens == 0 || dout.cols == 0) return;
+  if (tokens == 0) return;
+  if (dout.cols == 0) {  // scalar products of no terms
+    cudaMemsetAsync(dweights, 0, sizeof(float) * g.slots, s);
+    return;
+  }
   for_dtype(y.dtype, [&](auto ty) {
     using T = decltype(ty);
     auto go = [&](auto v) {

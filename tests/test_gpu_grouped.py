@@ -503,6 +503,17 @@ def test_combine_and_gradients(gpu_lib, tokens, groups, top_k, n, dtype):
     assert torch.all(dy[offsets[-1]:] == 0)
 
 
+def test_gradient_of_the_weights_without_columns(gpu_lib):
+    """A scalar product of no terms is 0, whatever the output's memory held."""
+    import torch
+    r = _routing(gpu_lib, _random_ids(3, 50, 4, 2), 4)
+    dout, y = torch.empty(50, 0, device="cuda"), torch.empty(100, 0, device="cuda")
+    for _ in range(3):
+        torch.full((50, 2), 7.0, device="cuda")  # the block that the output gets
+        dy, dweights = gpu_lib.combine_backward(dout, y, r)
+        assert dy.shape == (100, 0) and torch.all(dweights == 0)
+
+
 # ---- the gated layer -----------------------------------------------------------------------------
 @pytest.mark.parametrize("tokens,groups,top_k,d,hidden,n", [
     (1, 1, 1, 8, 8, 8), (1, 16, 4, 64, 96, 64), (9, 8, 3, 72, 40, 136), (200, 6, 2, 128, 64, 200), (700, 4, 2, 264, 328, 128),
