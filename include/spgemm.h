@@ -458,7 +458,8 @@ int spgemm_combine(const spgemm_grouping* g, const float* weights, const spgemm_
                    void* stream);
 
 /* Gradients of spgemm_combine: dy[p, :] = weights[slot] * dout[t, :] (zero from offsets[groups]
- * on), dweights[slot] = <dout[t, :], y[p, :]> (zero for a slot without a group). */
+ * on), dweights[slot] = <dout[t, :], y[p, :]> (zero for a slot without a group).  dy has dout's type; y may have
+ * another: with y in 32 bits dweights carries no rounding of the rows to 16. */
 int spgemm_combine_backward(const spgemm_grouping* g, const float* weights, const spgemm_dense* dout,
                             const spgemm_dense* y, const spgemm_dense* dy, float* dweights, void* stream);
 

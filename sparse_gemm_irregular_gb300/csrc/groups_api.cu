@@ -264,7 +264,7 @@ int spgemm_combine_backward(const spgemm_grouping* g, const float* weights, cons
   if (g->slots > 0 && !dweights) return bad("combine backward: null dweights");
   if (y->rows != g->slots || y->cols != dout->cols || dy->rows != y->rows || dy->cols != y->cols)
     return bad("combine backward: shapes differ");
-  if (y->dtype != dout->dtype || dy->dtype != dout->dtype) return bad("combine backward: types differ");
+  if (dy->dtype != dout->dtype) return bad("combine backward: types of dout and dy differ");
   launch_combine_backward(*g, weights, *dout, *y, *dy, dweights, static_cast<cudaStream_t>(stream));
   return check_cuda(cudaGetLastError(), "combine backward");
 }

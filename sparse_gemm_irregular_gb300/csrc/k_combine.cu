@@ -93,11 +93,11 @@ __global__ void __launch_bounds__(kThreads) k_spread_rows(const int32_t* __restr
 
 // One block per token: the row of dout is read once per slot, from L1 after the first.  65536 x 2048 in bf16:
 // 101 us, 604 MB at 6.0 TB/s.
-template <typename T, int V>
+template <typename T, typename TY, int V>
 __global__ void __launch_bounds__(kThreads) k_combine_backward(
     const int32_t* __restrict__ offsets, int groups, const int32_t* __restrict__ position, int64_t tokens, int top_k,
     int64_t slots, const float* __restrict__ weights, const T* __restrict__ dout, int64_t dout_stride,
-    const T* __restrict__ y, int64_t y_stride, T* __restrict__ dy, int64_t dy_stride, float* __restrict__ dweights,
+    const TY* __restrict__ y, int64_t y_stride, T* __restrict__ dy, int64_t dy_stride, float* __restrict__ dweights,
     int64_t cols) {
   __shared__ float s_part[kThreads / 32];
   pdl_wait();
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) k_combine_backward(
         const float w = weights ? weights[t * top_k + j] : 1.0f;
         for (int64_t c = static_cast<int64_t>(threadIdx.x) * V; c < cols; c += kThreads * V) {
           const Pack<T, V> d = *reinterpret_cast<const Pack<T, V>*>(dout + t * dout_stride + c);
-          const Pack<T, V> r = *reinterpret_cast<const Pack<T, V>*>(y + p * y_stride + c);
+          const Pack<TY, V> r = *reinterpret_cast<const Pack<TY, V>*>(y + p * y_stride + c);
           Pack<T, V> o;
 #pragma unroll
           for (int v = 0; v < V; ++v) {
@@ -174,18 +174,21 @@ void launch_combine_backward(const spgemm_grouping& g, const float* weights, con
     cudaMemsetAsync(dweights, 0, sizeof(float) * g.slots, s);
     return;
   }
-  for_dtype(y.dtype, [&](auto ty) {
-    using T = decltype(ty);
-    auto go = [&](auto v) {
-      constexpr int V = decltype(v)::value;
-      launch_next(k_combine_backward<T, V>, static_cast<unsigned>(std::min<int64_t>(tokens, 1 << 20)), kThreads, 0, s,
-                  g.offsets, g.groups, g.position, tokens, g.top_k, g.slots, weights, static_cast<const T*>(dout.data),
-                  dout.stride, static_cast<const T*>(y.data), y.stride, static_cast<T*>(dy.data), dy.stride, dweights,
-                  dout.cols);
-    };
-    constexpr int W = 16 / sizeof(T);
-    if (packs<T>(dout, W) && packs<T>(y, W) && packs<T>(dy, W)) go(std::integral_constant<int, W>());
-    else go(std::integral_constant<int, 1>());
+  for_dtype(dout.dtype, [&](auto td) {
+    for_dtype(y.dtype, [&](auto ty) {
+      using T = decltype(td);
+      using TY = decltype(ty);
+      auto go = [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        launch_next(k_combine_backward<T, TY, V>, static_cast<unsigned>(std::min<int64_t>(tokens, 1 << 20)), kThreads, 0, s,
+                    g.offsets, g.groups, g.position, tokens, g.top_k, g.slots, weights, static_cast<const T*>(dout.data),
+                    dout.stride, static_cast<const TY*>(y.data), y.stride, static_cast<T*>(dy.data), dy.stride, dweights,
+                    dout.cols);
+      };
+      constexpr int W = 16 / (sizeof(TY) > sizeof(T) ? sizeof(TY) : sizeof(T));
+      if (packs<T>(dout, W) && packs<TY>(y, W) && packs<T>(dy, W)) go(std::integral_constant<int, W>());
+      else go(std::integral_constant<int, 1>());
+    });
   });
 }
 

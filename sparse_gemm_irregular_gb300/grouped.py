@@ -298,10 +298,10 @@ def combine(y, routing: Routing, *, out_dtype=None, stream=None):
 
 @_on_stream
 def combine_backward(dout, y, routing: Routing, *, stream=None):
-    """(dy, dweights) of ``combine`` (see spgemm_combine_backward)."""
+    """(dy, dweights) of ``combine``; dy has dout's type, y may have another (see spgemm_combine_backward)."""
     import torch
     g = routing._grouping
-    dy = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+    dy = torch.empty(y.shape, dtype=dout.dtype, device=y.device)
     dweights = torch.empty(routing.ids.shape, dtype=torch.float32, device=y.device)
     _call("spgemm_combine_backward", y.device, g, routing.weights.data_ptr(),
           _dense(dout, "dout"), _dense(y, "y"), _dense(dy, "dy"), dweights.data_ptr())

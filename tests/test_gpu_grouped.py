@@ -503,6 +503,42 @@ def test_combine_and_gradients(gpu_lib, tokens, groups, top_k, n, dtype):
     assert torch.all(dy[offsets[-1]:] == 0)
 
 
+@pytest.mark.parametrize("tokens,groups,top_k,d,n,dtype", [
+    (4096, 8, 4, 2048, 1024, "bf16"), (509, 16, 2, 1024, 776, "f16"), (70, 5, 2, 264, 33, "bf16")])
+def test_gradient_of_the_weights_from_32_bit_rows(gpu_lib, tokens, groups, top_k, d, n, dtype):
+    """The chain with rows in 32 bits and everything else in 16: dweights of the unrounded product."""
+    import torch
+    ids = _random_ids(tokens, tokens, groups, top_k)
+    weights = np.random.default_rng(1).random(ids.shape).astype(np.float32)
+    r = _routing(gpu_lib, ids, groups, weights)
+    x, w = _normal(1, tokens, d, dtype=dtype).cuda(), _normal(2, groups, n, d, dtype=dtype, std=d ** -0.5).cuda()
+    dout = _normal(3, tokens, n, dtype=dtype).cuda()
+    y = gpu_lib.expert_product(x, w, r, out_dtype=torch.float32)
+    out = gpu_lib.combine(y, r, out_dtype=x.dtype)
+    dy, dweights = gpu_lib.combine_backward(dout, y, r)
+    assert out.dtype == dy.dtype == x.dtype and dweights.dtype == torch.float32
+    same, _ = gpu_lib.combine_backward(dout, y.to(x.dtype), r)
+    assert torch.equal(dy, same)
+    want = torch.zeros(tokens, top_k, dtype=torch.float64, device="cuda")
+    for g in range(groups):
+        at = (torch.tensor(ids).cuda() == g).nonzero()
+        want[at[:, 0], at[:, 1]] = (dout[at[:, 0]].double() * (x[at[:, 0]].double() @ w[g].double().t())).sum(1)
+    assert float((dweights.double() - want).norm() / want.norm()) <= 1e-5
+    dx, dw = gpu_lib.expert_product_backward(dy, x, w, r)  # the rest of the chain takes it
+    assert dx.dtype == dw.dtype == x.dtype
+
+
+@pytest.mark.parametrize("dout_type,y_type", [("f32", "bf16"), ("bf16", "f16"), ("f16", "f32")])
+def test_combine_backward_of_mixed_types(gpu_lib, dout_type, y_type):
+    r = _routing(gpu_lib, _random_ids(3, 50, 4, 2), 4)
+    dout, y = _normal(1, 50, 40, dtype=dout_type).cuda(), _normal(2, 100, 40, dtype=y_type).cuda()
+    dy, dweights = gpu_lib.combine_backward(dout, y, r)
+    ref_dy, ref = gpu_lib.combine_backward(dout.float(), y.float(), r)
+    assert dy.dtype == dout.dtype and (dy == ref_dy.to(dout.dtype)).all()
+    mag = (dout.float().abs().amax() * y.float().abs().amax()).item() * 40
+    assert (dweights - ref).abs().max() <= SUM * 40 * mag
+
+
 def test_gradient_of_the_weights_without_columns(gpu_lib):
     """A scalar product of no terms is 0, whatever the output's memory held."""
     import torch
