@@ -480,10 +480,11 @@ int spgemm_adapted_product(const spgemm_dense* x, const spgemm_dense* w, const s
  * SPGEMM_OK, or SPGEMM_ERR_DEVICE when a device-side check failed since the last call. */
 int spgemm_grouped_status(void* stream);
 
-/* For tests: polls > 0 limits every wait inside the tensor-core kernels of later calls of this process
+/* For tests: polls > 0 limits every wait inside the tensor-core kernels of later calls of this thread
  * to that many polls (0: about a second's worth), and hold != 0 makes the first block of each such
  * kernel withhold one announcement, so that a wait runs out and spgemm_grouped_status answers
- * SPGEMM_ERR_DEVICE; that call's results are meaningless, the context and later calls are not affected. */
+ * SPGEMM_ERR_DEVICE; that call's results are meaningless, the context, later calls and other threads' calls
+ * are not affected. */
 int spgemm_grouped_debug(int32_t hold, int32_t polls);
 
 const char* spgemm_strerror(int code);

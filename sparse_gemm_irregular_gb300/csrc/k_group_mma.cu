@@ -865,13 +865,12 @@ int64_t most_tiles(const spgemm_grouping& g, int tile_n) {
   return g.slots / tile_n + std::min<int64_t>(g.groups, g.slots);
 }
 
-std::atomic<int32_t> g_hold{0}, g_polls{0};  // set by tests
+thread_local int32_t t_hold = 0, t_polls = 0;  // set by tests, for the calls of their own thread
 
 MmaArgs base_args(const spgemm_grouping& g, int32_t dtype) {
   MmaArgs a = {};
-  const int32_t polls = g_polls.load(std::memory_order_relaxed);
-  a.hold = g_hold.load(std::memory_order_relaxed);
-  a.polls = polls > 0 ? static_cast<uint32_t>(polls) : tc::kMaxPolls;
+  a.hold = t_hold;
+  a.polls = t_polls > 0 ? static_cast<uint32_t>(t_polls) : tc::kMaxPolls;
   a.offsets = g.offsets;
   a.order = g.order;
   a.slots = static_cast<int>(g.slots);
@@ -887,8 +886,8 @@ bool aligned(const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>
 }  // namespace
 
 void mma_debug(int32_t hold, int32_t polls) {
-  g_hold.store(hold, std::memory_order_relaxed);
-  g_polls.store(polls, std::memory_order_relaxed);
+  t_hold = hold;
+  t_polls = polls;
 }
 
 bool mma_gathers(const spgemm_grouping& g) { return g.slots <= 64 * static_cast<int64_t>(g.groups); }

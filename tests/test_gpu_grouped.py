@@ -780,3 +780,28 @@ def test_a_wait_that_runs_out_is_reported(gpu_lib):
             lib.spgemm_grouped_debug(0, 0)
         assert torch.equal(call(), before)
         gpu_lib.grouped_status()
+
+
+def test_the_hook_of_one_thread_leaves_the_others_alone(gpu_lib):
+    import threading
+
+    import torch
+    lib = gpu_lib.load()
+    r = _routing(gpu_lib, _random_ids(2, 600, 2, 2), 2)
+    x, w = _normal(1, 600, 256).cuda(), _normal(2, 2, 256, 256, std=1 / 16).cuda()
+    want = gpu_lib.expert_product(x, w, r)
+    got = []
+
+    def other():
+        got.append(gpu_lib.expert_product(x, w, r))
+        gpu_lib.grouped_status()
+
+    try:
+        assert lib.spgemm_grouped_debug(1, 500) == 0
+        t = threading.Thread(target=other)
+        t.start()
+        t.join()
+    finally:
+        lib.spgemm_grouped_debug(0, 0)
+    assert len(got) == 1 and torch.equal(got[0], want)
+    gpu_lib.grouped_status()
