@@ -487,6 +487,11 @@ int spgemm_grouped_status(void* stream);
  * are not affected. */
 int spgemm_grouped_debug(int32_t hold, int32_t polls);
 
+/* For tests: the tensor-core kernels of later calls of this thread take tiles of `width` rows (16 to 256, a power
+ * of two; 0: by their own rule), shared by two blocks when `pair` is set and width is 256, their depth split over up
+ * to `split` blocks, as far as each kernel can. */
+int spgemm_grouped_force(int32_t width, int32_t pair, int32_t split);
+
 const char* spgemm_strerror(int code);
 /* Detail of the last failure on the calling host thread ("" if none). */
 const char* spgemm_last_error(void);

@@ -35,6 +35,8 @@ struct MmaArgs {
 
 // see spgemm_grouped_debug
 void mma_debug(int32_t hold, int32_t polls);
+// see spgemm_grouped_force
+void mma_force(int32_t width, int32_t pair, int32_t split);
 
 // whether the copy engine can fetch rows of this matrix: 16-bit, 16-byte aligned rows
 bool mma_takes(const spgemm_dense& m);

@@ -359,6 +359,13 @@ int spgemm_grouped_debug(int32_t hold, int32_t polls) {
   return SPGEMM_OK;
 }
 
+int spgemm_grouped_force(int32_t width, int32_t pair, int32_t split) {
+  const bool two = width >= 16 && width <= 256 && (width & (width - 1)) == 0;
+  if ((width && !two) || pair < 0 || pair > 1 || split < 0 || split > 8) return bad("grouped force: out of range");
+  mma_force(width, pair, split);
+  return SPGEMM_OK;
+}
+
 int spgemm_grouped_status(void* stream) {
   set_last_error("");
   cudaStream_t st = static_cast<cudaStream_t>(stream);

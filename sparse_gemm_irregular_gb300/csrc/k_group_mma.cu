@@ -807,6 +807,21 @@ struct Width {
   int split;
 };
 
+// set by tests, for the calls of their own thread
+thread_local int32_t t_hold = 0, t_polls = 0;
+thread_local Width t_width = {0, false, 0};
+
+// What a test asked for, as far as the kernel at hand allows it (widths from `least` to `most`, and the limits of
+// most_split() without its question whether there are idle SMs); nothing asked: `rule`.
+Width chosen(const Width& rule, int least, int most, bool splits, int64_t slices) {
+  if (!t_width.n) return rule;
+  Width w{std::min(std::max(t_width.n, least), most), false, 1};
+  w.pair = t_width.pair && w.n == 256;
+  if (splits && w.n <= kSplitTile)
+    while (w.split < t_width.split && w.split * 4 <= slices && w.split * 8 <= w.n) w.split *= 2;
+  return w;
+}
+
 // The most blocks (up to 8) that may share a tile's depth: only where the tiles (at most `tiles`) leave half
 // the SMs idle, as many as fit at two per SM, with at least two slices each.
 int most_split(int n, int64_t tiles, int64_t slices) {
@@ -842,7 +857,7 @@ Width pick_width(int64_t m, int m_per_block, int64_t slices, int least, bool spl
         best = Width{n, side == 2, split};
       }
     }
-  return best;
+  return chosen(best, least, 256, splits, slices);
 }
 
 // N-side tiles of a grouping whose groups are not known here: each group that has rows ends in a part tile
@@ -865,7 +880,6 @@ int64_t most_tiles(const spgemm_grouping& g, int tile_n) {
   return g.slots / tile_n + std::min<int64_t>(g.groups, g.slots);
 }
 
-thread_local int32_t t_hold = 0, t_polls = 0;  // set by tests, for the calls of their own thread
 
 MmaArgs base_args(const spgemm_grouping& g, int32_t dtype) {
   MmaArgs a = {};
@@ -889,6 +903,7 @@ void mma_debug(int32_t hold, int32_t polls) {
   t_hold = hold;
   t_polls = polls;
 }
+void mma_force(int32_t width, int32_t pair, int32_t split) { t_width = Width{width, pair != 0, split}; }
 
 bool mma_gathers(const spgemm_grouping& g) { return g.slots <= 64 * static_cast<int64_t>(g.groups); }
 
@@ -996,8 +1011,10 @@ bool launch_mma_shrink(const spgemm_grouping& g, const spgemm_dense& x, const sp
   // the widest tile that still gives every SM one: x is read once either way, a's rows once per tile
   a.tile_n = 32;
   while (a.tile_n < 128 && g.slots > static_cast<int64_t>(a.tile_n) * sm_count()) a.tile_n *= 2;
+  const Width asked = chosen(Width{a.tile_n, false, 0}, 32, 128, true, ceil_div(a.depth, kDeep));
+  a.tile_n = asked.n;
   const int64_t tiles = most_tiles(g, a.tile_n) * ceil_div(a.m, 128);
-  const Width width{a.tile_n, false, most_split(a.tile_n, tiles, ceil_div(a.depth, kDeep))};
+  const Width width{a.tile_n, false, asked.split ? asked.split : most_split(a.tile_n, tiles, ceil_div(a.depth, kDeep))};
   a.box_rows = 32;
   a.out = v.data;
   a.out_stride = v.stride;

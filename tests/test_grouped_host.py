@@ -107,6 +107,13 @@ def test_debug_refuses_negative_polls():
     assert lib.spgemm_grouped_debug(0, 0) == 0
 
 
+def test_force_refuses_what_no_kernel_has():
+    lib = sg.load()
+    for args in ((8, 0, 0), (48, 0, 0), (512, 0, 0), (-16, 0, 0), (256, 2, 0), (256, -1, 0), (64, 0, 9), (64, 0, -1)):
+        assert lib.spgemm_grouped_force(*args) == -1, args
+    assert lib.spgemm_grouped_force(64, 0, 4) == 0 and lib.spgemm_grouped_force(0, 0, 0) == 0
+
+
 def test_products_refuse():
     lib = sg.load()
     g, x, w, y = grouping(8, 2, 3), dense(4, 16), weights(3, 24, 16), dense(8, 24)
