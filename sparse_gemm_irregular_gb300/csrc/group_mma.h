@@ -25,6 +25,8 @@ struct MmaArgs {
   const float* scale;      // per group (scatter)
   const int32_t* ids;      // Adapted: the adapter of each row
   int adapters, rank;
+  const void *x, *w, *v, *b;  // Adapted: the operands again, for sums that came out NaN or infinite
+  int64_t x_stride, w_stride, v_stride, b_stride, b_group;
   int split;               // blocks that share a tile's contracted range
   uint32_t* unsure;        // Forward, 16-bit rows out: where the marks go (k_group_settle.cu), or NULL
   float near;              // sums closer than this times the largest beside them to a rounding boundary are marked

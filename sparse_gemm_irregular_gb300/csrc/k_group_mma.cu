@@ -108,6 +108,43 @@ struct Tile {
 
 }  // namespace
 
+// Adapted: the products of a tile's adapters go to all of its columns, the tokens of others meeting them with zeros.
+// Zero times an infinite or NaN b is NaN, so a sum that is not finite is formed again, in 32 bits, from what belongs to
+// its token.  True when there was reason to: the tile [j0, j0 + n) holds an adapter that is not the token's own.
+template <typename T>
+__device__ __noinline__ bool own_sum(const MmaArgs& p, int j0, int n, int token, int m, float* sum) {
+  auto id_of = [&](int t) {
+    const int id = p.ids[t];
+    return id >= 0 && id < p.adapters ? id : -1;
+  };
+  const int own = id_of(token);
+  bool others = false;
+  for (int j = j0; j < j0 + n && !others; ++j) {
+    const int id = id_of(j);
+    others = id >= 0 && id != own;
+  }
+  if (!others) return false;
+  pdl_wait();  // v is the kernel's before this one
+  float acc = 0.0f;
+  auto dot = [&](const void* a, int64_t a_at, const void* b, int64_t b_at, int depth) {  // rows start on 16 bytes
+    const T *u = static_cast<const T*>(a) + a_at, *v = static_cast<const T*>(b) + b_at;
+    int k = 0;
+    for (; k + 8 <= depth; k += 8) {
+      const uint4 x = *reinterpret_cast<const uint4*>(u + k), y = *reinterpret_cast<const uint4*>(v + k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        acc = fmaf(to_f32(reinterpret_cast<const T*>(&x)[e]), to_f32(reinterpret_cast<const T*>(&y)[e]), acc);
+    }
+    for (; k < depth; ++k) acc = fmaf(to_f32(u[k]), to_f32(v[k]), acc);
+  };
+  dot(p.x, token * p.x_stride, p.w, m * p.w_stride, p.depth);
+  if (own >= 0) dot(p.v, token * p.v_stride, p.b, own * p.b_group + m * p.b_stride, p.rank);
+  *sum = acc;
+  return true;
+}
+
+__device__ __forceinline__ bool not_finite(uint32_t bits) { return (bits & 0x7fffffffu) >= 0x7f800000u; }
+
 struct MmaMaps {
   CUtensorMap a, b, c, d;  // Forward, Dx: weights, rows (gathered: also in boxes); Dw: x, dy, then rows of dy and of x; Adapted: w, x, b[i], v rows
 };
@@ -591,6 +628,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
             if (p.out_type == SPGEMM_DTYPE_BF16) mark(__nv_bfloat16());
             else mark(__half());
           }
+          uint32_t odd = 0;  // Adapted: sums to form again
+          if (MODE == kMmaAdapted) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) odd |= not_finite(r[e]) && e < n ? 1u << e : 0u;
+            if (m >= p.m) odd = 0;
+          }
           int token = 0;
           float f = 1.0f;
           if (MODE == kMmaForward && p.scatter) {  // rows leave in the tokens' order
@@ -615,6 +658,13 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (e < n && m < p.m) out[o + e * p.out_stride] = from_f32<T>(__uint_as_float(r[e]));
+            }
+            if constexpr (MODE == kMmaAdapted && sizeof(T) == 2) {
+              for (; odd; odd &= odd - 1) {
+                const int e = __ffs(odd) - 1;
+                float sum;
+                if (own_sum<T>(p, t.j0, t.n, t.j0 + j + e, m, &sum)) out[o + e * p.out_stride] = from_f32<T>(sum);
+              }
             }
           };
           if (p.out_type == SPGEMM_DTYPE_F32) put(float());
@@ -688,6 +738,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           if (MODE == kMmaForward && p.scatter) {
             row = max(p.order[row], 0) / p.top_k;
             if (p.scale) sum[e] *= p.scale[t.g];
+          }
+          if (MODE == kMmaAdapted && not_finite(__float_as_uint(sum[e]))) {
+            if (p.bf16) own_sum<__nv_bfloat16>(p, t.j0, t.n, static_cast<int>(row), m, &sum[e]);
+            else own_sum<__half>(p, t.j0, t.n, static_cast<int>(row), m, &sum[e]);
           }
           const int64_t o = row * p.out_stride + m;
           if (p.out_type == SPGEMM_DTYPE_F32) static_cast<float*>(p.out)[o] = sum[e];
@@ -1034,6 +1088,15 @@ bool launch_mma_adapted(const spgemm_dense& x, const spgemm_dense& w, const spge
   a.ids = ids;
   a.adapters = static_cast<int>(b.groups);
   a.rank = static_cast<int>(b.cols);
+  a.x = x.data;
+  a.x_stride = x.stride;
+  a.w = w.data;
+  a.w_stride = w.stride;
+  a.v = v.data;
+  a.v_stride = v.stride;
+  a.b = b.data;
+  a.b_stride = b.row_stride;
+  a.b_group = b.group_stride;
   a.early = 1;
   a.m = static_cast<int>(y.cols);
   a.depth = static_cast<int>(x.cols);

@@ -143,6 +143,35 @@ def test_adapters(gpu_lib, tokens, adapters, rank, d, n, mixed, shape, dtype):
     near(y, want, dtype, 1.01 * tol)
 
 
+@pytest.mark.parametrize("tokens,adapters,rank,d,n", [(600, 5, 24, 1096, 264), (61, 3, 16, 1096, 136)])
+@pytest.mark.parametrize("shape", ADAPTED)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_a_broken_adapter_reaches_its_own_rows_only(gpu_lib, tokens, adapters, rank, d, n, shape, dtype):
+    """Infinite and NaN values in an adapter that is used: rows of other adapters and of none stay what they are,
+    its own become what the formula says, whatever else is in their tile."""
+    import torch
+    ids = torch.tensor(np.random.default_rng(5).integers(-1, adapters, tokens).astype(np.int32)).cuda()
+    x, w = normal(1, tokens, d, dtype=dtype), normal(2, n, d, dtype=dtype, std=d ** -0.5)
+    a, b = normal(3, adapters, rank, d, dtype=dtype, std=d ** -0.5), normal(4, adapters, n, rank, dtype=dtype, std=0.3)
+    b[1, 7, 3], b[1, 20:40, 0], b[1, n - 1] = float("nan"), float("inf"), float("-inf")
+    x[tokens // 2] = float("nan")  # and a broken row
+    with forced(gpu_lib, *shape):
+        y = gpu_lib.adapted_product(x, w, a, b, ids)
+    gpu_lib.grouped_status()
+    xd, wd = x.double(), w.double()
+    want, tol = xd @ wd.t(), SUM * (d + rank) * (xd.abs() @ wd.abs().t())
+    for i in range(adapters):
+        t = (ids == i).nonzero()[:, 0]
+        v, mv = xd[t] @ a[i].double().t(), xd[t].abs() @ a[i].double().abs().t()
+        want[t] += v @ b[i].double().t()
+        tol[t] += (SUM * (d + rank) * mv + (U[dtype] + 2.0 ** -22) * v.abs() + TINY[dtype]) @ b[i].double().abs().t()
+    fine = torch.isfinite(want)
+    clean = (ids != 1) & (torch.arange(tokens, device="cuda") != tokens // 2)
+    assert fine[clean].all() and not fine[(ids == 1)][:, n - 1].any()
+    assert torch.equal(torch.isfinite(y), fine)
+    near(y[fine], want[fine], dtype, 1.01 * tol[fine])
+
+
 @pytest.mark.parametrize("shape", [(256, 1), (256, 0), (64, 0, 8), (64, 0, 2), (16, 0, 2)])
 def test_a_wait_that_runs_out_is_reported(gpu_lib, shape):
     """In the kernels of two blocks to a tile and of split depth too: the status says so, later calls are right."""
