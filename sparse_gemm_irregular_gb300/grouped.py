@@ -88,7 +88,7 @@ class Routing:
         sparse products.  Copies the number of entries to the host."""
         import torch
         from . import DeviceCSR
-        there = self.ids >= 0
+        there = self.position >= 0  # an id out of range has none
         row_ptr = torch.zeros(self.tokens + 1, dtype=torch.int64, device=self.ids.device)
         row_ptr[1:] = there.sum(1).cumsum(0)
         return DeviceCSR(self.tokens, self.groups, row_ptr, self.ids[there].contiguous(),

@@ -187,6 +187,20 @@ def test_strides_arrive_as_they_are():
         assert (w.row_stride, w.group_stride) == (want, 0)
 
 
+def test_sparse_matrices_of_a_routing_hold_no_id_out_of_range():
+    """An id outside its range counts as none in the grouping: as a column it would lead the product astray."""
+    import torch
+    ids = np.array([[0, 5], [2, -1], [-7, 1]], np.int32)
+    off, order, pos = transpose(np.where((ids < 3) & (ids >= 0), ids, -1), 3)
+    i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32)  # noqa: E731
+    r = sg.Routing._made(i32(ids), torch.arange(6.0).view(3, 2), i32(off), i32(order), i32(pos))
+    m = r.to_csr()
+    assert (m.rows, m.cols, m.nnz) == (3, 3, 3)
+    assert m.row_ptr.tolist() == [0, 1, 2, 3] and m.col.tolist() == [0, 2, 1] and m.val.tolist() == [0, 2, 5]
+    t = r.transposed_csr()
+    assert t.row_ptr.tolist() == [0, 1, 2, 3] and t.col.tolist() == [0, 2, 1] and t.val.tolist() == [0, 5, 2]
+
+
 # ---- the reference of the GPU tests, pinned by closed forms -------------------------------------
 def test_reference_route_closed_forms():
     ids, w, _ = route(np.array([[0.0, np.log(2.0), np.log(4.0), -np.inf]]), 2)
