@@ -498,7 +498,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_backward(const T* __restr
     __syncwarp();
 #pragma unroll
     for (int v = 0; v < V; ++v) d[v] = full[e0 + v];
-    if (r.renormalise) {  // w = s / sum: ds = (dw - sum of dw * w) / sum, over the chosen ones
+    // d becomes s times the gradient of the scores.  w = s / sum: s ds = w (dw - sum of dw w), over the chosen ones,
+    // formed without ds itself, which overflows where the scores are small.
+    if (r.renormalise) {
       float sum = 0.0f, mean = 0.0f;
       for (int j = 0; j < r.top_k; ++j) {
         const int e = there ? ids[t * r.top_k + j] : -1;
@@ -514,18 +516,21 @@ __global__ void __launch_bounds__(kWarps * 32) k_route_backward(const T* __restr
         if (((chosen >> v) & 1u) && sum > 0.0f) mean += d[v] * (s[v] / sum);
       mean = lanes_sum<L>(mean);
 #pragma unroll
-      for (int v = 0; v < V; ++v) d[v] = ((chosen >> v) & 1u) && sum > 0.0f ? (d[v] - mean) / sum : 0.0f;
+      for (int v = 0; v < V; ++v) d[v] = ((chosen >> v) & 1u) && sum > 0.0f ? s[v] / sum * (d[v] - mean) : 0.0f;
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] *= s[v];
     }
     float dot = 0.0f;
     if (r.score == SPGEMM_SCORE_SOFTMAX) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) dot += d[v] * s[v];
+      for (int v = 0; v < V; ++v) dot += d[v];
       dot = lanes_sum<L>(dot);
     }
     Piece<T, V> o;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      o.v[v] = from_f32<T>(r.score == SPGEMM_SCORE_SOFTMAX ? s[v] * (d[v] - dot) : d[v] * s[v] * (1.0f - s[v]));
+      o.v[v] = from_f32<T>(r.score == SPGEMM_SCORE_SOFTMAX ? d[v] - s[v] * dot : d[v] * (1.0f - s[v]));
     if (there) {
       if (out_pieces && e0 + V <= experts) {
         *reinterpret_cast<Piece<T, V>*>(out + t * out_stride + e0) = o;

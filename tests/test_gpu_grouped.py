@@ -181,6 +181,34 @@ def test_a_single_renormalised_choice_has_no_gradient(gpu_lib, score, dtype):
     assert torch.all(gpu_lib.route_backward(l, r, torch.randn(777, 1, device="cuda")) == 0)
 
 
+def test_gradient_where_the_chosen_scores_are_tiny(gpu_lib):
+    """Renormalised weights do not care how small the scores are, and neither do their gradients: the gradient of the
+    scores themselves, a weight's divided by their sum, is past the 32-bit range here."""
+    import torch
+    # sigmoid: every logit near -88, scores near 1e-38
+    l = (torch.rand(64, 16, generator=_gen(1)) * 2 - 88).float()
+    g = _normal(2, 64, 3, dtype="f32")
+    opt = dict(score="sigmoid", scale=50.0)
+    r = gpu_lib.route(l.cuda(), 3, **opt)
+    d = _np(gpu_lib.route_backward(l.cuda(), r, g.cuda()))
+    want = route_grad(l.double().numpy(), r.ids.cpu().numpy(), g.numpy(), "sigmoid", True, 50.0)
+    # terms of at most 50 |g|, a few roundings each; the scores, below 2^-126, keep 21 bits
+    assert np.abs(d - want).max() <= 50 * np.abs(g.numpy()).max() * 4 * 2.0 ** -20
+    # softmax: a bias prefers experts 86 below the best
+    l = torch.rand(64, 16, generator=_gen(3)).float() - 86
+    l[:, 0] = 0.0
+    bias = torch.full((16,), 2.0)
+    bias[0] = 0.0
+    opt = dict(score="softmax", scale=100.0)
+    r = gpu_lib.route(l.cuda(), 3, bias=bias.cuda(), **opt)
+    ids = r.ids.cpu().numpy()
+    assert (ids > 0).all()
+    d = _np(gpu_lib.route_backward(l.cuda(), r, g.cuda()))
+    want = route_grad(l.double().numpy(), ids, g.numpy(), "softmax", True, 100.0)
+    # exp of -86 in 32 bits is 8 spacings off at most
+    assert np.abs(d - want).max() <= 100 * np.abs(g.numpy()).max() * 4 * 2.0 ** -20
+
+
 def test_route_empty_batch(gpu_lib):
     import torch
     r = gpu_lib.route(torch.empty(0, 16, device="cuda"), 2)
