@@ -77,13 +77,23 @@ __global__ void __launch_bounds__(kThreads) k_combine(const int32_t* __restrict_
 // bf16 to 65536: 48 us, 335 MB at 7.0 TB/s (the writes end in L2).
 __global__ void __launch_bounds__(kThreads) k_spread_rows(const int32_t* __restrict__ position, int64_t tokens, int top_k,
                                                           int64_t slots, const uint4* __restrict__ x, int64_t x_stride,
-                                                          uint4* __restrict__ out, int64_t out_stride, int per) {
+                                                          uint4* __restrict__ out, int64_t out_stride, int per, int rest) {
   pdl_wait();
   pdl_go();
   const int c = blockIdx.y * kThreads + threadIdx.x;
   if (c >= per) return;
   for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
-    const uint4 v = x[t * x_stride + c];
+    uint4 v;
+    if (rest == 0 || c + 1 < per) {
+      v = x[t * x_stride + c];
+    } else {  // `rest` elements: the matrix may end with them
+      const uint16_t* from = reinterpret_cast<const uint16_t*>(x + t * x_stride + c);
+      uint32_t word[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < rest) word[e / 2] |= static_cast<uint32_t>(from[e]) << (e % 2 * 16);
+      v = make_uint4(word[0], word[1], word[2], word[3]);
+    }
     for (int j = 0; j < top_k; ++j) {
       const int64_t p = position[t * top_k + j];
       if (p >= 0 && p < slots) out[p * out_stride + c] = v;
@@ -160,10 +170,10 @@ void launch_combine(const spgemm_grouping& g, const float* weights, const spgemm
 
 void launch_spread_rows(const spgemm_grouping& g, const spgemm_dense& x, const spgemm_dense& out, cudaStream_t s) {
   if (g.slots == 0) return;
-  const int per = static_cast<int>(ceil_div(x.cols, 8));  // strides are multiples of 8: a row's last 16 bytes are its own
+  const int per = static_cast<int>(ceil_div(x.cols, 8));
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(x.rows, 1 << 20)), static_cast<unsigned>(ceil_div(per, kThreads)));
   launch_next(k_spread_rows, grid, kThreads, 0, s, g.position, x.rows, g.top_k, g.slots, static_cast<const uint4*>(x.data),
-              x.stride / 8, static_cast<uint4*>(out.data), out.stride / 8, per);
+              x.stride / 8, static_cast<uint4*>(out.data), out.stride / 8, per, static_cast<int>(x.cols % 8));
 }
 
 void launch_combine_backward(const spgemm_grouping& g, const float* weights, const spgemm_dense& dout,

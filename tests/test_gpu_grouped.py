@@ -383,6 +383,25 @@ def test_product_strides_and_streams(gpu_lib):
         assert np.all(np.abs(_np(y) - want) <= rounding("bf16", want) + SUM * 128 * mag)
 
 
+@pytest.mark.parametrize("d", [117, 120, 121, 3, 8])
+def test_rows_that_end_with_the_storage(gpu_lib, d):
+    """The last row has no padding behind it (its 16-byte pieces may not be read whole), others have NaN."""
+    import torch
+    ids = _random_ids(8, 700, 3, 2)
+    r = _routing(gpu_lib, ids, 3)
+    stride = (d + 7) // 8 * 8 + 8
+    flat = torch.full((699 * stride + d,), float("nan"), dtype=torch.bfloat16).cuda()
+    x = flat.as_strided((700, d), (stride, 1))
+    dense = _normal(1, 700, d).cuda()
+    x.copy_(dense)
+    w, dy = _normal(2, 3, 40, (d + 7) // 8 * 8).cuda()[:, :, :d], _normal(3, 1400, 40).cuda()
+    assert torch.equal(gpu_lib.expert_product(x, w, r), gpu_lib.expert_product(dense, w, r))
+    got, want = gpu_lib.expert_product_backward(dy, x, w, r), gpu_lib.expert_product_backward(dy, dense.clone(), w, r)
+    near = lambda a, b: ((a.double() - b.double()).abs() <= 2 * U["bf16"] * b.double().abs() + 1e-4).all()  # noqa: E731
+    assert near(got[0], want[0]) and near(got[1], want[1])
+    gpu_lib.grouped_status()
+
+
 def _busy(torch):
     """Some tens of milliseconds of ordinary work on the current stream."""
     a = torch.ones(8192, 8192, device="cuda", dtype=torch.bfloat16)
