@@ -342,7 +342,11 @@ def adapted_product(x, w, a, b, ids, scale=None, *, stream=None):
 
 
 def grouped_status(stream=None):
-    """Synchronise and raise SpgemmError if a device-side check of the calls above failed."""
+    """Synchronise and raise SpgemmError if a device-side check of the calls above failed on the stream's device.
+
+    Without a stream: the current one.  A call whose wait expired hands back meaningless values and says so only here:
+    ask before results are handed on (after a training step, at the end of a request)."""
     import torch
-    s = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
-    binding.spgemm_grouped_status(s)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    with torch.cuda.device(s.device):
+        binding.spgemm_grouped_status(s.cuda_stream)

@@ -201,6 +201,28 @@ def test_sparse_matrices_of_a_routing_hold_no_id_out_of_range():
     assert t.row_ptr.tolist() == [0, 1, 2, 3] and t.col.tolist() == [0, 2, 1] and t.val.tolist() == [0, 5, 2]
 
 
+def test_status_is_read_on_the_device_of_its_stream(monkeypatch):
+    """Each device has a status word: the call looks at the stream's, not at the current one's."""
+    import contextlib
+    import types
+
+    import torch
+    at, seen = ["cuda:0"], []
+
+    @contextlib.contextmanager
+    def device(d):
+        at.append(d)
+        yield
+        at.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(device="cuda:0", cuda_stream=7))
+    monkeypatch.setattr(b, "spgemm_grouped_status", lambda s=0: seen.append((at[-1], s)))
+    sg.grouped_status(types.SimpleNamespace(device="cuda:1", cuda_stream=9))
+    sg.grouped_status()
+    assert seen == [("cuda:1", 9), ("cuda:0", 7)]
+
+
 # ---- the reference of the GPU tests, pinned by closed forms -------------------------------------
 def test_reference_route_closed_forms():
     ids, w, _ = route(np.array([[0.0, np.log(2.0), np.log(4.0), -np.inf]]), 2)
