@@ -476,8 +476,10 @@ int spgemm_adapted_product(const spgemm_dense* x, const spgemm_dense* w, const s
                            const spgemm_weights* b, const int32_t* ids, const float* scale, const spgemm_dense* y,
                            void* stream);
 
-/* Synchronises `stream`, then reads and clears the device's status word of the calls above:
- * SPGEMM_OK, or SPGEMM_ERR_DEVICE when a device-side check failed since the last call. */
+/* Synchronises `stream`, then reads and clears (in one step) the current device's status word of the calls
+ * above: SPGEMM_OK, or SPGEMM_ERR_DEVICE when a device-side check failed since the last call.  The results of the
+ * calls since then are not to be used: nothing else tells of it, so a program asks before it hands results on (after a
+ * training step, at the end of a request), not after every call. */
 int spgemm_grouped_status(void* stream);
 
 /* For tests: polls > 0 limits every wait inside the tensor-core kernels of later calls of this thread

@@ -26,6 +26,9 @@ uint32_t* grouped_err() {
   return p;
 }
 
+// Reads and clears the word in one step: what another stream sets meanwhile is in this answer or in the next.
+static __global__ void k_take_error(uint32_t* word, uint32_t* out) { *out = atomicExch(word, 0u); }
+
 namespace {
 
 constexpr int64_t kMaxSlots = (int64_t(1) << 31) - (1 << 20);  // positions and tile ends stay 32-bit
@@ -372,11 +375,16 @@ int spgemm_grouped_status(void* stream) {
   uint32_t* p = grouped_err();
   if (!p) return check_cuda(cudaErrorInvalidSymbol, "grouped status");
   uint32_t err = 0;
-  SG_TRY(check_cuda(cudaMemcpyAsync(&err, p, sizeof(err), cudaMemcpyDeviceToHost, st), "grouped status"));
-  SG_TRY(check_cuda(cudaStreamSynchronize(st), "grouped status"));
+  {
+    Scratch scratch(st, {sizeof(err)});
+    if (!scratch.ok()) return SPGEMM_ERR_OUT_OF_MEMORY;
+    note_launch();
+    k_take_error<<<1, 1, 0, st>>>(p, scratch.part<uint32_t>(0));
+    SG_TRY(check_cuda(cudaGetLastError(), "grouped status"));
+    SG_TRY(check_cuda(cudaMemcpyAsync(&err, scratch.part(0), sizeof(err), cudaMemcpyDeviceToHost, st), "grouped status"));
+    SG_TRY(check_cuda(cudaStreamSynchronize(st), "grouped status"));
+  }
   if (!err) return SPGEMM_OK;
-  SG_TRY(check_cuda(cudaMemsetAsync(p, 0, sizeof(err), st), "grouped status"));
-  SG_TRY(check_cuda(cudaStreamSynchronize(st), "grouped status"));
   if (err & kErrTimeout) set_last_error("a wait expired (sites " + std::to_string(err >> 8) + ")");
   else set_last_error("an id is outside its range");
   return SPGEMM_ERR_DEVICE;

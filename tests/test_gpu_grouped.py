@@ -241,6 +241,23 @@ def test_group_rows_out_of_range_ids_are_reported(gpu_lib):
     gpu_lib.grouped_status()  # reading clears it
 
 
+def test_status_of_a_side_stream(gpu_lib):
+    """An error set on one stream is told once, on whichever stream of the device asks next."""
+    import torch
+    side = torch.cuda.Stream()
+    ids = torch.tensor([[0], [9]], dtype=torch.int32).cuda()
+    torch.cuda.synchronize()
+    gpu_lib.group_rows(ids, 3, stream=side)
+    with pytest.raises(gpu_lib.SpgemmError):
+        gpu_lib.grouped_status(side)
+    gpu_lib.grouped_status()
+    gpu_lib.group_rows(ids, 3)
+    torch.cuda.synchronize()
+    with pytest.raises(gpu_lib.SpgemmError, match="range"):
+        gpu_lib.grouped_status(side)
+    gpu_lib.grouped_status(side)
+
+
 # ---- products --------------------------------------------------------------------------------
 # tokens, groups, top_k, d, n: one token; a group longer than a tile; empty groups; sizes that end
 # inside every tile; rows that do not start on 16 bytes (odd d, odd n)
