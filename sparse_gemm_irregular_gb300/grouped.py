@@ -55,6 +55,7 @@ class Routing:
                                  % (name, "float32" if name == "weights" else "int32"))
             if t.numel() != n and name != "offsets":
                 raise ValueError("routing: ids, weights, order and position want tokens * top_k entries each")
+        _same_device("routing", self.ids, self.weights, self.offsets, self.order, self.position)
         if self.ids.dim() != 2 or self.offsets.dim() != 1:
             raise ValueError("ids: (tokens, top_k) and offsets: (groups + 1) are wanted")
 
@@ -70,6 +71,10 @@ class Routing:
         tokens, k = self.ids.shape
         return _pack_grouping(tokens * k, k, self.offsets.shape[0] - 1, self.offsets.data_ptr(), self.order.data_ptr(),
                               self.position.data_ptr())
+
+    @property
+    def device(self):
+        return self.ids.device
 
     @property
     def tokens(self) -> int:
@@ -154,6 +159,14 @@ def _weights(t, name: str) -> bytes:
 _entry: dict = {}  # entry points by name
 
 
+def _same_device(name: str, first, *others):
+    """Refuses tensors (and routings, None left out) of different devices: a kernel follows their addresses on one."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError("%s: tensors on %s and on %s" % (name, dev, t.device))
+
+
 def _on_stream(fn):
     """Gives a call its ``stream`` argument: everything that it allocates, fills and launches belongs there."""
     @functools.wraps(fn)
@@ -201,6 +214,7 @@ def route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int 
     experts form ``groups`` equal runs of which the ``groups_kept`` best ("max": by their best
     expert, "top2": by the sum of their two best) take part.  See spgemm_route."""
     import torch
+    _same_device("route", logits, bias)
     d = _dense(logits, "logits")
     if score not in _SCORES or group_score not in _GROUP_SCORES:
         raise ValueError("score: softmax or sigmoid; group_score: max or top2")
@@ -225,6 +239,7 @@ def route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int 
 def route_backward(logits, routing: Routing, grad_weights, *, stream=None):
     """Gradient of the logits for a gradient of ``routing.weights`` (see spgemm_route_backward)."""
     import torch
+    _same_device("route_backward", logits, routing, grad_weights)
     if routing.rule is None:
         raise ValueError("route_backward: the routing does not come from route()")
     d = _dense(logits, "logits")
@@ -242,6 +257,7 @@ def group_rows(ids, groups: int, *, weights=None, stream=None) -> Routing:
     """The Routing of given ids (tokens, top_k) or (tokens,) int32, -1 for none; weights default to
     ones (see spgemm_group_rows)."""
     import torch
+    _same_device("group_rows", ids, weights)
     _want(ids, "ids", torch.int32)
     ids = ids if ids.dim() == 2 else ids[:, None]
     dev = ids.device
@@ -265,6 +281,7 @@ def expert_product(x, w, routing: Routing, *, grouped: bool = False, out_dtype=N
     x (tokens, d), or (slots, d) in group order with ``grouped``; w (groups, n, d).  See
     spgemm_grouped_product."""
     import torch
+    _same_device("expert_product", x, w, routing)
     g = routing._grouping
     dx, dw = _dense(x, "x"), _weights(w, "w")
     y = torch.empty((routing.ids.numel(), w.shape[1]), dtype=out_dtype or x.dtype, device=x.device)
@@ -276,6 +293,7 @@ def expert_product(x, w, routing: Routing, *, grouped: bool = False, out_dtype=N
 def expert_product_backward(dy, x, w, routing: Routing, *, need_dx: bool = True, need_dw: bool = True, stream=None):
     """(dx, dw) of ``expert_product`` with one row of x per token (see spgemm_grouped_product_backward)."""
     import torch
+    _same_device("expert_product_backward", x, dy, w, routing)
     g = routing._grouping
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
     dw = torch.empty(w.shape, dtype=w.dtype, device=x.device) if need_dw else None
@@ -289,6 +307,7 @@ def expert_product_backward(dy, x, w, routing: Routing, *, need_dx: bool = True,
 def combine(y, routing: Routing, *, out_dtype=None, stream=None):
     """Weighted sum of a token's rows: (tokens, y.shape[1]) (see spgemm_combine)."""
     import torch
+    _same_device("combine", y, routing)
     g = routing._grouping
     out = torch.empty((routing.tokens, y.shape[1]), dtype=out_dtype or y.dtype, device=y.device)
     _call("spgemm_combine", y.device, g, routing.weights.data_ptr(), _dense(y, "y"),
@@ -300,6 +319,7 @@ def combine(y, routing: Routing, *, out_dtype=None, stream=None):
 def combine_backward(dout, y, routing: Routing, *, stream=None):
     """(dy, dweights) of ``combine``; dy has dout's type, y may have another (see spgemm_combine_backward)."""
     import torch
+    _same_device("combine_backward", y, dout, routing)
     g = routing._grouping
     dy = torch.empty(y.shape, dtype=dout.dtype, device=y.device)
     dweights = torch.empty(routing.ids.shape, dtype=torch.float32, device=y.device)
@@ -313,6 +333,7 @@ def experts(x, w_up, w_down, routing: Routing, *, stream=None):
     """A gated expert layer, (tokens, d) -> (tokens, w_down.shape[1]): w_up (groups, 2 * hidden, d)
     holds the gate's rows, then up's; w_down (groups, n, hidden).  See spgemm_experts."""
     import torch
+    _same_device("experts", x, w_up, w_down, routing)
     g = routing._grouping
     out = torch.empty((x.shape[0], w_down.shape[1]), dtype=x.dtype, device=x.device)
     _call("spgemm_experts", x.device, g, routing.weights.data_ptr(), _dense(x, "x"),
@@ -327,6 +348,7 @@ def adapted_product(x, w, a, b, ids, scale=None, *, stream=None):
     x (tokens, d), w (n, d), a (adapters, rank, d), b (adapters, n, rank), scale (adapters)
     float32.  See spgemm_adapted_product."""
     import torch
+    _same_device("adapted_product", x, w, a, b, ids, scale)
     _want(ids, "ids", torch.int32)
     if ids.numel() != x.shape[0]:
         raise ValueError("ids: one per row of x is wanted")

@@ -201,6 +201,31 @@ def test_sparse_matrices_of_a_routing_hold_no_id_out_of_range():
     assert t.row_ptr.tolist() == [0, 1, 2, 3] and t.col.tolist() == [0, 2, 1] and t.val.tolist() == [0, 5, 2]
 
 
+def test_tensors_of_different_devices_are_refused():
+    """Every tensor of every call, before anything is allocated or launched."""
+    import types
+    here, there = (types.SimpleNamespace(device="cuda:%d" % i) for i in range(2))
+    routing = lambda on: sg.Routing._made(on, on, on, on, on, rule=b"")  # noqa: E731
+    calls = {
+        sg.route: ([here, 2], dict(bias=here)), sg.route_backward: ([here, routing(here), here], {}),
+        sg.group_rows: ([here, 2], dict(weights=here)), sg.expert_product: ([here, here, routing(here)], {}),
+        sg.expert_product_backward: ([here, here, here, routing(here)], {}), sg.combine: ([here, routing(here)], {}),
+        sg.combine_backward: ([here, here, routing(here)], {}), sg.experts: ([here, here, here, routing(here)], {}),
+        sg.adapted_product: ([here, here, here, here, here, here], {})}
+    for fn, (args, kw) in calls.items():
+        for i in range(len(args)):
+            if isinstance(args[i], int):
+                continue
+            bad = list(args)
+            bad[i] = routing(there) if isinstance(args[i], sg.Routing) else there
+            if len(args) - sum(isinstance(a, int) for a in args) + len(kw) > 1:
+                with pytest.raises(ValueError, match="cuda:0.*cuda:1|cuda:1.*cuda:0"):
+                    fn(*bad, **kw)
+        for name in kw:
+            with pytest.raises(ValueError, match="cuda:1"):
+                fn(*args, **{name: there})
+
+
 def test_status_is_read_on_the_device_of_its_stream(monkeypatch):
     """Each device has a status word: the call looks at the stream's, not at the current one's."""
     import contextlib
