@@ -447,7 +447,8 @@ int spgemm_grouped_product(const spgemm_grouping* g, const spgemm_dense* x, int3
 
 /* Gradients of spgemm_grouped_product with one row of x per token: dx[t, :] = sum over the
  * token's slots of dy[position, :] * w[g], dw[g] = sum over the group's positions of dy[p, :]^T
- * x[row(p), :] (zero for an empty group).  dx or dw may be NULL. */
+ * x[row(p), :] (zero for an empty group).  dx or dw may be NULL.  The groups of w may share storage (a stride of
+ * 0: one matrix for all), those of dw may not. */
 int spgemm_grouped_product_backward(const spgemm_grouping* g, const spgemm_dense* dy, const spgemm_dense* x,
                                     const spgemm_weights* w, const spgemm_dense* dx, const spgemm_weights* dw,
                                     void* stream);

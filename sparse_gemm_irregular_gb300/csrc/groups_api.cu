@@ -229,6 +229,8 @@ int spgemm_grouped_product_backward(const spgemm_grouping* g, const spgemm_dense
   if (dx && (dx->rows != x->rows || dx->cols != x->cols)) return bad("grouped product backward: shape of dx");
   if (dw && (dw->groups != w->groups || dw->rows != w->rows || dw->cols != w->cols))
     return bad("grouped product backward: shape of dw");
+  if (dw && dw->groups > 1 && dw->group_stride < (dw->rows - 1) * dw->row_stride + dw->cols)
+    return bad("grouped product backward: groups of dw overlap");
   if (w->dtype != x->dtype || dy->dtype != x->dtype || (dx && dx->dtype != x->dtype) || (dw && dw->dtype != x->dtype))
     return bad("grouped product backward: types differ");
   cudaStream_t st = static_cast<cudaStream_t>(stream);

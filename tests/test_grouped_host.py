@@ -130,6 +130,16 @@ def test_products_refuse():
         assert back(**kw) == -1, kw
 
 
+def test_gradients_of_groups_may_not_share_storage():
+    lib = sg.load()
+    g, x, w, dy = grouping(8, 2, 3), dense(4, 16), weights(3, 24, 16), dense(8, 24)
+    for stride in (0, 16, 24 * 16 - 1):
+        dw = weights(3, 24, 16)
+        dw.group_stride = stride
+        assert lib.spgemm_grouped_product_backward(R(g), R(dy), R(x), R(w), None, R(dw), None) == -1
+        assert "overlap" in sg.spgemm_last_error()
+
+
 def test_layers_refuse():
     lib = sg.load()
     g, x, up, down, out = grouping(8, 2, 3), dense(4, 16), weights(3, 48, 16), weights(3, 40, 24), dense(4, 40)
