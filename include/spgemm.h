@@ -466,13 +466,16 @@ int spgemm_combine_backward(const spgemm_grouping* g, const float* weights, cons
 
 /* A gated expert layer: out[t, :] = sum over the token's slots of weights[slot] * h(slot) *
  * w_down[g]^T with h = silu(x[t] * gate[g]^T) * (x[t] * up[g]^T); w_up[g] holds the gate's hidden
- * rows, then up's.  The hidden row of a slot is held in x's type, everything else in 32 bits. */
+ * rows, then up's.  The hidden row of a slot is held in x's type, everything else in 32 bits: in f16 a hidden value
+ * past 65504 is infinite, and so is what it reaches in out. */
 int spgemm_experts(const spgemm_grouping* g, const float* weights, const spgemm_dense* x,
                    const spgemm_weights* w_up, const spgemm_weights* w_down, const spgemm_dense* out, void* stream);
 
 /* A projection with a low-rank adapter per row: y[t, :] = x[t] * w^T + scale[i] * (x[t] * a[i]^T) *
  * b[i]^T with i = ids[t]; -1: the projection alone.  a: adapters x rank x x.cols, b: adapters x
- * y.cols x rank, scale: one 32-bit factor per adapter, or NULL for ones. */
+ * y.cols x rank, scale: one 32-bit factor per adapter, or NULL for ones.  On the tensor cores the row between the
+ * two small products, scale[i] * (x[t] * a[i]^T), is held in x's type (in f16 infinite past 65504), on the CUDA cores,
+ * where rows of an operand do not start on 16 bytes, in 32 bits like everything else. */
 int spgemm_adapted_product(const spgemm_dense* x, const spgemm_dense* w, const spgemm_weights* a,
                            const spgemm_weights* b, const int32_t* ids, const float* scale, const spgemm_dense* y,
                            void* stream);

@@ -669,6 +669,46 @@ def test_no_wait_runs_out_over_many_calls(gpu_lib, tokens, groups, top_k, d, hid
     gpu_lib.grouped_status()
 
 
+@pytest.mark.parametrize("hidden", [8, 9])  # on the tensor cores, on the CUDA cores
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_range_of_the_hidden_row(gpu_lib, hidden, dtype):
+    """It is held in x's type: in f16 a value past 65504 is infinite and reaches out, in bf16 it is not."""
+    import torch
+    ids = np.zeros((20, 1), np.int32)
+    r = _routing(gpu_lib, ids, 1)
+    x = torch.ones(20, 16, dtype=_t(dtype))
+    x[::2] *= 0.875
+    up = torch.zeros(1, 2 * hidden, 16, dtype=_t(dtype))
+    up[:, :hidden] = 4.0  # gate 64 (56): silu(64) = 64
+    up[:, hidden:] = 70.0  # up 1120 (980): hidden value 71680 (54880)
+    down = torch.full((1, 24, hidden), 2.0 ** -6, dtype=_t(dtype))
+    out = _np(gpu_lib.experts(x.cuda(), up.cuda(), down.cuda(), r))
+    want = np.where(np.arange(20) % 2 == 0, 54880.0, 71680.0)[:, None] * hidden / 64
+    loud = np.abs(want) * 64 / hidden > 65504
+    if dtype == "f16":
+        assert np.all(np.isinf(out[loud[:, 0]]))
+        want, out = want[~loud[:, 0]], out[~loud[:, 0]]
+    assert np.all(np.abs(out - want) <= 2.02 * U[dtype] * want)  # roundings of the hidden value and of out
+
+
+@pytest.mark.parametrize("rank", [8, 7])  # on the tensor cores, on the CUDA cores
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_range_of_the_row_between_an_adapters_products(gpu_lib, rank, dtype):
+    """On the tensor cores it is held in x's type (f16: infinite past 65504), on the CUDA cores in 32 bits."""
+    import torch
+    ids = torch.arange(20, dtype=torch.int32) % 2
+    x, w = torch.ones(20, 64, dtype=_t(dtype)), torch.ones(24, 64, dtype=_t(dtype))
+    a = torch.full((2, rank, 64), 1100.0, dtype=_t(dtype))  # 70400, in bf16 from 1104: 70656
+    a[1] = 500.0
+    b = torch.full((2, 24, rank), 2.0 ** -4, dtype=_t(dtype))
+    y = _np(gpu_lib.adapted_product(x.cuda(), w.cuda(), a.cuda(), b.cuda(), ids.cuda()))
+    want = 64 + np.where(np.arange(20) % 2 == 0, 64 * float(a[0, 0, 0]), 32000.0)[:, None] * rank / 16
+    if dtype == "f16" and rank == 8:
+        assert np.all(np.isinf(y[::2]))
+        want, y = want[1::2], y[1::2]
+    assert np.all(np.abs(y - want) <= 2.02 * U[dtype] * want)
+
+
 # ---- adapters ------------------------------------------------------------------------------------
 @pytest.mark.parametrize("tokens,adapters,rank,d,n", [
     (1, 1, 8, 64, 64), (1, 3, 16, 128, 72), (5, 2, 8, 40, 136), (64, 48, 16, 256, 264), (300, 3, 64, 512, 128),
