@@ -772,6 +772,50 @@ def test_results_repeat_bit_for_bit(gpu_lib):
         assert all(torch.equal(a, b) for a, b in zip(first, now))
 
 
+@pytest.mark.parametrize("tokens", [6, 700])
+def test_calls_replay_as_a_graph(gpu_lib, tokens):
+    """A layer of all calls, captured and replayed on new inputs: the bits of the direct calls, again and again."""
+    import torch
+    experts, top_k, d, hidden = 12, 3, 256, 128
+    w_in, a, b = _normal(1, d, d, std=1 / 16).cuda(), _normal(2, 4, 16, d, std=1 / 16).cuda(), _normal(3, 4, d, 16).cuda()
+    scale, bias = torch.rand(4, generator=_gen(4)).cuda(), torch.zeros(experts).cuda()
+    router = _normal(5, experts, d, std=1 / 16).cuda()
+    up, down = _normal(6, experts, 2 * hidden, d, std=1 / 16).cuda(), _normal(7, experts, d, hidden, std=1 / 11).cuda()
+    w = _normal(8, experts, d, d, std=1 / 16).cuda()
+
+    def layer(x, which):
+        h = gpu_lib.adapted_product(x, w_in, a, b, which, scale)
+        l = (h @ router.t()).float()
+        r = gpu_lib.route(l, top_k, bias=bias, score="sigmoid", groups=4, groups_kept=2, group_score="top2")
+        out = gpu_lib.experts(h, up, down, r)
+        y = gpu_lib.expert_product(h, w, r)
+        s = gpu_lib.combine(y, r)
+        dy, dweights = gpu_lib.combine_backward(out, y, r)
+        dx, dw = gpu_lib.expert_product_backward(dy, h, w, r)
+        dl = gpu_lib.route_backward(l, r, dweights)
+        again = gpu_lib.group_rows(r.ids, experts)
+        return [h, r.ids, r.weights, r.order, out, y, s, dy, dweights, dx, dw, dl, again.position]
+
+    x, which = _normal(9, tokens, d).cuda(), torch.randint(-1, 4, (tokens,), generator=_gen(10)).int().cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer(x, which)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = layer(x, which)
+    for seed in (11, 12, 11):
+        x.copy_(_normal(seed, tokens, d))
+        which.copy_(torch.randint(-1, 4, (tokens,), generator=_gen(seed)).int())
+        for _ in range(3):
+            g.replay()
+        got = [t.clone() for t in held]
+        want = layer(x, which)
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+    gpu_lib.grouped_status()
+
+
 def test_routing_as_sparse_matrices(gpu_lib):
     """The choice and its transpose as CSR, multiplied by the library's SpGEMM: how often two experts
     serve the same token."""
