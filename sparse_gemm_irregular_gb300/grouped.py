@@ -8,6 +8,9 @@ current stream and do not synchronise.  ``Routing`` is the choice together with 
 A call with ``stream=`` is the call with that stream current: its outputs belong to that stream, its inputs'
 memory is not handed out again before the stream has passed it.  What the inputs still wait for on other
 streams, and who reads the outputs on others, is the caller's to order, as everywhere in PyTorch.
+
+The calls take no part in autograd: gradients are formed by the calls whose names end in ``_backward``.  An output
+of inputs that want a gradient raises when one is asked of it.
 """
 from __future__ import annotations
 
@@ -167,23 +170,69 @@ def _same_device(name: str, first, *others):
             raise ValueError("%s: tensors on %s and on %s" % (name, dev, t.device))
 
 
-def _on_stream(fn):
-    """Gives a call its ``stream`` argument: everything that it allocates, fills and launches belongs there."""
+def _used(args, kw) -> list:
+    """The tensors of a call, those of its routing among them."""
+    found = []
+    for a in (*args, *kw.values()):
+        if isinstance(a, Routing):
+            found += (a.ids, a.weights, a.offsets, a.order, a.position)
+        elif hasattr(a, "requires_grad"):
+            found.append(a)
+    return found
+
+
+_stop = None  # made on first use (the package imports without torch)
+
+
+def _without_graph(name: str, out, used):
+    """`out`, with a node in the graph that says that there is no way back through `name`."""
+    import torch
+    global _stop
+    if _stop is None:
+        class Stop(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, name, t, *used):
+                ctx.call = name
+                return t.view_as(t)
+
+            @staticmethod
+            def backward(ctx, *_):
+                raise RuntimeError("%s takes no part in autograd: form its gradient with the call of that name that ends in "
+                                   "_backward, or detach() its inputs" % ctx.call)
+        _stop = Stop
+
+    def stop(t):
+        return _stop.apply(name, t, *used) if t is not None and t.is_floating_point() else t
+
+    if isinstance(out, Routing):
+        return Routing._made(out.ids, stop(out.weights), out.offsets, out.order, out.position, out.rule)
+    return tuple(map(stop, out)) if isinstance(out, tuple) else stop(out)
+
+
+def _entry_point(fn):
+    """Gives a call its ``stream`` argument (everything that it allocates, fills and launches belongs there), and an
+    end to the graph that tells of itself where an input wants a gradient."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
         import torch
-        used = [t for a in (*args, *kw.values()) for t in
-                ((a.ids, a.weights, a.offsets, a.order, a.position) if isinstance(a, Routing) else (a,))
-                if isinstance(t, torch.Tensor)]
-        for t in used:
-            if t.device != stream.device:
-                raise ValueError("stream: on %s, a tensor on %s" % (stream.device, t.device))
-        with torch.cuda.stream(stream):
+        grad = torch.is_grad_enabled()
+        if stream is None and not grad:
+            return fn(*args, **kw)
+        used = _used(args, kw)
+        if stream is None:
             out = fn(*args, **kw)
-        for t in used:
-            t.record_stream(stream)
+        else:
+            for t in used:
+                if t.device != stream.device:
+                    raise ValueError("stream: on %s, a tensor on %s" % (stream.device, t.device))
+            with torch.cuda.stream(stream):
+                out = fn(*args, **kw)
+            for t in used:
+                t.record_stream(stream)
+        if grad:
+            for t in used:
+                if t.requires_grad:
+                    return _without_graph(fn.__name__, out, used)
         return out
     return call
 
@@ -205,7 +254,7 @@ def _call(name: str, device, *args):
         _check(rc, name)
 
 
-@_on_stream
+@_entry_point
 def route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int = 1, groups_kept: int = 1,
           group_score: str = "max", renormalise: bool = True, scale: float = 1.0, stream=None) -> Routing:
     """Choose ``top_k`` experts per token from router logits (tokens, experts).
@@ -235,7 +284,7 @@ def route(logits, top_k: int, *, bias=None, score: str = "softmax", groups: int 
     return Routing._made(ids, weights, offsets, order, position, rule)
 
 
-@_on_stream
+@_entry_point
 def route_backward(logits, routing: Routing, grad_weights, *, stream=None):
     """Gradient of the logits for a gradient of ``routing.weights`` (see spgemm_route_backward)."""
     import torch
@@ -252,7 +301,7 @@ def route_backward(logits, routing: Routing, grad_weights, *, stream=None):
     return out
 
 
-@_on_stream
+@_entry_point
 def group_rows(ids, groups: int, *, weights=None, stream=None) -> Routing:
     """The Routing of given ids (tokens, top_k) or (tokens,) int32, -1 for none; weights default to
     ones (see spgemm_group_rows)."""
@@ -274,7 +323,7 @@ def group_rows(ids, groups: int, *, weights=None, stream=None) -> Routing:
     return Routing._made(ids, weights, offsets, order, position)
 
 
-@_on_stream
+@_entry_point
 def expert_product(x, w, routing: Routing, *, grouped: bool = False, out_dtype=None, stream=None):
     """Rows times the matrix of their group: (slots, w.shape[1]) in group order.
 
@@ -289,7 +338,7 @@ def expert_product(x, w, routing: Routing, *, grouped: bool = False, out_dtype=N
     return y
 
 
-@_on_stream
+@_entry_point
 def expert_product_backward(dy, x, w, routing: Routing, *, need_dx: bool = True, need_dw: bool = True, stream=None):
     """(dx, dw) of ``expert_product`` with one row of x per token (see spgemm_grouped_product_backward)."""
     import torch
@@ -303,7 +352,7 @@ def expert_product_backward(dy, x, w, routing: Routing, *, need_dx: bool = True,
     return dx, dw
 
 
-@_on_stream
+@_entry_point
 def combine(y, routing: Routing, *, out_dtype=None, stream=None):
     """Weighted sum of a token's rows: (tokens, y.shape[1]) (see spgemm_combine)."""
     import torch
@@ -315,7 +364,7 @@ def combine(y, routing: Routing, *, out_dtype=None, stream=None):
     return out
 
 
-@_on_stream
+@_entry_point
 def combine_backward(dout, y, routing: Routing, *, stream=None):
     """(dy, dweights) of ``combine``; dy has dout's type, y may have another (see spgemm_combine_backward)."""
     import torch
@@ -328,7 +377,7 @@ def combine_backward(dout, y, routing: Routing, *, stream=None):
     return dy, dweights
 
 
-@_on_stream
+@_entry_point
 def experts(x, w_up, w_down, routing: Routing, *, stream=None):
     """A gated expert layer, (tokens, d) -> (tokens, w_down.shape[1]): w_up (groups, 2 * hidden, d)
     holds the gate's rows, then up's; w_down (groups, n, hidden).  See spgemm_experts."""
@@ -341,7 +390,7 @@ def experts(x, w_up, w_down, routing: Routing, *, stream=None):
     return out
 
 
-@_on_stream
+@_entry_point
 def adapted_product(x, w, a, b, ids, scale=None, *, stream=None):
     """x w^T + scale[i] (x a[i]^T) b[i]^T with i = ids[token] (int32; -1: the projection alone).
 

@@ -816,6 +816,32 @@ def test_calls_replay_as_a_graph(gpu_lib, tokens):
     gpu_lib.grouped_status()
 
 
+def test_no_silent_end_of_a_graph(gpu_lib):
+    """An input that wants a gradient does not lose it without a word."""
+    import torch
+    l = _normal(1, 6, 8, dtype="f32").cuda().requires_grad_()
+    r = gpu_lib.route(l, 2)
+    x, w = _normal(2, 6, 16).cuda().requires_grad_(), _normal(3, 8, 24, 16).cuda()
+    up, down = _normal(6, 8, 48, 16).cuda(), _normal(7, 8, 24, 24).cuda()
+    a, b = _normal(8, 3, 4, 16).cuda(), _normal(9, 3, 24, 4).cuda().requires_grad_()
+    which = torch.zeros(6, dtype=torch.int32, device="cuda")
+    plain = gpu_lib.route(l.detach(), 2)
+    y = gpu_lib.expert_product(x, w, plain)
+    for name, out in (("route", r.weights), ("expert_product", y), ("combine", gpu_lib.combine(y, plain)),
+                      ("combine", gpu_lib.combine(y.detach(), r)), ("experts", gpu_lib.experts(x, up, down, plain)),
+                      ("adapted_product", gpu_lib.adapted_product(x.detach(), w[0], a, b, which))):
+        with pytest.raises(RuntimeError, match=name + " takes no part in autograd"):
+            (out.float().sum() * 2).backward()
+    assert torch.equal(r.ids, plain.ids) and torch.equal(r.weights, plain.weights)
+    with torch.no_grad():
+        assert not gpu_lib.expert_product(x, w, plain).requires_grad
+    assert not gpu_lib.expert_product(x.detach(), w, plain).requires_grad
+    # the same parameters, their gradients formed by hand
+    dy, _ = gpu_lib.combine_backward(_normal(4, 6, 24).cuda(), y.detach(), plain)
+    x.grad = gpu_lib.expert_product_backward(dy, x.detach(), w, plain)[0]
+    assert x.grad.shape == x.shape
+
+
 def test_routing_as_sparse_matrices(gpu_lib):
     """The choice and its transpose as CSR, multiplied by the library's SpGEMM: how often two experts
     serve the same token."""
