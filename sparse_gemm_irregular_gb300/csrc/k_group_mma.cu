@@ -623,6 +623,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
                 const float near = __uint_as_float(most) * p.near;
                 if (rounds_apart<T>(v - near, v + near)) marks |= 1u << e;
               }
+              // fewer than eight columns say too little of how large the parts of a sum were: all in order
+              if (p.m - (m - lane) < 8) marks = n == 32 ? 0xffffffffu : (1u << n) - 1u;
               if (m < p.m) p.unsure[(static_cast<int64_t>(w.r) * ((p.tile_n + 31) / 32) + j / 32) * p.m + m] = marks;
             };
             if (p.out_type == SPGEMM_DTYPE_BF16) mark(__nv_bfloat16());

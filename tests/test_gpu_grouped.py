@@ -344,6 +344,30 @@ def test_16_bit_rows_are_the_ordered_sums_rounded_on_both_paths(gpu_lib, tokens,
     gpu_lib.grouped_status()
 
 
+@pytest.mark.parametrize("n", [1, 3, 33, 36, 161])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_16_bit_rows_with_few_columns_beside(gpu_lib, n, dtype):
+    """The last columns may have none beside them to tell how large a sum's parts were."""
+    import torch
+    r = _routing(gpu_lib, np.zeros((20000, 1), np.int32), 1)
+    x, w = _normal(1, 20000, 1024, dtype=dtype).cuda(), _normal(2, 1, n, 1024, dtype=dtype, std=1 / 32).cuda()
+    want = gpu_lib.expert_product(x.float(), w.float(), r).to(x.dtype)  # the CUDA cores add in order
+    assert torch.equal(gpu_lib.expert_product(x, w, r), want)
+
+
+def test_weights_with_any_group_stride(gpu_lib):
+    """Groups need not lie a whole number of rows apart."""
+    import torch
+    r = _routing(gpu_lib, _random_ids(8, 700, 3, 2), 3)
+    x, dy = _normal(1, 700, 64).cuda(), _normal(3, 1400, 40).cuda()
+    flat = _normal(2, 3 * (40 * 72 + 8)).cuda()
+    w = flat.as_strided((3, 40, 64), (40 * 72 + 8, 72, 1))
+    assert torch.equal(gpu_lib.expert_product(x, w, r), gpu_lib.expert_product(x, w.contiguous(), r))
+    assert torch.equal(gpu_lib.expert_product_backward(dy, x, w, r)[0], gpu_lib.expert_product_backward(dy, x, w.contiguous(), r)[0])
+    overlap = flat.as_strided((3, 40, 64), (8, 72, 1))  # read only: groups may share storage
+    assert torch.equal(gpu_lib.expert_product(x, overlap, r), gpu_lib.expert_product(x, overlap.contiguous(), r))
+
+
 @pytest.mark.parametrize("tokens,groups,top_k,d,n,dtype", [
     (4096, 8, 4, 2048, 1024, "bf16"), (509, 16, 2, 1024, 776, "f16"), (900, 30, 3, 4000, 520, "bf16"), (2000, 6, 2, 1576, 792, "f16")])
 def test_gradient_of_the_weights_in_the_chain(gpu_lib, tokens, groups, top_k, d, n, dtype):
