@@ -308,6 +308,8 @@ def group_rows(ids, groups: int, *, weights=None, stream=None) -> Routing:
     import torch
     _same_device("group_rows", ids, weights)
     _want(ids, "ids", torch.int32)
+    if ids.dim() not in (1, 2):
+        raise ValueError("ids: (tokens, top_k) or (tokens) are wanted")
     ids = ids if ids.dim() == 2 else ids[:, None]
     dev = ids.device
     offsets = torch.empty(groups + 1, dtype=torch.int32, device=dev)

@@ -236,6 +236,16 @@ def test_tensors_of_different_devices_are_refused():
                 fn(*args, **{name: there})
 
 
+@pytest.mark.parametrize("shape", [(), (2, 3, 4)])
+def test_ids_of_other_dimensions_are_refused(shape):
+    import types
+
+    import torch
+    ids = types.SimpleNamespace(dtype=torch.int32, is_cuda=True, device="cuda:0", is_contiguous=lambda: True, dim=lambda: len(shape))
+    with pytest.raises(ValueError, match="ids"):
+        sg.group_rows(ids, 4)
+
+
 def test_status_is_read_on_the_device_of_its_stream(monkeypatch):
     """Each device has a status word: the call looks at the stream's, not at the current one's."""
     import contextlib
