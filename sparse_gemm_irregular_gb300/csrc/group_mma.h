@@ -35,6 +35,8 @@ struct MmaArgs {
   int hold;                // tests: withhold an announcement
 };
 
+int sm_count();
+
 // see spgemm_grouped_debug
 void mma_debug(int32_t hold, int32_t polls);
 // see spgemm_grouped_force
@@ -55,9 +57,10 @@ bool mma_gathers(const spgemm_grouping& g);
 bool launch_mma_forward(const spgemm_grouping& g, const spgemm_dense& x, bool gather, const spgemm_weights& w,
                         bool gated, const spgemm_dense& y, uint32_t* unsure, bool early, cudaStream_t s);
 
-// Rows of the N-side tiles that launch_mma_forward takes (not gated), and the bytes of its marks: a word per 32
-// rows of a tile and column of y.
+// Rows of the N-side tiles that launch_mma_forward takes (not gated), about how many there are, and the bytes of
+// its marks: a word per 32 rows of a tile and column of y.
 int mma_forward_tile(const spgemm_grouping& g, const spgemm_dense& x, bool gather, int64_t cols);
+int64_t mma_likely_tiles(const spgemm_grouping& g, int tile_n);
 int64_t mma_marks_bytes(const spgemm_grouping& g, int tile_n, int64_t cols);
 // Sums the marked elements of y again in index order (k_group_settle.cu); arguments as of launch_mma_forward.
 bool launch_settle(const spgemm_grouping& g, const spgemm_dense& x, bool gather, const spgemm_weights& w,

@@ -828,6 +828,8 @@ bool encode_weights(CUtensorMap* map, const spgemm_weights& w) {
   return encode(map, w.dtype, w.data, 3, dims, strides, kDeep, 64);
 }
 
+}  // namespace
+
 int sm_count() {
   static const int sms = [] {  // the library runs on one kind of device
     int dev = 0, n = 1;
@@ -837,6 +839,8 @@ int sm_count() {
   }();
   return sms;
 }
+
+namespace {
 
 template <int MODE, bool PAIR, bool SPLIT>
 bool launch(const MmaMaps& maps, MmaArgs a, int64_t grid, cudaStream_t s) {
@@ -1013,6 +1017,8 @@ Width forward_width(const spgemm_grouping& g, const spgemm_dense& x, bool gather
 int mma_forward_tile(const spgemm_grouping& g, const spgemm_dense& x, bool gather, int64_t cols) {
   return forward_width(g, x, gather, false, cols).n;
 }
+
+int64_t mma_likely_tiles(const spgemm_grouping& g, int tile_n) { return likely_tiles(g, tile_n); }
 
 int64_t mma_marks_bytes(const spgemm_grouping& g, int tile_n, int64_t cols) {
   return 4 * most_tiles(g, tile_n) * ceil_div(tile_n, 32) * cols;

@@ -7,7 +7,7 @@
 // first kernel marks each sum that is no further from a boundary than the two orders may differ, one bit per
 // element, and this one computes exactly those in order: 3.5% of a bf16 result, 18% of an f16 one (2048 terms).
 //
-// A block takes up to 128 rows of one tile and 128 columns and passes over the contracted index in 64-deep slices
+// A block takes up to 128 rows of one tile and 128 columns (or 64) and passes over the contracted index in 64-deep slices
 // through shared memory (only the rows and columns with a mark).  A thread computes an element, up to six at a time,
 // from 16-byte pieces of its row and column.  Lane i works i modulo 8 pieces behind: the eight lanes that read together
 // are at eight different pieces of 128-byte rows, so they meet different banks whatever their rows and columns
@@ -25,12 +25,11 @@ namespace sg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsOf = 128, kColsOf = 128;  // of a block: rows of x, rows of w
+constexpr int kRowsOf = 128;                 // of a block: rows of x
 constexpr int kDeep = 64;
 constexpr int kEach = 6;                     // elements of a thread at a time
 constexpr int kStages = 3;                   // a slice that arrives, the current one, the one before
-constexpr int kStage = (kRowsOf + kColsOf) * kDeep * 2;
-constexpr int kWords = kRowsOf / 32 * kColsOf;
+constexpr int stage_bytes(int cols_of) { return (kRowsOf + cols_of) * kDeep * 2; }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {  // the rest of 16 as zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -60,13 +59,14 @@ __device__ __forceinline__ float add8(float acc, const uint4& a, const uint4& b)
 
 }  // namespace
 
-template <typename T>
+template <typename T, int kColsOf>
 __global__ void __launch_bounds__(kThreads, 2) k_settle(const int32_t* __restrict__ offsets, int groups, int slots, int tile_n,
                                                      const int32_t* __restrict__ order, int top_k, int64_t x_rows,
                                                      const T* __restrict__ x, int64_t x_stride, const T* __restrict__ w,
                                                      int64_t w_group, int64_t w_row, int depth,
                                                      const uint32_t* __restrict__ unsure, T* __restrict__ y,
                                                      int64_t y_stride, int cols) {
+  constexpr int kStage = stage_bytes(kColsOf), kWords = kRowsOf / 32 * kColsOf;
   extern __shared__ __align__(16) unsigned char s_stage[];  // rows of x, then rows of w, per stage
   __shared__ uint32_t s_word[kWords], s_rows[kRowsOf / 32];  // marks: column by column, four words of 32 rows each
   __shared__ int s_pre[kWords], s_tmp[33], s_tile[3];        // marks before each word
@@ -117,10 +117,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_settle(const int32_t* __restric
   __syncthreads();
   int total = 0;
   {
-    const int one = __popc(s_word[2 * tid]), both = one + __popc(s_word[2 * tid + 1]);
-    const int before = block_incl_scan(both, s_tmp, &total) - both;
-    s_pre[2 * tid] = before;
-    s_pre[2 * tid + 1] = before + one;
+    constexpr int kOwn = kWords / kThreads;
+    int own = 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) own += __popc(s_word[kOwn * tid + i]);
+    int before = block_incl_scan(own, s_tmp, &total) - own;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      s_pre[kOwn * tid + i] = before;
+      before += __popc(s_word[kOwn * tid + i]);
+    }
   }
   if (total == 0) return;
   {
@@ -134,12 +140,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_settle(const int32_t* __restric
         }
         if (r >= 0 && r < x_rows) from = x + r * x_stride;
       }
-    } else {
+    } else if (tid < kRowsOf + kColsOf) {
       const int c = tid - kRowsOf;
       if (s_word[4 * c] | s_word[4 * c + 1] | s_word[4 * c + 2] | s_word[4 * c + 3])
         from = w + g * w_group + (m0 + c) * w_row;
     }
-    s_from[tid] = from;
+    if (tid < kRowsOf + kColsOf) s_from[tid] = from;
   }
   __syncthreads();
   const uint32_t stage = static_cast<uint32_t>(__cvta_generic_to_shared(s_stage));
@@ -224,31 +230,41 @@ bool launch_settle(const spgemm_grouping& g, const spgemm_dense& x, bool gather,
                    const spgemm_dense& y, const uint32_t* unsure, int tile_n, cudaStream_t s) {
   if (g.slots == 0 || y.cols == 0) return true;
   bool ok = true;
-  const int64_t grid = mma_marks_bytes(g, tile_n, 1) / (4 * ceil_div(tile_n, 32)) * std::max(tile_n / kRowsOf, 1) * ceil_div(y.cols, kColsOf);
-  if (grid > 0x7fffffff) {
-    set_last_error("too many tiles");
-    return false;
-  }
-  auto go = [&](auto type) {
+  const int64_t per = std::max(tile_n / kRowsOf, 1);
+  auto go = [&](auto type, auto cols_of) {
     using T = decltype(type);
+    constexpr int kColsOf = decltype(cols_of)::value, kSmem = kStages * stage_bytes(kColsOf);
+    const int64_t grid = mma_marks_bytes(g, tile_n, 1) / (4 * ceil_div(tile_n, 32)) * per * ceil_div(y.cols, kColsOf);
+    if (grid > 0x7fffffff) {
+      set_last_error("too many tiles");
+      ok = false;
+      return;
+    }
     static std::atomic<uint64_t> raised{0};  // devices on which the kernel may use this much shared memory
     int dev = 0;
     cudaGetDevice(&dev);
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(raised.load(std::memory_order_relaxed) & bit)) {
-      if (cudaFuncSetAttribute(k_settle<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * kStage) != cudaSuccess) {
+      if (cudaFuncSetAttribute(k_settle<T, kColsOf>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) {
         ok = false;
         return;
       }
       raised.fetch_or(bit, std::memory_order_relaxed);
     }
-    ok = launch_next(k_settle<T>, static_cast<unsigned>(grid), kThreads, kStages * kStage, s, g.offsets, g.groups, static_cast<int>(g.slots), tile_n,
-                     gather ? g.order : nullptr, g.top_k, x.rows, static_cast<const T*>(x.data), x.stride,
-                     static_cast<const T*>(w.data), w.group_stride, w.row_stride, static_cast<int>(x.cols), unsure,
-                     static_cast<T*>(y.data), y.stride, static_cast<int>(y.cols));
+    ok = launch_next(k_settle<T, kColsOf>, static_cast<unsigned>(grid), kThreads, kSmem, s, g.offsets, g.groups,
+                     static_cast<int>(g.slots), tile_n, gather ? g.order : nullptr, g.top_k, x.rows,
+                     static_cast<const T*>(x.data), x.stride, static_cast<const T*>(w.data), w.group_stride, w.row_stride,
+                     static_cast<int>(x.cols), unsure, static_cast<T*>(y.data), y.stride, static_cast<int>(y.cols));
   };
-  if (x.dtype == SPGEMM_DTYPE_BF16) go(__nv_bfloat16());
-  else go(__half());
+  // Half as wide where that many blocks of 128 columns leave SMs idle: 1018 rows, 16 groups, 1024 x 776 (112 blocks) 75 us
+  // with 128 columns, 48 with 64 (f16; bf16 35 and 30); 1018 rows, 1024 x 2048 (256 blocks) 84 and 80 (bf16 43 and 51).
+  const bool narrow = mma_likely_tiles(g, tile_n) * per * ceil_div(y.cols, 128) < sm_count();
+  for_dtype(x.dtype, [&](auto type) {
+    if constexpr (sizeof(type) == 2) {
+      if (narrow) go(type, std::integral_constant<int, 64>());
+      else go(type, std::integral_constant<int, 128>());
+    }
+  });
   return ok;
 }
 
