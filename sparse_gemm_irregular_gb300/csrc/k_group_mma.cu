@@ -650,9 +650,13 @@ __global__ void __launch_bounds__(kThreads, SPLIT ? 2 : 1) k_group_mma(const __g
           }
           uint32_t odd = 0;  // Adapted: sums to form again
           if (MODE == kMmaAdapted) {
+            uint32_t worst = 0;  // twice the bits: no sign
 #pragma unroll
-            for (int e = 0; e < 32; ++e) odd |= not_finite(r[e]) && e < n ? 1u << e : 0u;
-            if (m >= p.m) odd = 0;
+            for (int e = 0; e < 32; ++e) worst = max(worst, r[e] + r[e]);
+            if (worst >= 0xff000000u && m < p.m) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) odd |= not_finite(r[e]) && e < n ? 1u << e : 0u;
+            }
           }
           int token = 0;
           float f = 1.0f;
