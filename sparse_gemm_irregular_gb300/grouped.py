@@ -181,6 +181,13 @@ def _used(args, kw) -> list:
     return found
 
 
+def _wants_gradient(args, kw) -> bool:
+    for a in args if not kw else (*args, *kw.values()):
+        if getattr(a.weights if a.__class__ is Routing else a, "requires_grad", False):
+            return True
+    return False
+
+
 _stop = None  # made on first use (the package imports without torch)
 
 
@@ -215,13 +222,10 @@ def _entry_point(fn):
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         import torch
-        grad = torch.is_grad_enabled()
-        if stream is None and not grad:
-            return fn(*args, **kw)
-        used = _used(args, kw)
         if stream is None:
             out = fn(*args, **kw)
         else:
+            used = _used(args, kw)
             for t in used:
                 if t.device != stream.device:
                     raise ValueError("stream: on %s, a tensor on %s" % (stream.device, t.device))
@@ -229,10 +233,8 @@ def _entry_point(fn):
                 out = fn(*args, **kw)
             for t in used:
                 t.record_stream(stream)
-        if grad:
-            for t in used:
-                if t.requires_grad:
-                    return _without_graph(fn.__name__, out, used)
+        if torch.is_grad_enabled() and _wants_gradient(args, kw):
+            return _without_graph(fn.__name__, out, _used(args, kw))
         return out
     return call
 
