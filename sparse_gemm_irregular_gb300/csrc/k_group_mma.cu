@@ -14,9 +14,8 @@
 //
 // Operands go to shared memory in 64-deep slices by bulk copies: 128-byte swizzled boxes.  Rows in any
 // order come by gathering copies, four rows each, about 40 cycles from one warp where the matrix instruction
-// takes 8 for them.  They serve tiles of at most 128 rows (mma_gathers(): the weights bound these, and they
-// save the launch that lays x out: product chain of 509 rows 97 -> 81 us) and the ends of groups; for more
-// rows x is laid out in group order first (65536 rows, 2048 x 2048: 1.95 ms a chain gathering throughout, 1.61 ms so).
+// takes 8 for them.  They serve tiles of at most 128 rows where groups have few rows (mma_gathers()) and the ends of
+// groups; for more rows x is laid out in group order first.
 // A gathered row index past the matrix reads as zeros: that masks the positions behind a group's
 // end (Dw, where they are contracted, on both operands, so that a NaN there cannot leak) and, in Adapted,
 // the tokens of other adapters.
@@ -36,7 +35,8 @@
 // in the order of their ranks.
 //
 // Measured on GB300 (of the measured 1935 TFLOP/s and 6.69 TB/s): 65536 rows, 32 unequal groups, 2048 x 2048:
-// forward 315 us (1745 TFLOP/s, 90%; equal groups 303 us, the library's dense batched product 280 us), dx 344 us
+// forward 315 us with 32-bit rows (1745 TFLOP/s, 90%; equal groups 303 us, the library's dense batched product 280 us),
+// 348 us with 16-bit rows and their marks (k_group_settle.cu adds 1.58 ms in bf16), dx 344 us
 // (83%, 32-bit rows out), dw 336 us (85%); tensor pipe 73% busy, the rest is barrier rounds and the epilogue's
 // stores (20 us of 303).  Gated, 49152 rows, 64 groups, 2048 x 2048: 267 us (1540 TFLOP/s, 80%).  Adapted, 8192
 // rows, 4096 x 4096, rank 64: 165 us (1760 TFLOP/s, 91%).  A layer of eight tokens and 64 experts reads its
@@ -64,7 +64,7 @@ constexpr int kMaxStages = 12;
 constexpr int kABytes = 128 * 128; // A's part of a stage: 128 rows of 128 bytes
 constexpr int kBox = 64 * 128;     // a 64 x 64 box
 constexpr int kTmemCols = 512;
-constexpr int kSplitTile = 64;     // widest tile that is split
+constexpr int kSplitTile = 64;     // widest tile that is split: its sums (128 x 64, 32 KB) meet in the stages of half an SM
 constexpr int kSmemMost = 227 * 1024;
 
 struct Control {
@@ -921,9 +921,10 @@ int most_split(int n, int64_t tiles, int64_t slices) {
 // cycles per column) and its bytes at 60 per cycle and SM, a tile the longer of its slices and of the
 // epilogue (12 cycles per column) plus 1000 to change over, or 8000 for the meeting of a split tile's blocks;
 // `tiles(n)` of them on the N side.
-// Measured against "twice the average group, pairs at 256": product chain of 801 rows x 4 of 40 groups,
-// 3864 x 384, 181 -> 163 us; adapters of 387 rows, 2192 x 5592, 88 -> 55 us; where there are many tiles
-// both pick the same.
+// The constants are estimates from the kernel's traffic and from profiles, not a fit.  Held against every width a
+// kernel can take (48 sweeps: forward, layer, dx, dw and adapted, 64 to 65536 rows, 4 to 64 groups, 280 to 8192 deep):
+// within 1% of the best in 28, 5% above it on average, at worst 40% (six rows in each of 64 groups: tiles of 16 rows
+// 35 us, of 64 rows 25 us; the groups' sizes are not known here).
 template <typename F>
 Width pick_width(int64_t m, int m_per_block, int64_t slices, int least, bool splits, F tiles) {
   Width best{256, true, 1};
@@ -991,6 +992,8 @@ void mma_debug(int32_t hold, int32_t polls) {
 }
 void mma_force(int32_t width, int32_t pair, int32_t split) { t_width = Width{width, pair != 0, split}; }
 
+// Gathered against laid out first, 2048 x 2048, 64 groups of 32 rows 93 us and 94, of 96 rows 109 and 110, of 128 rows 152
+// and 116, of 512 rows 452 and 245; 16 groups of 32 rows 30 and 31; 8 groups of 16 rows, 4096 x 1024, 24 and 26.
 bool mma_gathers(const spgemm_grouping& g) { return g.slots <= 64 * static_cast<int64_t>(g.groups); }
 
 bool mma_takes(const spgemm_dense& m) { return m.dtype != SPGEMM_DTYPE_F32 && aligned(m.data, m.stride) && m.rows < (1LL << 31) && m.cols < (1LL << 31); }
@@ -1004,12 +1007,12 @@ namespace {
 // How far the tensor cores' sum of `depth` products may be from the 32-bit sum in index order, in units of the
 // largest sum of the row's 32 columns beside it: half a unit in the last place (2^-24) for each of its depth / 16
 // additions, and 16 more for the other order's own roundings.  Largest distance measured, in units of this:
-// 0.97 in 7e8 sums of normal, uniform and shifted values of 64 to 8192 terms, 1.22 where a hundredth of the features
-// is thirty times the rest; no element of these was rounded another way without being marked.  At half of this
-// 3e-8 of them were, at twice this twice as many sums are marked.
+// 0.97 in 7e8 sums of normal, uniform and shifted values and rows of very different sizes, 64 to 8192 terms; 1.22 where a
+// hundredth of the features is thirty times the rest.  No element of these was rounded another way without being
+// marked.  Half of this would mark 45% fewer and leave up to 1e-6 of the elements (5e-5 of 8192 shifted terms) wrong.
 float near_of(int64_t depth) { return static_cast<float>(depth + 256) * 0x1p-28f; }
 
-// gathered rows come to blocks on their own, 128 at most
+// Tiles of gathered rows belong to single blocks and have 128 rows at most: groups with more come laid out.
 Width forward_width(const spgemm_grouping& g, const spgemm_dense& x, bool gather, bool gated, int64_t cols) {
   const Width width =
       pick_width(cols, gated ? 64 : 128, ceil_div(x.cols, kDeep), 16, false, [&](int n) { return likely_tiles(g, n); });
@@ -1096,7 +1099,9 @@ bool launch_mma_shrink(const spgemm_grouping& g, const spgemm_dense& x, const sp
   a.gather = a.scatter = 1;
   a.m = static_cast<int>(v.cols);
   a.depth = static_cast<int>(x.cols);
-  // the widest tile that still gives every SM one: x is read once either way, a's rows once per tile
+  // The widest tile that still gives every SM one: x is read once either way, a's rows once per tile.  The whole call
+  // with 16 adapters, rank 64, 64 outputs: 8192 rows of 4096, tiles of 32 72 us, 64 54 us, 128 59 us; 20000 rows of 2048
+  // 75, 57 and 52 us.  (2048 rows: 41 us with the 32 that this takes, 35 with 64.)
   a.tile_n = 32;
   while (a.tile_n < 128 && g.slots > static_cast<int64_t>(a.tile_n) * sm_count()) a.tile_n *= 2;
   const Width asked = chosen(Width{a.tile_n, false, 0}, 32, 128, true, ceil_div(a.depth, kDeep));
