@@ -102,6 +102,24 @@ class Rows8:
         r.dtype, r.shape, r._values, r._scales, r._store, r._bytes = self.dtype, self.shape, self.values, scales, None, None
         return r
 
+    def __copy__(self) -> "Rows8":
+        r = Rows8.__new__(Rows8)
+        for name in Rows8.__slots__:
+            if hasattr(self, name):
+                setattr(r, name, getattr(self, name))
+        return r
+
+    def __reduce__(self):
+        """Copies and saved ones are made of the tensors: the packed addresses are this one's.  As bytes, because the values
+        and the scales may lie in one storage, which cannot be saved as two types."""
+        import torch
+        if self._store is not None:
+            return Rows8._made, (self._store, self._at, *map(int, self.shape), self.dtype)
+        if self.requires_grad:
+            raise RuntimeError("Rows8: of an input that wants a gradient, there is no copy (make it of detach()ed inputs)")
+        scales = self._scales.t().clone(memory_format=torch.contiguous_format)
+        return _rows8_again, (self._values.view(torch.uint8), scales.view(torch.uint8), self.dtype)
+
     def _packed(self) -> bytes:
         if self._bytes is not None:
             return self._bytes
@@ -109,6 +127,15 @@ class Rows8:
         rows, cols = v.shape
         stride = v.stride(0) if rows > 1 else (cols + 15) // 16 * 16
         return _pack_rows8(v.data_ptr(), s.data_ptr(), rows, cols, stride, s.stride(1) if s.shape[1] > 1 else rows)
+
+
+def _rows8_again(values, scales, dtype) -> Rows8:
+    """A Rows8 from its bytes."""
+    import torch
+    r = Rows8.__new__(Rows8)
+    r.dtype, r.shape, r._store, r._bytes = dtype, values.shape, None, None
+    r._values, r._scales = values.view(torch.float8_e4m3fn), scales.view(torch.float32).t()
+    return r
 
 
 @dataclass(frozen=True)
