@@ -416,8 +416,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_few(const __grid_constant_
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int r = 2 * q + j;
-      acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 2);  // h's two parts
-      acc[2 + j] += __shfl_xor_sync(0xffffffffu, acc[2 + j], 2);
+      // h's two parts.  An infinite entry of the matrix times the second one, of either sign or 0, says nothing: the first's is the answer.
+      const float rest = __shfl_xor_sync(0xffffffffu, acc[j], 2), rest8 = __shfl_xor_sync(0xffffffffu, acc[2 + j], 2);
+      if (fabsf(acc[j]) < INFINITY) acc[j] += rest;
+      if (fabsf(acc[2 + j]) < INFINITY) acc[2 + j] += rest8;
       if (r < rows && r < kHalf) {
         float* to = mine + token[first + r] * 16 + g;
         const float w = ordered[first + r];
