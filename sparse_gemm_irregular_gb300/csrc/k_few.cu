@@ -31,6 +31,7 @@
 // more, 8 tokens 26.  The choice takes 6 us and the logits 3, of one token's 26.  One number to a hidden value instead of two: 1 us
 // less for one token, 16 for 32.
 #include <algorithm>
+#include <atomic>
 
 #include "group_mma.h"
 #include "quant8.cuh"
@@ -567,17 +568,33 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_few(const __grid_constant_
 
 namespace {
 
+// Length of a list: an expert's last tile may be part of one.
+constexpr int64_t most_tiles(int64_t slots, int64_t experts, int tile) { return std::min(slots, std::min(slots, experts) + slots / tile); }
+
+// Shared memory of a block: the warps' sums, the list, each hidden row's token and weight
+constexpr int sums_bytes(bool down, int tokens) { return down ? kWarps * tokens * 16 * 4 : 2 * kWarps * 512; }
+constexpr int block_bytes(int sums, int most, int slots) { return sums + most * static_cast<int>(sizeof(Chosen)) + 8 * slots; }
+constexpr int kMostSlots = kMaxTokens * kMaxTopK;
+constexpr int kMostBytes = block_bytes(sums_bytes(true, kMaxTokens), static_cast<int>(most_tiles(kMostSlots, kMaxGroups, kHalf)), kMostSlots);
+static_assert(kPerSm * (kMostBytes + 1024) <= 227 * 1024, "blocks of an SM");
+
 template <typename T, bool EIGHT, bool DOWN>
 bool launch(Args a, cudaStream_t s) {
-  a.sums = DOWN ? kWarps * a.tokens * 16 * 4 : 2 * kWarps * 512;
-  const int bytes = a.sums + a.most * static_cast<int>(sizeof(Chosen)) + 8 * a.slots;
+  a.sums = sums_bytes(DOWN, a.tokens);
+  const int bytes = block_bytes(a.sums, a.most, a.slots);
   auto kern = k_few<T, EIGHT, DOWN>;
-  if (bytes > 47 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  // The limit belongs to the kernel, not to the call: it is raised to the most that any call takes, once per device, and never
+  // lowered, so that another thread's call does not take it from under this one's launch.
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(raised.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes) != cudaSuccess) return false;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+  }
   return launch_next(kern, dim3(static_cast<unsigned>(kPerSm * sm_count())), kThreads, static_cast<size_t>(bytes), s, a);
 }
-
-// Length of a list: an expert's last tile may be part of one.
-int64_t most_tiles(int64_t slots, int64_t experts, int tile) { return std::min(slots, std::min(slots, experts) + slots / tile); }
 
 // How many blocks share a unit of the down product: the fewest turns of all blocks times pieces of a warp; a unit's end takes
 // as long as a piece, with other blocks to meet as three (one token, 6 experts of 1024 x 2048: 29.9 us a layer with one block to a

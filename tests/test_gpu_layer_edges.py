@@ -33,3 +33,45 @@ def test_infinities_in_the_down_matrix(gpu_lib, tokens, dtype):
             with np.errstate(invalid="ignore"):
                 want = np.sum(np.sign(h) * signs[n] * np.inf)
             assert np.array_equal(got[t, n], want, equal_nan=True), (t, n, got[t, n], want)
+
+
+def test_layers_of_several_host_threads(gpu_lib):
+    """Calls that take different amounts of shared memory, at once on four threads: none is refused, all are right."""
+    import threading
+
+    import torch
+
+    from sparse_gemm_irregular_gb300.grouped import _dense, _pack_rule
+    x, router = normal((64, 64), "bf16"), normal((512, 64), "bf16", seed=1, std=1 / 8)
+    up8 = gpu_lib.quantise_weights(normal((512, 32, 64), "bf16", seed=2, std=1 / 8))
+    down8 = gpu_lib.quantise_weights(normal((512, 48, 16), "bf16", seed=3, std=1 / 4))
+    sizes = (64, 60, 64, 7)
+    want = {t: gpu_lib.expert_layer(x[:t], router, up8, down8, 16) for t in sizes}
+    torch.cuda.synchronize()
+    lib, go, refused, got = gpu_lib.load(), threading.Barrier(len(sizes)), [], {}
+
+    def calls(i, t):
+        s = torch.cuda.Stream()
+        out, ids, weights = (torch.empty_like(v) for v in want[t])
+        # the entry point itself, which lets the other threads run: through the Python layer calls hardly meet
+        args = (_dense(x[:t], "x"), _dense(router, "w_router"), _pack_rule(16, 0, 1, 1, 0, 1, 1.0, 0), None, None, None, up8._packed(),
+                down8._packed(), _dense(out, "out"), ids.data_ptr(), weights.data_ptr(), s.cuda_stream)
+        torch.cuda.synchronize()
+        go.wait()
+        for _ in range(4000):
+            rc = lib.spgemm_expert_layer(*args)
+            if rc:
+                refused.append((t, rc, gpu_lib.spgemm_last_error()))
+                break
+        s.synchronize()
+        got[i] = out, ids, weights
+
+    threads = [threading.Thread(target=calls, args=a) for a in enumerate(sizes)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not refused, refused
+    for i, t in enumerate(sizes):
+        assert all(torch.equal(p, q) for p, q in zip(got[i], want[t]))
+    gpu_lib.grouped_status()
