@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_few(const __grid_constant_
       }
       acc[j] = acc[2 + j] = 0.0f;
     }
+    __syncwarp();  // a token may be in another row of the next expert, and its sums in another lane's hands
   };
   // the warps' sums of a unit meet
   auto finish = [&]() {

@@ -75,3 +75,34 @@ def test_layers_of_several_host_threads(gpu_lib):
     for i, t in enumerate(sizes):
         assert all(torch.equal(p, q) for p, q in zip(got[i], want[t]))
     gpu_lib.grouped_status()
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_a_token_in_another_row_of_each_expert(gpu_lib, dtype, bits):
+    """Token 3 is the first, second, third and fourth of the experts that it chooses, one after the other: its sums pass from lane to
+    lane of the warps that form them."""
+    import torch
+    tokens, experts, top_k, d, hidden, n = 4, 16, 8, 256, 48, 144
+    chosen = [[e for e in range(8) if t == 3 or e % 4 > t] for t in range(tokens)]
+    chosen = [c + list(range(8 + t, 8 + t + top_k - len(c))) for t, c in enumerate(chosen)]
+    assert all(len(c) == top_k and max(c) < experts for c in chosen)
+    x, router = normal((tokens, d), dtype), torch.zeros(experts, d)
+    x[:, :tokens] = torch.eye(tokens) * 4
+    for t, c in enumerate(chosen):
+        for i, e in enumerate(c):
+            router[e, t] = 1 + i / 16  # no two alike
+    router = router.to(x)
+    up, down = normal((experts, 2 * hidden, d), dtype, seed=2, std=d ** -0.5), normal((experts, n, hidden), dtype, seed=3, std=hidden ** -0.5)
+    if bits == 8:
+        up, down = gpu_lib.quantise_weights(up), gpu_lib.quantise_weights(down)
+        u64, d64 = (f64(gpu_lib.dequantise(w, torch.float32)) for w in (up, down))
+    else:
+        u64, d64 = f64(up), f64(down)
+    want, ids, weights, err, gap = layer_ref(f64(x), f64(router), u64, d64, dtype, top_k, None, parts=2)
+    assert gap > 1e-6 and [list(i) for i in ids] == chosen
+    first, gi, _ = gpu_lib.expert_layer(x, router, up, down, top_k)
+    assert np.array_equal(gi.cpu().numpy(), ids)
+    assert np.all(np.abs(f64(first) - want) <= err)
+    for _ in range(50):
+        assert torch.equal(gpu_lib.expert_layer(x, router, up, down, top_k)[0], first)
