@@ -91,11 +91,11 @@ class Rows8:
 
     @property
     def requires_grad(self) -> bool:
-        return self._scales is not None and self._scales.requires_grad
+        return any(t is not None and t.requires_grad for t in (self._values, self._scales))
 
     @property
     def _tensors(self):
-        return (self._store,) if self._store is not None else (self._values, self._scales)
+        return tuple(t for t in (self._store, self._values, self._scales) if t is not None)
 
     def _with_scales(self, scales) -> "Rows8":
         r = Rows8.__new__(Rows8)
@@ -113,10 +113,10 @@ class Rows8:
         """Copies and saved ones are made of the tensors: the packed addresses are this one's.  As bytes, because the values
         and the scales may lie in one storage, which cannot be saved as two types."""
         import torch
-        if self._store is not None:
-            return Rows8._made, (self._store, self._at, *map(int, self.shape), self.dtype)
         if self.requires_grad:
             raise RuntimeError("Rows8: of an input that wants a gradient, there is no copy (make it of detach()ed inputs)")
+        if self._store is not None:
+            return Rows8._made, (self._store, self._at, *map(int, self.shape), self.dtype)
         scales = self._scales.t().clone(memory_format=torch.contiguous_format)
         return _rows8_again, (self._values.view(torch.uint8), scales.view(torch.uint8), self.dtype)
 
@@ -173,7 +173,7 @@ class Weights8:
 
     @property
     def requires_grad(self) -> bool:
-        return self.scales.requires_grad
+        return self.values.requires_grad or self.scales.requires_grad
 
     @property
     def _tensors(self):
