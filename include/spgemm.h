@@ -563,6 +563,10 @@ int spgemm_grouped_debug(int32_t hold, int32_t polls);
  * to `split` blocks, as far as each kernel can. */
 int spgemm_grouped_force(int32_t width, int32_t pair, int32_t split);
 
+/* For tests: spgemm_quantised_product in later calls of this thread takes tiles of `width` columns (64 to 240, a multiple of
+ * 16: what its own rule chooses from; 0: by that rule, or by spgemm_grouped_force), shared by two blocks when `pair` is set. */
+int spgemm_quantised_force(int32_t width, int32_t pair);
+
 const char* spgemm_strerror(int code);
 /* Detail of the last failure on the calling host thread ("" if none). */
 const char* spgemm_last_error(void);

@@ -143,6 +143,7 @@ EXPORTS = {
     "spgemm_grouped_status": (ctypes.c_int, [_vp]),
     "spgemm_grouped_debug": (ctypes.c_int, [_i32, _i32]),
     "spgemm_grouped_force": (ctypes.c_int, [_i32, _i32, _i32]),
+    "spgemm_quantised_force": (ctypes.c_int, [_i32, _i32]),
     "spgemm_release_memory": (ctypes.c_int, []),
     "spgemm_destroy": (ctypes.c_int, [_vp]),
     "spgemm_strerror": (ctypes.c_char_p, [ctypes.c_int]),

@@ -57,6 +57,7 @@ bool encode_bytes(CUtensorMap* map, const void* data, int rank, const int64_t* d
 int64_t mma_likely_tiles(const spgemm_grouping& g, int tile_n);
 
 // y = rows times the matrix of their group, both in 8 bits (k_group8.cu); x in group order.  early: as below.
+void mma8_force(int32_t width, int32_t pair);  // see spgemm_quantised_force
 bool launch_mma_8bit(const spgemm_grouping& g, const spgemm_rows8& x, const spgemm_weights8& w, const spgemm_dense& y, bool early,
                      cudaStream_t s);
 

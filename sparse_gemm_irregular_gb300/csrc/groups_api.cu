@@ -588,6 +588,12 @@ int spgemm_grouped_force(int32_t width, int32_t pair, int32_t split) {
   return SPGEMM_OK;
 }
 
+int spgemm_quantised_force(int32_t width, int32_t pair) {
+  if ((width && (width < 64 || width > 240 || width % 16)) || pair < 0 || pair > 1) return bad("quantised force: out of range");
+  mma8_force(width, pair);
+  return SPGEMM_OK;
+}
+
 int spgemm_grouped_status(void* stream) {
   set_last_error("");
   cudaStream_t st = static_cast<cudaStream_t>(stream);

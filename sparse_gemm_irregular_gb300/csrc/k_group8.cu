@@ -453,7 +453,10 @@ struct Width {
   int n;
   bool pair;
 };
+thread_local Width t_width = {0, false};  // tests: the width of this thread's calls
+
 Width pick_width(const spgemm_grouping& g, int64_t n, int64_t blocks) {
+  if (t_width.n) return t_width;
   const MmaHooks hooks = mma_hooks();
   if (hooks.width) return {std::min(std::max(hooks.width, 32), kMostCols), hooks.pair && hooks.width == 256};
   Width best{kMostCols, true};
@@ -472,6 +475,8 @@ Width pick_width(const spgemm_grouping& g, int64_t n, int64_t blocks) {
 }
 
 }  // namespace
+
+void mma8_force(int32_t width, int32_t pair) { t_width = {width, pair != 0}; }
 
 bool launch_mma_8bit(const spgemm_grouping& g, const spgemm_rows8& x, const spgemm_weights8& w, const spgemm_dense& y, bool early,
                      cudaStream_t s) {
