@@ -7,6 +7,7 @@
 // All of them read and write each number once and are bound by that.  16 lanes hold a block, eight numbers (16 bytes of
 // a 16-bit type) each, so that a block's largest magnitude is four shuffles away and nothing waits for another warp.
 #include <algorithm>
+#include <type_traits>
 
 #include "quant8.cuh"
 
@@ -206,10 +207,16 @@ __global__ void __launch_bounds__(kThreads)
     load_piece(pre, c, hidden, whole_gate, g);
     load_piece(pre + hidden, c, hidden, whole_up, u);
     Scale8 sg, su;
-    const uint2 g8 = quantise_block(g, most_of_block(most_of(g)), &sg), u8 = quantise_block(u, most_of_block(most_of(u)), &su);
+    const uint32_t most_gate = most_of_block(most_of(g));
+    const uint2 g8 = quantise_block(g, most_gate, &sg), u8 = quantise_block(u, most_of_block(most_of(u)), &su);
     if (c < hidden) {
+      auto product = [&](auto is_short) {
 #pragma unroll
-      for (int e = 0; e < kPiece; ++e) o[e] = g[e] * sigmoid<TO>(g[e]) * u[e];
+        for (int e = 0; e < kPiece; ++e) o[e] = g[e] * sigmoid<decltype(is_short)::value>(g[e]) * u[e];
+      };
+      // (magnitudes compare as their bits do; what is not finite is above all)
+      if (sizeof(TO) == 2 && most_gate <= __float_as_uint(kShortGate)) product(std::true_type());
+      else product(std::false_type());
       store_piece(h, c, hidden, whole_h, o);
       store_piece8(gate, c, hidden, g8);
       store_piece8(up, c, hidden, u8);
@@ -253,15 +260,21 @@ __global__ void __launch_bounds__(kThreads)
   for (; r < rows; r += step) {
     float g[kPiece], u[kPiece], d[kPiece], dg[kPiece], du[kPiece], o[kPiece];
     load_piece(dh, c, hidden, whole_dh, d);
-    dequantise_piece(load_piece8(gate, c, hidden), *gate_scales, g);
+    const float gate_scale = *gate_scales;
+    dequantise_piece(load_piece8(gate, c, hidden), gate_scale, g);
     dequantise_piece(load_piece8(up, c, hidden), *up_scales, u);
+    auto product = [&](auto is_short) {
 #pragma unroll
-    for (int e = 0; e < kPiece; ++e) {
-      const float s = sigmoid<T>(g[e]), gs = g[e] * s;
-      o[e] = gs * u[e];
-      du[e] = d[e] * gs;
-      dg[e] = d[e] * u[e] * (s + gs * (1.0f - s));
-    }
+      for (int e = 0; e < kPiece; ++e) {
+        const float s = sigmoid<decltype(is_short)::value>(g[e]), gs = g[e] * s;
+        o[e] = gs * u[e];
+        du[e] = d[e] * gs;
+        dg[e] = d[e] * u[e] * (s + gs * (1.0f - s));
+      }
+    };
+    // no number of the block is above 448 of its scale
+    if (sizeof(T) == 2 && fabsf(gate_scale) <= kShortGate / 448.0f) product(std::true_type());
+    else product(std::false_type());
     store_piece(dpre, c, hidden, whole_gate, dg);
     store_piece(dpre + hidden, c, hidden, whole_up, du);
     if (again) store_piece(h, c, hidden, whole_h, o);

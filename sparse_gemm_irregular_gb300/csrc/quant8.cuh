@@ -141,11 +141,13 @@ __device__ __forceinline__ float held(float v) { return v; }
 template <>
 __device__ __forceinline__ float held<__half>(float v) { return fabsf(v) > 65504.0f ? copysignf(65504.0f, v) : v; }
 
-// 1 / (1 + exp(-g)) for a result that is rounded to T: to 16 bits the short exponential and division will do (relative error
-// below 2^-18, see gated_silu_short)
-template <typename T>
+// 1 / (1 + exp(-g)).  SHORT: the short exponential and division, for results that are rounded to 16 bits and |g| up to kShortGate:
+// relative error below 2^-17 there (the exponent -g log2(e) is rounded to 2^-18 at most and its factor to 2^-26 of 126, times
+// ln 2; the approximations themselves a few units).  The short division gives 0 where its divisor passes 2^126 (g below -87.3).
+constexpr float kShortGate = 87.0f;
+template <bool SHORT>
 __device__ __forceinline__ float sigmoid(float g) {
-  return sizeof(T) == 2 ? __fdividef(1.0f, 1.0f + __expf(-g)) : 1.0f / (1.0f + expf(-g));
+  return SHORT ? __fdividef(1.0f, 1.0f + __expf(-g)) : 1.0f / (1.0f + expf(-g));
 }
 
 }  // namespace sg
