@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "group_mma.h"
 #include "quant8.cuh"
 
 namespace sg {
@@ -17,7 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRowsOf = kThreads / 32;   // rows of a block: one a warp, two blocks of a row at a time
-constexpr int64_t kBlocksMost = 152 * 16;
+constexpr int64_t kBlocksPerSm = 16;     // of the grid, where there are rows for several a warp
 
 // f(p) for every position p of token t, read by the lanes at once; the whole warp calls it.
 template <typename F>
@@ -299,7 +300,7 @@ bool on_16(const void* data, int64_t stride, int32_t dtype, int64_t offset = 0) 
 // blocks per SM 96 and 120 us, 8 of them 97 and 119, 64 of them 101 and 124, a warp for every row 114 and 140.
 dim3 row_grid(int64_t rows, int64_t cols) {
   const int64_t across = ceil_div(cols, 2 * kBlock8), down = ceil_div(rows, kRowsOf);
-  return dim3(static_cast<unsigned>(std::min(down, std::max<int64_t>(1, kBlocksMost / across))), static_cast<unsigned>(across));
+  return dim3(static_cast<unsigned>(std::min(down, std::max<int64_t>(1, kBlocksPerSm * sm_count() / across))), static_cast<unsigned>(across));
 }
 
 uint8_t* bytes(void* p) { return static_cast<uint8_t*>(p); }
