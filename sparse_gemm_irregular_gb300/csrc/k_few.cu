@@ -254,12 +254,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_few(const __grid_constant_
   int* token = reinterpret_cast<int*>(list + p.most);           // of each hidden row
   float* ordered = reinterpret_cast<float*>(token + p.slots);   // its weight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // The choice was complete before the kernel that starts this one early (down) was itself let past its wait.
+  // The choice was complete before the kernel that starts this one early (down) was itself let past its wait; so were the matrices
+  // and their scales, which the kernels of this call do not write.
   if (!DOWN) {
     pdl_wait();
     pdl_go();
   }
-  // (From L2: what L1 holds of it may be of another call.)
+  // Past L1: every call writes its choice, often at the same addresses, and a line of the one before may have stayed there.
   const int total = __ldcg(p.total);
   for (int i = threadIdx.x; i < p.most; i += kThreads) reinterpret_cast<uint4*>(list)[i] = __ldcg(reinterpret_cast<const uint4*>(p.chosen) + i);
   for (int i = threadIdx.x; i < p.slots; i += kThreads) {

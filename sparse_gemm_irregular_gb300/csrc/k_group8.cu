@@ -142,15 +142,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_8bit(const __grid_constan
     pdl_wait();
     pdl_go();
   }
-  // offsets are used as a non-decreasing sequence inside [0, slots], whatever the array holds
+  // offsets are used as a non-decreasing sequence inside [0, slots], whatever the array holds.  Where the kernel starts early they
+  // are read before its wait: the kernel ahead, which makes only x's rows, waited for everything before it and let this one start
+  // after that, so they were complete.  Past L1: a call before may have left other offsets there, at the same address.
   {
     int run = 0;
     for (int g0 = 0; g0 < p.groups; g0 += kThreads) {
       const int g = g0 + static_cast<int>(threadIdx.x);
       int lo = 0, hi = 0;
       if (g < p.groups) {
-        lo = min(max(p.offsets[g], 0), p.slots);
-        hi = min(max(p.offsets[g + 1], lo), p.slots);
+        lo = min(max(__ldcg(p.offsets + g), 0), p.slots);
+        hi = min(max(__ldcg(p.offsets + g + 1), lo), p.slots);
         c.first[g] = lo;
         if (g == p.groups - 1) c.first[p.groups] = hi;
       }
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_group_8bit(const __grid_constan
   };
   auto tile_of = [&](Walk& w) {
     while (w.g + 1 < p.groups && c.tiles[w.g + 1] <= w.r) ++w.g;
-    const int lo = c.first[w.g], hi = min(max(p.offsets[w.g + 1], lo), p.slots);
+    const int lo = c.first[w.g], hi = max(c.first[w.g + 1], lo);
     Tile t;
     t.g = w.g;
     t.n0 = w.n * p.tile_n;
