@@ -309,9 +309,16 @@ def expert_layer(x, w_router, w_up, w_down, top_k: int, *, bias=None, score: str
                  groups_kept: int = 1, group_score: str = "max", renormalise: bool = True, scale: float = 1.0, stream=None):
     """A whole layer, (out, ids, weights): logits = x w_router^T, the choice of ``route``, the gated experts of ``experts``.
 
-    x (tokens, d); w_router (experts, d); w_up (experts, 2 * hidden, d) and w_down (experts, n, hidden) in x's type or as
-    ``Weights8`` (x stays in 16 bits); ids and weights (tokens, top_k) as in ``Routing``.  Made for decoding, up to 32
-    tokens (64 with ``Weights8``); more are the calls one after the other.  See spgemm_expert_layer."""
+    x (tokens, d); w_router (experts, d) in x's type (a router in other bits: ``route`` of its logits, then ``experts``);
+    w_up (experts, 2 * hidden, d) and w_down (experts, n, hidden) in x's type or as ``Weights8`` (x stays in 16 bits); ids
+    and weights (tokens, top_k) as in ``Routing``.
+
+    Made for decoding, up to 32 tokens (64 with ``Weights8``) in 16 bits with rows of full 16-byte pieces.  There the hidden
+    row is held in two numbers of x's type, and scales multiply in 32 bits.  Anything else is the calls one after the other:
+    the hidden row in one number, as in ``experts`` (in bf16 the result is 2.4e-3 off instead of 1.7e-3), and ``Weights8``
+    of all experts, chosen or not, widened in every call to x's type (scratch of twice their size; scales that are no powers of two
+    rounded with the weights): slower than the same matrices in 16 bits.  Keep those, or the calls in 8 bits
+    (``expert_product8``, ``gated8``), for prompts.  See spgemm_expert_layer."""
     import torch
     _same_device("expert_layer", x, w_router, w_up, w_down, bias)
     d, r = _dense(x, "x"), _dense(w_router, "w_router")
