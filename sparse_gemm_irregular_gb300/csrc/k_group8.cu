@@ -18,8 +18,9 @@
 // share a tile (cta_group::2): each holds half of both operands.
 //
 // Measured: 49152 rows in 64 groups, 2048 x 2048: 178 us, 2320 TFLOP/s (unequal groups, last tiles part empty); 65536 rows in 32
-// groups 206 us, 2670 TFLOP/s.  Bound by what L2 supplies, 40 bytes per cycle and SM with all of them at it, and the tensor
-// pipe is busy 60% of the time.  96 rows in 64 groups: 34 to 37 us, 190 MB at 5.1 to 5.6 TB/s.  Fetching later stages into L2 first made it
+// groups 206 us, 2670 TFLOP/s.  The tensor pipe is busy 60% of the time, and the tiles take 40 bytes per cycle and SM from L2, less than
+// the 16-bit kernel (47): neither is at its limit, and what holds the rest is not established.  96 rows in 64 groups: 34 to 37 us,
+// 190 MB at 5.1 to 5.6 TB/s.  Fetching later stages into L2 first made it
 // slower (211 us for the first), and so did one accumulator of 448 columns (245 us: nothing runs while it is emptied).
 //
 // Every wait is bounded: a role that gives up sets the status word, the others see it, copies in flight are drained,
@@ -450,7 +451,10 @@ bool launch(const CUtensorMap& map_w, const CUtensorMap& map_x, Args a, cudaStre
 //    49152 rows, 64, 2048 x 2048   198 against 199, 230, 308, 416      3063 rows, 10,  712 x 992   11.1 against 13.7, 12.3, 13.5, 13.7
 //    12288                         75 against 76, 85, 110, 138         1018 rows, 16,  776 x 1024  9.9 against 13.0, 12.0, 10.1, 11.2
 //    96                            38 against 48, 39, 51, 59           64 rows, 1,  4096 x 4096    14.6 against 18.5, 21.1, 16.8, 14.7
-// (Without the 2500: 15.3 for the 3063 rows and 17.3 for the 64.)
+// (Without the 2500: 15.3 for the 3063 rows and 17.3 for the 64.)  Against all 24 shapes at 14 sizes, in a replayed graph (which
+// times short kernels in steps of 2 us): within 1% of the best at 5, within 5% at 6 more; 20% off at 1018 rows of 16 groups (12.3 us,
+// 10.3 with 112 to 160 columns), 22% at 20000 rows, 8, 512 x 512 (20.1, 16.4 with 128), 32% at 8 rows, 8, 1024 x 4096 (24.5, 18.5
+// with 176 or pairs).
 struct Width {
   int n;
   bool pair;
