@@ -24,6 +24,7 @@
 #include <memory>
 #include <mutex>
 #include <string>
+#include <unordered_map>
 
 #include "internal.h"
 
@@ -34,6 +35,22 @@ namespace sg {
 
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 long long launch_count() { return g_launches.load(std::memory_order_relaxed); }
+
+cudaError_t raise_smem_of(const void* kern, size_t bytes) {
+  struct Limits {
+    std::mutex mu;
+    std::unordered_map<const void*, size_t> of[64];  // by device
+  };
+  static Limits* limits = new Limits;  // outlives whatever launches at exit
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(limits->mu);
+  size_t& have = limits->of[dev & 63][kern];
+  if (bytes <= have) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) have = bytes;
+  return e;
+}
 
 void set_last_error(const std::string& s) { g_last_error = s; }
 

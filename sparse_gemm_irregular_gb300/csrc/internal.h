@@ -48,6 +48,15 @@ struct BinRule {
 // Bin numbering: level L hash = 2L, level L dense = 2L+1, heavy = 2n, empty = 255.
 constexpr uint8_t kBinEmpty = 255;
 
+// ---- shared memory of a block ---------------------------------------------------------------
+// Lets `kern` take `bytes` of dynamic shared memory on the current device.  The limit is the kernel's, not a call's: it is
+// raised where it is lower and never lowered, so that another host thread's launch keeps what it asked for.
+cudaError_t raise_smem_of(const void* kern, size_t bytes);
+template <typename... P>
+inline cudaError_t raise_smem(void (*kern)(P...), size_t bytes) {
+  return raise_smem_of(reinterpret_cast<const void*>(kern), bytes);
+}
+
 // ---- launch accounting --------------------------------------------------------------------
 void note_launch();        // every kernel launch of the library calls this once
 long long launch_count();

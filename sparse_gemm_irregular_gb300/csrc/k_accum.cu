@@ -644,7 +644,7 @@ static void launch_one(const AccParams& p, int tpr, cudaStream_t s) {
   const size_t gb = group_bytes(p.slots, WARP ? 32 : tpr, DENSE, NUMERIC, !CHUNK);
   const size_t smem = WARP ? gb * kWarpGroupsPerBlock : gb;
   auto kern = k_accum<WARP, NUMERIC, DENSE, CHUNK>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  raise_smem(kern, smem);
   const int64_t blocks = WARP ? ceil_div(p.count, kWarpGroupsPerBlock) : p.count;
   const int threads = WARP ? 32 * kWarpGroupsPerBlock : tpr;
   note_launch();

@@ -475,7 +475,7 @@ static void groups_launch(const ChunkSet& cs, const ChunkDesc* desc, int64_t cou
                           uint32_t* err, int sms, cudaStream_t s) {
   using C = GroupCfg<T>;
   const size_t smem = grp_bytes<T>(width) * C::kGroups;
-  cudaFuncSetAttribute(k_chunk_groups<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  raise_smem(k_chunk_groups<T>, smem);
   int per_sm = 1;
   cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_chunk_groups<T>, C::kBlock, smem);
   if (per_sm < 1) per_sm = 1;
@@ -506,7 +506,7 @@ template <bool WARP, int MODE>
 static void ck_launch(const CkParams& p, int tpr, cudaStream_t s) {
   const size_t smem = chunk_smem_bytes(p.width, p.slots, MODE, WARP);
   auto kern = k_chunk<WARP, MODE>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  raise_smem(kern, smem);
   const int64_t blocks = WARP ? ceil_div(p.count, kCkWarpsPerBlock) : p.count;
   const int threads = WARP ? 32 * kCkWarpsPerBlock : tpr;
   note_launch();
@@ -540,8 +540,7 @@ void launch_chunk_bitmap(const ChunkSet& cs, const int32_t* list, int64_t count,
     if (gacc) {  // L2-resident accumulators (one per SM): the shared array is not needed
       const int64_t blocks = std::min<int64_t>(count, sms);
       const size_t smem = chunk_smem_bytes(width, 0, 3, false);
-      cudaFuncSetAttribute(k_chunk_dense<true, 1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem));
+      raise_smem(k_chunk_dense<true, 1024>, smem);
       k_chunk_dense<true, 1024><<<static_cast<unsigned>(blocks), 1024, smem, s>>>(p, counter, gacc);
     } else {
       // as many blocks per SM as the value arrays allow; the block shrinks with them (three
@@ -552,7 +551,7 @@ void launch_chunk_bitmap(const ChunkSet& cs, const int32_t* list, int64_t count,
       const int threads = fit >= 3 ? 256 : (fit == 2 ? 512 : 1024);
       auto kern = threads == 256 ? k_chunk_dense<false, 256>
                                  : (threads == 512 ? k_chunk_dense<false, 512> : k_chunk_dense<false, 1024>);
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      raise_smem(kern, smem);
       int per_sm = 1;
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
       if (per_sm < 1) per_sm = 1;

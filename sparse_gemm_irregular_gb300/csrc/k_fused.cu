@@ -86,11 +86,11 @@ void launch_bsplit(const spgemm_csr& B, const int32_t* colcnt, const int32_t* bh
   const unsigned grid = static_cast<unsigned>(ceil_div(B.rows, kBsWarps));
   note_launch();
   if (bs_val) {
-    cudaFuncSetAttribute(k_bsplit<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    raise_smem(k_bsplit<true>, smem);
     k_bsplit<true><<<grid, 32 * kBsWarps, smem, s>>>(B.row_ptr, B.col_idx, B.vals, B.rows, colcnt, bh, shift, v, bo,
                                                      bs_col, bs_val, err);
   } else {
-    cudaFuncSetAttribute(k_bsplit<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    raise_smem(k_bsplit<false>, smem);
     k_bsplit<false><<<grid, 32 * kBsWarps, smem, s>>>(B.row_ptr, B.col_idx, nullptr, B.rows, colcnt, bh, shift, v,
                                                       bo, bs_col, nullptr, err);
   }
@@ -449,7 +449,7 @@ template <bool WARP, int MODE>
 static void fck_launch(const CkParams& p, const FusedSrc& f, int tpr, cudaStream_t s) {
   const size_t smem = chunk_smem_bytes(p.width, p.slots, MODE, WARP);
   auto kern = k_fchunk<WARP, MODE>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  raise_smem(kern, smem);
   const int64_t blocks = WARP ? ceil_div(p.count, kCkWarpsPerBlock) : p.count;
   const int threads = WARP ? 32 * kCkWarpsPerBlock : tpr;
   note_launch();
@@ -483,7 +483,7 @@ void launch_fused_chunks(const FusedSrc& f, const ChunkSet& cs, const int32_t* l
     const int fit = static_cast<int>(smem_sm / (smem + 1024));
     const int threads = fit >= 3 ? 256 : (fit == 2 ? 512 : 1024);
     auto kern = threads == 256 ? k_fchunk_dense<256> : (threads == 512 ? k_fchunk_dense<512> : k_fchunk_dense<1024>);
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    raise_smem(kern, smem);
     int per_sm = 1;
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
     if (per_sm < 1) per_sm = 1;

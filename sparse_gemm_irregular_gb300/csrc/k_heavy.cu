@@ -638,12 +638,12 @@ void launch_histogram(const int64_t* row_ptr, const int2* part, int64_t total, c
   const int64_t ntiles = ceil_div(total, kMsTile);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(ntiles, static_cast<int64_t>(sms) * 4));
   if (match) {
-    cudaFuncSetAttribute(k_histogram<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    raise_smem(k_histogram<true>, smem);
     note_launch();
     k_histogram<true><<<grid, kMsThreads, smem, s>>>(row_ptr, part, total, ntiles, col, shift, nchunks, group_rows,
                                                      counts, err);
   } else {
-    cudaFuncSetAttribute(k_histogram<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    raise_smem(k_histogram<false>, smem);
     note_launch();
     k_histogram<false><<<grid, kMsThreads, smem, s>>>(row_ptr, part, total, ntiles, col, shift, nchunks, group_rows,
                                                       counts, err);
@@ -733,7 +733,7 @@ static void ms_launch(const int64_t* row_ptr, const int2* part, int64_t total, c
   const size_t smem = bins * 8 + (group_rows + 1) * 8 + bins * 4;
   const int64_t ntiles = ceil_div(total, kMsTile);
   auto kern = k_multisplit<VALS, MATCH>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  raise_smem(kern, smem);
   int per_sm = 0;
   cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kMsThreads, smem);
   if (per_sm < 1) per_sm = 1;

@@ -223,7 +223,7 @@ bool launch_multisplit_tma(const int64_t* row_ptr, const int2* part, int64_t tot
     return false;
   const int64_t ntiles = ceil_div(total, static_cast<int64_t>(kT));
   auto kern = with_vals ? k_multisplit_tma<true> : k_multisplit_tma<false>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  raise_smem(kern, smem);
   int per_sm = 0;
   cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kMsThreads, smem);
   if (per_sm < 1) per_sm = 1;
